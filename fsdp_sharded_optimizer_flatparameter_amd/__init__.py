@@ -19,7 +19,13 @@ from .api import (  # noqa: F401
     zs_copy_out,
     zs_copy_out_dim0,
     zs_dim0_layout,
+    zs_embed_backward,
+    zs_embed_forward,
+    zs_embed_workspace_bytes,
     zs_flat_layout,
+    zs_layer_norm_backward,
+    zs_layer_norm_forward,
+    zs_layer_norm_workspace_bytes,
     zs_pack_shard,
     zs_pack_shard_dim0,
     zs_reduce_grads,

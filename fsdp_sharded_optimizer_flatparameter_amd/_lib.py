@@ -13,6 +13,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libzs.so")
 ZS_OK = 0
 ZS_F32 = 0
 ZS_BF16 = 1
+ZS_I32 = 2
+ZS_I64 = 3
 ZS_MAX_WORLD = 256
 ZS_NOALLOC_MAX_N = 1 << 28
 STATUS = {
@@ -71,6 +73,21 @@ SIGNATURES = {
                                        C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "zs_copy_out_dim0": (C.c_int32, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_int32,
                                      C.c_int64, C.c_int64, C.c_void_p]),
+    "zs_embed_forward": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                     C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int64,
+                                     C.c_float, C.c_void_p, C.c_int32, C.c_int64, C.c_void_p]),
+    "zs_embed_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64]),
+    "zs_embed_backward": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int32, C.c_int64,
+                                      C.c_int64, C.c_int64, C.c_int64, C.c_float, C.c_void_p, C.c_int32,
+                                      C.c_int64, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "zs_layer_norm_forward": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_void_p, C.c_int32,
+                                          C.c_int64, C.c_int64, C.c_double, C.c_void_p, C.c_int64, C.c_void_p,
+                                          C.c_void_p, C.c_void_p]),
+    "zs_layer_norm_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "zs_layer_norm_backward": (C.c_int32, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int32, C.c_void_p,
+                                           C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
+                                           C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p,
+                                           C.c_size_t, C.c_void_p]),
     "zs_status_string": (C.c_char_p, [C.c_int32]),
     "zs_version": (C.c_int32, []),
 }

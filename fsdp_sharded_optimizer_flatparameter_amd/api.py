@@ -387,5 +387,190 @@ def zs_clip_coefficient(partials, max_norm, coef_out, norm_out=None, stream=None
         _stream(stream, partials.device)))
 
 
+# ---------------------------------------------------------------- embedding, layer norm
+
+_INDEX_TYPES = {torch.int32: L.ZS_I32, torch.int64: L.ZS_I64}
+
+
+def _rows2d(t, name, dev):
+    """(rows, dim, row stride) of a tensor whose last dimension is a row: two
+    dimensions with any stride between rows, or contiguous with any number."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    shape = t.shape
+    if len(shape) == 2:
+        rows, dim = shape
+        ld, unit = t.stride()
+        if (unit == 1 or dim <= 1) and (ld >= dim or rows <= 1):
+            return rows, dim, ld if ld >= dim else dim
+        raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
+    if not shape or not t.is_contiguous():
+        raise ValueError(f"{name} must have two dimensions or be contiguous")
+    dim = shape[-1]
+    return (t.numel() // dim if dim else 0), dim, dim
+
+
+def _ids(t, name, n, dev):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if t.dtype not in _INDEX_TYPES:
+        raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return _INDEX_TYPES[t.dtype]
+
+
+def _vector(t, name, n, dev, dtype=None):
+    """Pointer of an optional contiguous vector of n elements on device `dev`."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+def _device_index(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.get_device()
+
+
+def _call(name, dev, stream, *args):
+    """One library call with device `dev` current: the null stream is the current device's."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    fn = getattr(_lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, int(stream))
+    if st != 0:
+        L.check(name, st)
+
+
+def zs_embed_forward(table, tokens, out, *, scale=1.0, pos_table=None, positions=None, stream=None):
+    """out[i] = scale * table[tokens[i]] (+ pos_table[positions[i]]); ids outside of a table
+    select zeros. `out` has a row per token."""
+    dev = _device_index(table, "table")
+    vocab, dim, table_ld = _rows2d(table, "table", dev)
+    n, out_dim, out_ld = _rows2d(out, "out", dev)
+    itype = _ids(tokens, "tokens", n if out_dim else None, dev)
+    if out_dim != dim:
+        raise ValueError(f"out has rows of {out_dim} elements, the table's have {dim}")
+    pos_ptr = positions_ptr = None
+    pos_rows = pos_ld = 0
+    if (pos_table is None) != (positions is None):
+        raise ValueError("pos_table and positions come together")
+    if pos_table is not None:
+        pos_rows, pos_dim, pos_ld = _rows2d(pos_table, "pos_table", dev)
+        if pos_dim != dim or pos_table.dtype != table.dtype:
+            raise ValueError("pos_table must have the table's width and dtype")
+        if _ids(positions, "positions", n, dev) != itype:
+            raise ValueError("positions must have the tokens' dtype")
+        pos_ptr, positions_ptr = pos_table.data_ptr(), positions.data_ptr()
+    _call("zs_embed_forward", dev, stream, table.data_ptr(), _DTYPES[table.dtype], vocab, dim, table_ld,
+          pos_ptr, pos_rows, pos_ld, tokens.data_ptr(), positions_ptr, itype, n, scale, out.data_ptr(),
+          _DTYPES[out.dtype], out_ld)
+
+
+def zs_embed_workspace_bytes(n: int, vocab: int, dim: int) -> int:
+    return int(_lib().zs_embed_workspace_bytes(int(n), int(vocab), int(dim)))
+
+
+def _workspace(ws, dev):
+    if ws is None:
+        return None, 0
+    _dev(ws, "workspace")
+    if ws.get_device() != dev:
+        raise ValueError("workspace is on another device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=False, workspace, stream=None):
+    """grad[v] = (0 if first else grad[v]) + scale * sum of dout[i] over tokens[i] == v."""
+    dev = _device_index(grad, "grad")
+    vocab, dim, grad_ld = _rows2d(grad, "grad", dev)
+    n, dout_dim, dout_ld = _rows2d(dout, "dout", dev)
+    itype = _ids(tokens, "tokens", n if dout_dim else None, dev)
+    if dout_dim != dim:
+        raise ValueError(f"dout has rows of {dout_dim} elements, grad's have {dim}")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("zs_embed_backward", dev, stream, dout.data_ptr(), _DTYPES[dout.dtype], dout_ld, tokens.data_ptr(),
+          itype, n, vocab, dim, padding_idx, scale, grad.data_ptr(), _DTYPES[grad.dtype], grad_ld,
+          1 if first else 0, ws, ws_bytes)
+
+
+def zs_layer_norm_forward(x, weight, bias, y, *, eps=1e-5, mean=None, rstd=None, stream=None):
+    """y = (x - mean) * rstd * weight + bias over the last dimension; weight and bias may be
+    None; mean and rstd (fp32, one per row) are written where given."""
+    dev = _device_index(x, "x")
+    rows, dim, x_ld = _rows2d(x, "x", dev)
+    y_rows, y_dim, y_ld = _rows2d(y, "y", dev)
+    if y_rows != rows or y_dim != dim or y.dtype != x.dtype:
+        raise ValueError("y must have x's rows, width and dtype")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    w = _vector(weight, "weight", dim, dev)
+    b = _vector(bias, "bias", dim, dev)
+    wdtype = (weight if weight is not None else bias if bias is not None else x).dtype
+    if wdtype not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {wdtype}")
+    _call("zs_layer_norm_forward", dev, stream, x.data_ptr(), _DTYPES[x.dtype], x_ld, w, b, _DTYPES[wdtype],
+          rows, dim, eps, y.data_ptr(), y_ld, _vector(mean, "mean", rows, dev, torch.float32),
+          _vector(rstd, "rstd", rows, dev, torch.float32))
+
+
+def zs_layer_norm_workspace_bytes(rows: int, dim: int) -> int:
+    return int(_lib().zs_layer_norm_workspace_bytes(int(rows), int(dim)))
+
+
+def zs_layer_norm_backward(dy, x, weight, mean, rstd, dx, *, dweight=None, dbias=None, first=False,
+                           workspace=None, stream=None):
+    """dx, and (0 if first else the old value) + the sums over rows in dweight and dbias
+    where given, which then need a workspace."""
+    dev = _device_index(x, "x")
+    rows, dim, x_ld = _rows2d(x, "x", dev)
+    dy_rows, dy_dim, dy_ld = _rows2d(dy, "dy", dev)
+    dx_rows, dx_dim, dx_ld = _rows2d(dx, "dx", dev)
+    if dy_rows != rows or dy_dim != dim or dx_rows != rows or dx_dim != dim:
+        raise ValueError("dy and dx must have x's rows and width")
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise ValueError("dy and dx must have x's dtype")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are those of the forward pass")
+    w = _vector(weight, "weight", dim, dev)
+    wdtype = x.dtype if weight is None else weight.dtype
+    if wdtype not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {wdtype}")
+    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+        raise ValueError("dweight and dbias must have one dtype")
+    dw = _vector(dweight, "dweight", dim, dev)
+    db = _vector(dbias, "dbias", dim, dev)
+    gdtype = (dweight if dweight is not None else dbias if dbias is not None else x).dtype
+    if gdtype not in _DTYPES:
+        raise ValueError(f"unsupported gradient dtype {gdtype}")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("zs_layer_norm_backward", dev, stream, dy.data_ptr(), dy_ld, x.data_ptr(), x_ld, _DTYPES[x.dtype], w,
+          _DTYPES[wdtype], _vector(mean, "mean", rows, dev, torch.float32),
+          _vector(rstd, "rstd", rows, dev, torch.float32), rows, dim, dx.data_ptr(), dx_ld, dw, db,
+          _DTYPES[gdtype], 1 if first else 0, ws, ws_bytes)
+
+
 def zs_version() -> int:
     return int(_lib().zs_version())

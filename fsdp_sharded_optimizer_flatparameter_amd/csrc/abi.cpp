@@ -73,11 +73,43 @@ bool scale_overlaps(const float* scale, const void* a, const void* b, const void
                    overlaps(scale, 4, c, n * 4) || (bf16_out && overlaps(scale, 4, bf16_out, n * 2)));
 }
 
+inline bool float_type(int32_t dtype) { return dtype == ZS_F32 || dtype == ZS_BF16; }
+inline bool index_type_ok(int32_t t) { return t == ZS_I32 || t == ZS_I64; }
+inline int64_t index_size(int32_t t) { return t == ZS_I32 ? 4 : 8; }
+
+// Sizes of the embedding and layer norm calls: counts stay in 31 bits (sorted
+// positions and keys are 32-bit), widths in 27 (column offsets are 32-bit in
+// places).
+constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxDim = (int64_t(1) << 27) - 1;
+inline bool count_ok(int64_t n) { return n >= 0 && n <= kMaxCount; }
+inline bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
+
+// A row stride holds a row, and the last row's end (in bytes) stays in 63 bits.
+inline bool stride_ok(int64_t rows, int64_t dim, int64_t ld) {
+  return ld >= dim && ld <= (INT64_MAX / 8 - dim) / (rows > 0 ? rows : 1);
+}
+
+// Device memory of one argument, for the overlap checks. Rows that leave gaps
+// between them count with their gaps.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+Span rows_span(const void* p, int64_t rows, int64_t dim, int64_t ld, int32_t dtype) {
+  return Span{p, p && rows > 0 && dim > 0 ? ((rows - 1) * ld + dim) * elem_size(dtype) : 0};
+}
+bool any_overlap(const Span& a, const Span* b, int n) {
+  for (int i = 0; i < n; ++i)
+    if (overlaps(a.p, a.bytes, b[i].p, b[i].bytes)) return true;
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
 
-int32_t zs_version(void) { return 100; /* 0.1.0 */ }
+int32_t zs_version(void) { return 200; /* 0.2.0 */ }
 
 const char* zs_status_string(zs_status s) {
   switch (s) {
@@ -441,6 +473,127 @@ zs_status zs_clip_coefficient(const double* partials, int32_t count, double max_
   if (!aligned(partials, 8) || !aligned(coef_out, 4) || (norm_out && !aligned(norm_out, 8)))
     return ZS_ERR_ALIGN;
   return launch([&] { return zs::launch_clip(partials, count, max_norm, coef_out, norm_out, stream); });
+}
+
+zs_status zs_embed_forward(const void* table, int32_t dtype, int64_t vocab, int64_t dim,
+                           int64_t table_ld, const void* pos_table, int64_t pos_rows, int64_t pos_ld,
+                           const void* tokens, const void* positions, int32_t index_type, int64_t n,
+                           float scale, void* out, int32_t out_dtype, int64_t out_ld,
+                           hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(out_dtype) || !index_type_ok(index_type)) return ZS_ERR_DTYPE;
+  if (!count_ok(n) || !count_ok(vocab) || !dim_ok(dim)) return ZS_ERR_SIZE;
+  if (!stride_ok(vocab, dim, table_ld) || !stride_ok(n, dim, out_ld)) return ZS_ERR_SIZE;
+  if (pos_table && (!count_ok(pos_rows) || !stride_ok(pos_rows, dim, pos_ld))) return ZS_ERR_SIZE;
+  if (!std::isfinite(scale)) return ZS_ERR_HPARAM;
+  if (n == 0 || dim == 0) return ZS_OK;
+  if (!out || !tokens || (vocab > 0 && !table) || (pos_table && !positions)) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), is = (uintptr_t)index_size(index_type);
+  if (!aligned(table, es) || !aligned(pos_table, es) || !aligned(out, (uintptr_t)elem_size(out_dtype)) ||
+      !aligned(tokens, is) || (pos_table && !aligned(positions, is)))
+    return ZS_ERR_ALIGN;
+  const Span in[4] = {rows_span(table, vocab, dim, table_ld, dtype),
+                      rows_span(pos_table, pos_rows, dim, pos_ld, dtype),
+                      {tokens, n * (int64_t)is},
+                      {positions, pos_table ? n * (int64_t)is : 0}};
+  if (any_overlap(rows_span(out, n, dim, out_ld, out_dtype), in, 4)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_embed_forward(table, dtype, vocab, dim, table_ld, pos_table, pos_rows, pos_ld, tokens,
+                                    positions, index_type, n, scale, out, out_dtype, out_ld, stream);
+  });
+}
+
+size_t zs_embed_workspace_bytes(int64_t n, int64_t vocab, int64_t dim) {
+  if (!count_ok(n) || !count_ok(vocab) || !dim_ok(dim)) return 0;
+  return (size_t)zs::embed_plan(n, vocab, dim).bytes;
+}
+
+zs_status zs_embed_backward(const void* dout, int32_t dtype, int64_t dout_ld, const void* tokens,
+                            int32_t index_type, int64_t n, int64_t vocab, int64_t dim,
+                            int64_t padding_idx, float scale, void* grad, int32_t grad_dtype,
+                            int64_t grad_ld, int32_t first, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(grad_dtype) || !index_type_ok(index_type)) return ZS_ERR_DTYPE;
+  if (!count_ok(n) || !count_ok(vocab) || !dim_ok(dim)) return ZS_ERR_SIZE;
+  if (!stride_ok(n, dim, dout_ld) || !stride_ok(vocab, dim, grad_ld)) return ZS_ERR_SIZE;
+  if (!std::isfinite(scale)) return ZS_ERR_HPARAM;
+  if (vocab == 0 || dim == 0 || (n == 0 && !first)) return ZS_OK;
+  if (!grad || (n > 0 && (!dout || !tokens))) return ZS_ERR_NULL;
+  if (!aligned(grad, (uintptr_t)elem_size(grad_dtype)) ||
+      (n > 0 && (!aligned(dout, (uintptr_t)elem_size(dtype)) || !aligned(tokens, (uintptr_t)index_size(index_type)))))
+    return ZS_ERR_ALIGN;
+  if (!workspace || workspace_bytes < zs_embed_workspace_bytes(n, vocab, dim)) return ZS_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
+  const Span g = rows_span(grad, vocab, dim, grad_ld, grad_dtype), ws = {workspace, (int64_t)workspace_bytes};
+  const Span in[2] = {rows_span(dout, n, dim, dout_ld, dtype), {tokens, n * index_size(index_type)}};
+  if (any_overlap(g, in, 2) || any_overlap(ws, in, 2) || any_overlap(g, &ws, 1)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_embed_backward(dout, dtype, dout_ld, tokens, index_type, n, vocab, dim, padding_idx, scale, grad,
+                                     grad_dtype, grad_ld, first != 0, workspace, stream);
+  });
+}
+
+zs_status zs_layer_norm_forward(const void* x, int32_t dtype, int64_t x_ld, const void* weight,
+                                const void* bias, int32_t wdtype, int64_t rows, int64_t dim,
+                                double eps, void* y, int64_t y_ld, float* mean, float* rstd,
+                                hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(wdtype)) return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim) || (rows > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, x_ld) || !stride_ok(rows, dim, y_ld)) return ZS_ERR_SIZE;
+  if (!std::isfinite(eps) || eps < 0) return ZS_ERR_HPARAM;
+  if (rows == 0) return ZS_OK;
+  if (!x || !y) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), wsz = (uintptr_t)elem_size(wdtype);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, wsz) || !aligned(bias, wsz) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return ZS_ERR_ALIGN;
+  const Span in[3] = {rows_span(x, rows, dim, x_ld, dtype), rows_span(weight, 1, dim, dim, wdtype),
+                      rows_span(bias, 1, dim, dim, wdtype)};
+  const Span out[3] = {rows_span(y, rows, dim, y_ld, dtype), {mean, mean ? rows * 4 : 0}, {rstd, rstd ? rows * 4 : 0}};
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(out[i], in, 3) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_layer_norm_forward(x, dtype, x_ld, weight, bias, wdtype, rows, dim, (float)eps, y, y_ld, mean,
+                                         rstd, stream);
+  });
+}
+
+size_t zs_layer_norm_workspace_bytes(int64_t rows, int64_t dim) {
+  if (!count_ok(rows) || !dim_ok(dim)) return 0;
+  const zs::LnPlan p = zs::ln_plan(rows, dim);
+  return (size_t)(2 * p.parts * p.pitch) * sizeof(float);
+}
+
+zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
+                                 int32_t dtype, const void* weight, int32_t wdtype, const float* mean,
+                                 const float* rstd, int64_t rows, int64_t dim, void* dx, int64_t dx_ld,
+                                 void* dweight, void* dbias, int32_t grad_dtype, int32_t first,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(wdtype) || !float_type(grad_dtype)) return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim) || (rows > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, dy_ld) || !stride_ok(rows, dim, x_ld) || !stride_ok(rows, dim, dx_ld)) return ZS_ERR_SIZE;
+  const bool grads = dweight || dbias;
+  if (dim == 0 || (rows == 0 && (!grads || !first))) return ZS_OK;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), gs = (uintptr_t)elem_size(grad_dtype);
+  if (rows > 0 && (!aligned(dy, es) || !aligned(x, es) || !aligned(dx, es) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+                   !aligned(weight, (uintptr_t)elem_size(wdtype))))
+    return ZS_ERR_ALIGN;
+  if (!aligned(dweight, gs) || !aligned(dbias, gs)) return ZS_ERR_ALIGN;
+  if (grads && rows > 0) {
+    if (!workspace || workspace_bytes < zs_layer_norm_workspace_bytes(rows, dim)) return ZS_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
+  }
+  const Span in[5] = {rows_span(dy, rows, dim, dy_ld, dtype), rows_span(x, rows, dim, x_ld, dtype),
+                      rows_span(weight, rows > 0, dim, dim, wdtype), {mean, rows * 4}, {rstd, rows * 4}};
+  const Span out[4] = {rows_span(dx, rows, dim, dx_ld, dtype), rows_span(dweight, 1, dim, dim, grad_dtype),
+                       rows_span(dbias, 1, dim, dim, grad_dtype),
+                       {workspace, grads && rows > 0 ? (int64_t)workspace_bytes : 0}};
+  for (int i = 0; i < 4; ++i)
+    if (any_overlap(out[i], in, 5) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_layer_norm_backward(dy, dy_ld, x, x_ld, dtype, weight, wdtype, mean, rstd, rows, dim, dx, dx_ld,
+                                          dweight, dbias, grad_dtype, first != 0, workspace, stream);
+  });
 }
 
 }  // extern "C"

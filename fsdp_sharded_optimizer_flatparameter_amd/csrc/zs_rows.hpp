@@ -1,0 +1,109 @@
+// Row access and wave sums shared by the embedding and layer norm kernels.
+//
+// A row is `dim` consecutive elements at any element-aligned address: odd
+// widths and row strides put rows off the 16-byte grid. gfx950 reads and
+// writes 16 bytes at any address in one instruction, so a lane's unit of work
+// is VEC consecutive elements wherever they start, and only the last, shorter
+// piece of a row goes element by element.
+#pragma once
+
+#include "zs_device.hpp"
+
+namespace zs {
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at a 2-byte aligned address
+
+// 16 bytes at any element-aligned address of global memory. (Not through ld_g:
+// a template parameter would drop the typedef's alignment.)
+__device__ __forceinline__ u32x4 ld16(const void* p) {
+  return *(const __attribute__((address_space(1))) u32x4_any*)p;
+}
+__device__ __forceinline__ void st16(u32x4 v, void* p) {
+  *(__attribute__((address_space(1))) u32x4_any*)p = v;
+}
+
+// VEC consecutive elements of a row as they lie in memory.
+template <typename T, int VEC>
+struct Piece {
+  static constexpr int N = VEC * (int)sizeof(T) / 16;
+  static_assert(N >= 1 && N * 16 == VEC * (int)sizeof(T), "whole 16-byte vectors");
+  u32x4 r[N];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = ld16(p + i * (16 / (int)sizeof(T)));
+  }
+  // the first n (below VEC) elements, zeros behind them
+  __device__ __forceinline__ void load_part(const T* p, int n) {
+    clear();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e < n) put(e, ld_g(p + e));
+  }
+  __device__ __forceinline__ void put(int e, float x) { r[e / 4][e % 4] = __float_as_uint(x); }
+  __device__ __forceinline__ void put(int e, uint16_t h) {
+    r[e / 8][(e % 8) / 2] |= (uint32_t)h << (16 * (e & 1));
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[e / 4][e % 4]);
+    const uint32_t w = r[e / 8][(e % 8) / 2];
+    return (e & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+
+// One value rounded to the row's type.
+template <typename T>
+__device__ __forceinline__ T round_to(float x) {
+  if constexpr (sizeof(T) == 4) return x;
+  else return (T)f32_to_bf16(x);
+}
+
+// VEC fp32 values stored as a row's elements, each rounded once.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_piece(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      st16(u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                 __float_as_uint(v[4 * i + 3])}, p + 4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 8; ++i)
+      st16(u32x4{pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                 pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])}, p + 8 * i);
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_part(T* p, const float* v, int n) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    if (e < n) st_g(round_to<T>(v[e]), p + e);
+}
+
+// Sum over the wave's lanes (G = 64) or over each aligned group of 16 (G = 16),
+// the same bits in every lane of the group: pairs of lanes that mirror each
+// other are added, so both hold the same sum after each step.
+template <int G>
+__device__ __forceinline__ float lane_sum(float x) {
+  static_assert(G == 16 || G == 64, "a row of 16 lanes or the wave");
+  auto dpp = [](float v, auto ctrl) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  x += dpp(x, std::integral_constant<int, 0xb1>{});   // lane ^ 1
+  x += dpp(x, std::integral_constant<int, 0x4e>{});   // lane ^ 2
+  x += dpp(x, std::integral_constant<int, 0x141>{});  // mirrored within 8
+  x += dpp(x, std::integral_constant<int, 0x140>{});  // mirrored within 16
+  if constexpr (G == 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return x;
+}
+
+}  // namespace zs

@@ -17,6 +17,9 @@
  *               buffer; zs_copy_out: a gathered flat buffer -> per-parameter
  *               tensors (the unshard copy-out).
  *   Fused       zs_sharded_step: steps 2-3 (and the cast) in one pass.
+ * And around the update, for the parameters that no matrix product stands for:
+ *   embedding   zs_embed_forward, zs_embed_backward
+ *   layer norm  zs_layer_norm_forward, zs_layer_norm_backward
  *
  * Pages (title, address) cited below:
  *   [L5]  "Lesson 5: ZeRO and FSDP", hpc.payai.win/train/lesson05.html
@@ -78,7 +81,7 @@ typedef int32_t zs_status;
 #define ZS_ERR_SIZE (-2)      /* negative or inconsistent element count           */
 #define ZS_ERR_WORLD (-3)     /* world size outside [1, ZS_MAX_WORLD]             */
 #define ZS_ERR_RANK (-4)      /* rank outside [0, world)                          */
-#define ZS_ERR_DTYPE (-5)     /* dtype code is not ZS_F32 or ZS_BF16              */
+#define ZS_ERR_DTYPE (-5)     /* dtype code is not ZS_F32 or ZS_BF16 (ids: ZS_I32, ZS_I64) */
 #define ZS_ERR_HPARAM (-6)    /* hyper-parameter not finite / out of range, step<1 */
 #define ZS_ERR_SHARD (-7)     /* shard_numel != ceil(total / world)               */
 #define ZS_ERR_WORKSPACE (-8) /* workspace missing or smaller than required       */
@@ -90,6 +93,10 @@ typedef int32_t zs_status;
 /* Element types of gradient contributions and parameters. */
 #define ZS_F32 0
 #define ZS_BF16 1
+
+/* Types of token and position ids. */
+#define ZS_I32 2
+#define ZS_I64 3
 
 /* Largest number of simulated ranks one reduce may combine. */
 #define ZS_MAX_WORLD 256
@@ -454,6 +461,134 @@ zs_status zs_pack_shard_dim0(const zs_dim0_desc* d_desc, int32_t nparams, int32_
 zs_status zs_copy_out_dim0(const uint16_t* gathered, int64_t gathered_numel,
                            const zs_dim0_desc* d_desc, int32_t nparams, int32_t world,
                            int64_t total, int64_t local_total, hipStream_t stream);
+
+/*
+ * Producers of parameter gradients. The entry points above take a parameter's
+ * gradient as it is; the ones below compute it for the parameters of a unit
+ * that no matrix product stands for -- embedding tables and the weights and
+ * biases of layer norms -- next to the forward pass that reads them. Like
+ * zs_accumulate_local they write a gradient where the update takes it from:
+ *   first != 0:  grad = the sum (a fresh contribution, every element written)
+ *   first == 0:  grad = grad + the sum (the accumulator of earlier
+ *                micro-batches; with a bf16 grad each call rounds once more)
+ * Rows are `dim` consecutive elements; `*_ld` is the distance between the
+ * starts of two rows in elements (>= dim), and what lies between two rows is
+ * neither read nor written. Any element-aligned pointer and any dim are
+ * accepted; rows on 16-byte boundaries are fastest. Arithmetic is fp32, each
+ * result rounded once to its type. The sums over rows run in an order that
+ * depends on the sizes (and on the tokens) alone: the same call gives the same
+ * bits. Sizes: n, rows and vocab below 2^31, dim below 2^27 (else ZS_ERR_SIZE).
+ */
+
+/*
+ * zs_embed_forward -- rows of an embedding table, scaled, optionally plus rows
+ * of a position table.
+ *   table[vocab, dim]     DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride table_ld
+ *   pos_table[pos_rows, dim]
+ *                         optional DEVICE (NULL = none), `dtype`, row stride pos_ld
+ *   tokens[n], positions[n]
+ *                         DEVICE ids, `index_type` ZS_I32 or ZS_I64; positions
+ *                         is read only with a pos_table
+ *   out[n, dim]           DEVICE, `out_dtype`, row stride out_ld:
+ *                         out[i] = scale * table[tokens[i]] (+ pos_table[positions[i]])
+ * An id outside of its table (below 0, or vocab / pos_rows and above: -100 or
+ * the like for ignored places) selects a row of zeros; nothing outside the
+ * tables is read. scale must be finite.
+ * out may not overlap the tables or the ids. Errors: ZS_ERR_NULL, ZS_ERR_SIZE
+ * (negative or too large sizes, a row stride below dim), ZS_ERR_DTYPE,
+ * ZS_ERR_HPARAM, ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_embed_forward(const void* table, int32_t dtype, int64_t vocab, int64_t dim,
+                           int64_t table_ld, const void* pos_table, int64_t pos_rows, int64_t pos_ld,
+                           const void* tokens, const void* positions, int32_t index_type, int64_t n,
+                           float scale, void* out, int32_t out_dtype, int64_t out_ld,
+                           hipStream_t stream);
+
+/* Bytes of workspace zs_embed_backward needs for n tokens of a [vocab, dim]
+ * table (0 for sizes it refuses). The contents need no initialisation. */
+size_t zs_embed_workspace_bytes(int64_t n, int64_t vocab, int64_t dim);
+
+/*
+ * zs_embed_backward -- gradient of an embedding table.
+ *   dout[n, dim]       DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride dout_ld
+ *   tokens[n]          DEVICE ids, `index_type` ZS_I32 or ZS_I64; ids outside of
+ *                      [0, vocab) and the id `padding_idx` (any id outside of
+ *                      the table, such as -1, for none) contribute nothing
+ *   grad[vocab, dim]   DEVICE, `grad_dtype`, row stride grad_ld:
+ *                      grad[v] = (first ? 0 : grad[v]) + scale * sum of dout[i]
+ *                      over the i with tokens[i] == v. With first != 0 every
+ *                      row is written (zeros where no token selects it), with
+ *                      first == 0 only the rows that tokens select.
+ *   workspace          DEVICE scratch of at least zs_embed_workspace_bytes(n,
+ *                      vocab, dim) bytes on a 16-byte boundary; calls that may
+ *                      run at the same time, and captured graphs that may be
+ *                      replayed at the same time, need one each
+ * For a position table, pass the positions as tokens. scale must be finite.
+ * A token's rows are added in fp32 in the order of their positions, in pieces
+ * of equal length, and the pieces in order.
+ * No two of grad, dout, tokens and workspace may share bytes. Errors:
+ * ZS_ERR_NULL, ZS_ERR_SIZE, ZS_ERR_DTYPE, ZS_ERR_HPARAM, ZS_ERR_WORKSPACE,
+ * ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_embed_backward(const void* dout, int32_t dtype, int64_t dout_ld, const void* tokens,
+                            int32_t index_type, int64_t n, int64_t vocab, int64_t dim,
+                            int64_t padding_idx, float scale, void* grad, int32_t grad_dtype,
+                            int64_t grad_ld, int32_t first, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/*
+ * zs_layer_norm_forward -- layer norm over the last dimension.
+ *   x[rows, dim]       DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride x_ld
+ *   weight[dim], bias[dim]
+ *                      DEVICE, `wdtype` (ZS_F32 or ZS_BF16); either may be NULL
+ *                      (ones, zeros)
+ *   eps                finite, >= 0
+ *   y[rows, dim]       DEVICE, `dtype`, row stride y_ld:
+ *                      y = (x - mean) * rstd * weight + bias with
+ *                      mean = sum(x) / dim, rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps)
+ *   mean[rows], rstd[rows]
+ *                      optional DEVICE fp32 outputs (NULL = skip; the backward
+ *                      pass needs both)
+ * y may not overlap x, weight or bias, nor mean and rstd anything. Errors:
+ * ZS_ERR_NULL, ZS_ERR_SIZE (dim < 1 with rows > 0 among them), ZS_ERR_DTYPE,
+ * ZS_ERR_HPARAM, ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_layer_norm_forward(const void* x, int32_t dtype, int64_t x_ld, const void* weight,
+                                const void* bias, int32_t wdtype, int64_t rows, int64_t dim,
+                                double eps, void* y, int64_t y_ld, float* mean, float* rstd,
+                                hipStream_t stream);
+
+/* Bytes of workspace zs_layer_norm_backward needs for the weight's and bias's
+ * gradient (0 for sizes it refuses). The contents need no initialisation. */
+size_t zs_layer_norm_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * zs_layer_norm_backward -- gradients of layer norm.
+ *   dy[rows, dim], x[rows, dim]
+ *                      DEVICE, `dtype`, row strides dy_ld, x_ld
+ *   weight[dim]        DEVICE, `wdtype`, or NULL (ones)
+ *   mean[rows], rstd[rows]
+ *                      DEVICE fp32, as zs_layer_norm_forward gives them
+ *   dx[rows, dim]      DEVICE, `dtype`, row stride dx_ld: with xh = (x - mean) * rstd,
+ *                      dx = rstd * (dy * weight - mean(dy * weight) - xh * mean(dy * weight * xh))
+ *   dweight[dim], dbias[dim]
+ *                      DEVICE, `grad_dtype`; either may be NULL (skipped):
+ *                      dweight = (first ? 0 : dweight) + sum over rows of dy * xh,
+ *                      dbias = (first ? 0 : dbias) + sum over rows of dy
+ *   workspace          DEVICE scratch of at least zs_layer_norm_workspace_bytes(rows,
+ *                      dim) bytes on a 16-byte boundary, required unless dweight and
+ *                      dbias are both NULL; calls and graph replays that may run at
+ *                      the same time need one each
+ * rows == 0 with first != 0 sets dweight and dbias to zero. No output may
+ * share bytes with an input, the workspace or another output. Errors:
+ * ZS_ERR_NULL, ZS_ERR_SIZE, ZS_ERR_DTYPE, ZS_ERR_WORKSPACE, ZS_ERR_ALIGN,
+ * ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, int64_t x_ld,
+                                 int32_t dtype, const void* weight, int32_t wdtype, const float* mean,
+                                 const float* rstd, int64_t rows, int64_t dim, void* dx, int64_t dx_ld,
+                                 void* dweight, void* dbias, int32_t grad_dtype, int32_t first,
+                                 void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, NUL-terminated name of a status code ("ZS_OK", "ZS_ERR_NULL", ...). */
 const char* zs_status_string(zs_status status);
