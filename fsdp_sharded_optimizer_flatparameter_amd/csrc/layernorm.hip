@@ -27,30 +27,30 @@ __device__ __forceinline__ int64_t col_of(int j, int l) {
   return (int64_t)(j * LPR + l) * VEC;
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void load_cols(Piece<T, VEC>& p, const T* row, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) p.load(row + c);
-  else if (c < dim) p.load_part(row + c, (int)(dim - c));
+  if (c + VEC <= dim) {
+    if constexpr (NT) p.load_nt(row + c);
+    else p.load(row + c);
+  } else if (c < dim) p.load_part(row + c, (int)(dim - c));
   else p.clear();
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_cols(T* row, const float* v, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) store_piece<T, VEC>(row + c, v);
+  if (c + VEC <= dim) store_piece<T, VEC, NT>(row + c, v);
   else if (c < dim) store_part<T, VEC>(row + c, v, (int)(dim - c));
 }
 
 // Weight or bias values of a piece; `missing` where the caller passes none.
 template <typename W, int VEC>
-__device__ __forceinline__ void load_affine(float* f, const W* p, float missing, int64_t c, int64_t dim) {
-  if (!p) {
+__device__ __forceinline__ void load_affine(Piece<W, VEC>& r, const W* p, float missing, int64_t c, int64_t dim) {
+  if (p) {
+    load_cols<W, VEC>(r, p, c, dim);
+  } else {
+    r.clear();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = missing;
-    return;
+    for (int e = 0; e < VEC; ++e) r.put(e, round_to<W>(missing));
   }
-  Piece<W, VEC> r;
-  load_cols<W, VEC>(r, p, c, dim);
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) f[e] = r.get(e);
 }
 
 // Statistics of one part of a row: count, mean and the sum of squared
@@ -60,7 +60,7 @@ struct Part {
   float n, mean, m2;
 };
 
-template <typename T, typename W, int LPR, int NV, int VEC>
+template <typename T, typename W, int LPR, int NV, int VEC, bool NT>
 __global__ __launch_bounds__(LPR > 256 ? LPR : 256)
 void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, const W* __restrict__ b,
               int64_t rows, int64_t dim, float eps, T* __restrict__ y, int64_t y_ld,
@@ -68,10 +68,19 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
   constexpr int BS = LPR > 256 ? LPR : 256;
   constexpr int RPB = BS / LPR;         // rows in flight per workgroup
   constexpr int NW = LPR / 64;          // waves per row (0 below a wave)
-  constexpr int G = LPR < 64 ? 16 : 64;
-  __shared__ Part parts[2][NW > 1 ? NW : 1];
+  constexpr int G = LPR < 64 ? LPR : 64;
+  __shared__ Part parts[2][BS / 64];
   const int l = threadIdx.x % LPR;
-  float wf[NV][VEC], bf[NV][VEC];
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  Piece<T, VEC> next[NV];  // the next row is on its way while this one is worked on
+  auto fetch = [&](int64_t r) {
+    if (r < rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_cols<T, VEC, NT>(next[j], x + r * x_ld, col_of<LPR, VEC>(j, l), dim);
+  };
+  fetch(row);
+  Piece<W, VEC> wf[NV], bf[NV];  // as they lie in memory: half the registers for bf16
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     load_affine<W, VEC>(wf[j], w, 1.0f, col_of<LPR, VEC>(j, l), dim);
@@ -86,44 +95,60 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
     cnt += (float)(left >= VEC ? VEC : (left > 0 ? left : 0));
   }
   cnt = lane_sum<G>(cnt);
+  const float inv_cnt = 1.0f / (cnt > 0.0f ? cnt : 1.0f);
+  // every row group of the workgroup takes the same number of turns (barriers)
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step, row += step, turn ^= 1) {
     Piece<T, VEC> raw[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load_cols<T, VEC>(raw[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
+    for (int j = 0; j < NV; ++j) {
+      wf[j].stay_packed();
+      bf[j].stay_packed();
+      raw[j] = next[j];
+    }
+    fetch(row + step);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) s += raw[j].get(e);
-    float mean = lane_sum<G>(s) / (cnt > 0.0f ? cnt : 1.0f);
+    float mean = lane_sum<G>(s) * inv_cnt;
     float m2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int64_t left = dim - col_of<LPR, VEC>(j, l);
+      if (left >= VEC) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float d = raw[j].get(e) - mean;
-        m2 = e < left ? fmaf(d, d, m2) : m2;
+        for (int e = 0; e < VEC; ++e) {
+          const float d = raw[j].get(e) - mean;
+          m2 = fmaf(d, d, m2);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float d = raw[j].get(e) - mean;
+          m2 = e < left ? fmaf(d, d, m2) : m2;
+        }
       }
     }
     m2 = lane_sum<G>(m2);
     if constexpr (NW > 1) {
+      const int w0 = threadIdx.x / LPR * NW;  // the row's first wave
       if ((threadIdx.x & 63) == 0) parts[turn][threadIdx.x / 64] = Part{cnt, mean, m2};
       __syncthreads();  // the other turn's entries are read by nobody any more
       float total = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) total += parts[turn][i].n * parts[turn][i].mean;
+      for (int i = 0; i < NW; ++i) total += parts[turn][w0 + i].n * parts[turn][w0 + i].mean;
       mean = total * inv_dim;
       m2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
-        const Part p = parts[turn][i];
+        const Part p = parts[turn][w0 + i];
         const float d = p.mean - mean;
         m2 += fmaf(p.n * d, d, p.m2);
       }
     }
+    if (row >= rows) continue;
     const float rstd = 1.0f / sqrtf(m2 * inv_dim + eps);
     if (l == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -133,8 +158,8 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
     for (int j = 0; j < NV; ++j) {
       float v[VEC];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = fmaf((raw[j].get(e) - mean) * rstd, wf[j][e], bf[j][e]);
-      store_cols<T, VEC>(y + row * y_ld, v, col_of<LPR, VEC>(j, l), dim);
+      for (int e = 0; e < VEC; ++e) v[e] = fmaf((raw[j].get(e) - mean) * rstd, wf[j].get(e), bf[j].get(e));
+      store_cols<T, VEC, NT>(y + row * y_ld, v, col_of<LPR, VEC>(j, l), dim);
     }
   }
 }
@@ -154,6 +179,7 @@ __device__ __forceinline__ float block_sum(float x, float* lds) {
 }
 
 constexpr int kLongBS = 1024;
+constexpr int kMaxParts = 256;  // partial sums of the backward pass: a workgroup of 16 waves per CU
 
 // Rows longer than the registers of 1024 lanes hold: one workgroup walks over
 // the row three times (sum, squared distances, output); the second and third
@@ -196,12 +222,13 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
     }
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
       Piece<T, VEC> p;
-      float wf[VEC], bf[VEC], v[VEC];
+      Piece<W, VEC> wf, bf;
+      float v[VEC];
       load_cols<T, VEC>(p, xr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
       load_affine<W, VEC>(bf, b, 0.0f, c, dim);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = fmaf((p.get(e) - mean) * rstd, wf[e], bf[e]);
+      for (int e = 0; e < VEC; ++e) v[e] = fmaf((p.get(e) - mean) * rstd, wf.get(e), bf.get(e));
       store_cols<T, VEC>(y + row * y_ld, v, c, dim);
     }
   }
@@ -211,20 +238,38 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
 // dy xh and dy per column, which go to partials[2 g], partials[2 g + 1] (rows
 // of `pitch` fp32) for k_ln_grads to join. The columns' sums stay in registers
 // over all rows; the row groups of a workgroup join theirs in LDS in order.
-template <typename T, typename W, int LPR, int NV, int VEC>
-__global__ __launch_bounds__(LPR > 256 ? LPR : 256)
+template <typename T, typename W, int LPR, int NV, int VEC, int BS, bool NT>
+__global__ __launch_bounds__(BS)
 void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, int64_t x_ld,
               const W* __restrict__ w, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
               int64_t rows, int64_t dim, T* __restrict__ dx, int64_t dx_ld, float* __restrict__ partials,
               int64_t pitch) {
-  constexpr int BS = LPR > 256 ? LPR : 256;
   constexpr int RPB = BS / LPR;
   constexpr int NW = LPR / 64;
-  constexpr int G = LPR < 64 ? 16 : 64;
-  __shared__ float2 sums[2][NW > 1 ? NW : 1];
-  __shared__ float joined[RPB > 1 ? 2 * LPR * NV * VEC : 1];
+  constexpr int G = LPR < 64 ? LPR : 64;
+  constexpr int COLS = LPR * NV * VEC;
+  __shared__ float2 sums[2][BS / 64];
+  __shared__ __align__(16) float joined[RPB > 1 ? RPB * COLS : 1];
   const int l = threadIdx.x % LPR;
-  float wf[NV][VEC], dw[NV][VEC], db[NV][VEC];
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  Piece<T, VEC> nx[NV], ng[NV];  // the next row is on its way while this one is worked on
+  float mean = 0.0f, rstd = 0.0f, nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int64_t r) {
+    if (r < rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        load_cols<T, VEC, NT>(nx[j], x + r * x_ld, col_of<LPR, VEC>(j, l), dim);
+        load_cols<T, VEC, NT>(ng[j], dy + r * dy_ld, col_of<LPR, VEC>(j, l), dim);
+      }
+      nmean = mean_in[r];
+      nrstd = rstd_in[r];
+    }
+  };
+  constexpr bool AHEAD = NV == 1;  // two pieces a lane and a row ahead do not fit in 128 registers
+  if (AHEAD) fetch(row);
+  Piece<W, VEC> wf[NV];
+  float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     load_affine<W, VEC>(wf[j], w, 1.0f, col_of<LPR, VEC>(j, l), dim);
@@ -232,82 +277,91 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.0f;
   }
   const float inv_dim = 1.0f / (float)dim;
+  // every row group of the workgroup takes the same number of turns (barriers)
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < rows;
-       row += (int64_t)gridDim.x * RPB, turn ^= 1) {
+  for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step, row += step, turn ^= 1) {
+    if (!AHEAD) fetch(row);
     Piece<T, VEC> rx[NV], rg[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load_cols<T, VEC>(rx[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
-      load_cols<T, VEC>(rg[j], dy + row * dy_ld, col_of<LPR, VEC>(j, l), dim);
+      wf[j].stay_packed();
+      rx[j] = nx[j];
+      rg[j] = ng[j];
     }
-    const float mean = mean_in[row], rstd = rstd_in[row];
+    mean = nmean;
+    rstd = nrstd;
+    const bool live = row < rows;
+    if (AHEAD) fetch(row + step);
     float s1 = 0.0f, s2 = 0.0f;
+    if (live) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float g = rg[j].get(e), xh = (rx[j].get(e) - mean) * rstd, gw = g * wf[j][e];
-        s1 += gw;
-        s2 = fmaf(gw, xh, s2);
-        dw[j][e] = fmaf(g, xh, dw[j][e]);
-        db[j][e] += g;
-      }
-    s1 = lane_sum<G>(s1);
-    s2 = lane_sum<G>(s2);
+        for (int e = 0; e < VEC; ++e) {
+          const float g = rg[j].get(e), xh = (rx[j].get(e) - mean) * rstd, gw = g * wf[j].get(e);
+          s1 += gw;
+          s2 = fmaf(gw, xh, s2);
+          dw[j][e] = fmaf(g, xh, dw[j][e]);
+          db[j][e] += g;
+        }
+      s1 = lane_sum<G>(s1);
+      s2 = lane_sum<G>(s2);
+    }
     if constexpr (NW > 1) {
+      const int w0 = threadIdx.x / LPR * NW;  // the row's first wave
       if ((threadIdx.x & 63) == 0) sums[turn][threadIdx.x / 64] = float2{s1, s2};
       __syncthreads();  // the other turn's entries are read by nobody any more
       s1 = s2 = 0.0f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
-        s1 += sums[turn][i].x;
-        s2 += sums[turn][i].y;
+        s1 += sums[turn][w0 + i].x;
+        s2 += sums[turn][w0 + i].y;
       }
     }
-    const float a = s1 * inv_dim, c = s2 * inv_dim;
+    if (live) {
+      const float a = s1 * inv_dim, c = s2 * inv_dim;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (rx[j].get(e) - mean) * rstd;
+          v[e] = rstd * (fmaf(rg[j].get(e), wf[j].get(e), -a) - xh * c);
+        }
+        store_cols<T, VEC, NT>(dx + row * dx_ld, v, col_of<LPR, VEC>(j, l), dim);
+      }
+    }
+  }
+  if (!partials) return;  // uniform: an argument
+  float* pw = partials + 2 * (int64_t)blockIdx.x * pitch;
+  if constexpr (RPB > 1) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float* mine = joined + threadIdx.x / LPR * COLS;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+          *reinterpret_cast<f32x4*>(mine + (j * LPR + l) * VEC + e) =
+              k ? f32x4{db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]}
+                : f32x4{dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]};
+      __syncthreads();
+      for (int c = threadIdx.x; c < COLS && c < dim; c += BS) {
+        float t = joined[c];
+#pragma unroll
+        for (int g = 1; g < RPB; ++g) t += joined[g * COLS + c];
+        pw[k * pitch + c] = t;
+      }
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float v[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (rx[j].get(e) - mean) * rstd;
-        v[e] = rstd * (fmaf(rg[j].get(e), wf[j][e], -a) - xh * c);
+      const int64_t c = col_of<LPR, VEC>(j, l);
+      if (c < pitch) {  // pitch is a multiple of VEC
+        store_piece<float, VEC>(pw + c, dw[j]);
+        store_piece<float, VEC>(pw + pitch + c, db[j]);
       }
-      store_cols<T, VEC>(dx + row * dx_ld, v, col_of<LPR, VEC>(j, l), dim);
-    }
-  }
-  if (!partials) return;
-  if constexpr (RPB > 1) {
-    const int grp = threadIdx.x / LPR;
-    for (int turn2 = 0; turn2 < RPB; ++turn2) {
-      if (grp == turn2) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int at = (j * LPR + l) * VEC + e;
-            if (turn2 > 0) {
-              dw[j][e] = joined[at] + dw[j][e];
-              db[j][e] = joined[LPR * NV * VEC + at] + db[j][e];
-            }
-            if (turn2 + 1 < RPB) {
-              joined[at] = dw[j][e];
-              joined[LPR * NV * VEC + at] = db[j][e];
-            }
-          }
-      }
-      __syncthreads();
-    }
-    if (grp != RPB - 1) return;
-  }
-  float* pw = partials + 2 * (int64_t)blockIdx.x * pitch;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t c = col_of<LPR, VEC>(j, l);
-    if (c < pitch) {  // pitch is a multiple of VEC
-      store_piece<float, VEC>(pw + c, dw[j]);
-      store_piece<float, VEC>(pw + pitch + c, db[j]);
     }
   }
 }
@@ -326,13 +380,14 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
       Piece<T, VEC> px, pg;
-      float wf[VEC], t1 = 0.0f, t2 = 0.0f;
+      Piece<W, VEC> wf;
+      float t1 = 0.0f, t2 = 0.0f;
       load_cols<T, VEC>(px, xr, c, dim);
       load_cols<T, VEC>(pg, gr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float gw = pg.get(e) * wf[e];
+        const float gw = pg.get(e) * wf.get(e);
         t1 += gw;
         t2 = fmaf(gw, (px.get(e) - mean) * rstd, t2);
       }
@@ -342,12 +397,13 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
     const float a = block_sum<kLongBS>(s1, lds) * inv_dim, k = block_sum<kLongBS>(s2, lds) * inv_dim;
     for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
       Piece<T, VEC> px, pg;
-      float wf[VEC], v[VEC];
+      Piece<W, VEC> wf;
+      float v[VEC];
       load_cols<T, VEC>(px, xr, c, dim);
       load_cols<T, VEC>(pg, gr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = rstd * (fmaf(pg.get(e), wf[e], -a) - (px.get(e) - mean) * rstd * k);
+      for (int e = 0; e < VEC; ++e) v[e] = rstd * (fmaf(pg.get(e), wf.get(e), -a) - (px.get(e) - mean) * rstd * k);
       store_cols<T, VEC>(dx + row * dx_ld, v, c, dim);
     }
   }
@@ -388,7 +444,7 @@ void k_ln_cols(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x,
 // waves of a workgroup take every kJoinWaves-th partial, and their sums are
 // added in wave order. The grouping depends on the sizes alone, so the result
 // has the same bits on every call.
-constexpr int kJoinWaves = 8;
+constexpr int kJoinWaves = 16;
 template <typename Gt>
 __global__ __launch_bounds__(kJoinWaves * 64)
 void k_ln_grads(const float* __restrict__ partials, int64_t pitch, int parts, int64_t dim, Gt* __restrict__ dw,
@@ -400,45 +456,77 @@ void k_ln_grads(const float* __restrict__ partials, int64_t pitch, int parts, in
   Gt* out = bias ? db : dw;
   if (!out) return;  // uniform across the workgroup
   const int64_t c = ((int64_t)blockIdx.x - (bias ? tiles : 0)) * 64 + lane;
-  float s = 0.0f;
-  if (c < dim)
-    for (int p = wave; p < parts; p += kJoinWaves) s += partials[(2 * (int64_t)p + bias) * pitch + c];
+  float s = 0.0f, old = 0.0f;
+  if (c < dim) {
+    if (wave == 0 && !first) {
+      if constexpr (sizeof(Gt) == 4) old = out[c];
+      else old = bf16_to_f32(out[c]);
+    }
+    const float* p = partials + (bias ? pitch : 0) + c;
+    constexpr int U = kMaxParts / kJoinWaves;
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = u * kJoinWaves + wave;
+      v[u] = k < parts ? p[2 * (int64_t)k * pitch] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += v[u];
+  }
   lds[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || c >= dim) return;
 #pragma unroll
   for (int i = 1; i < kJoinWaves; ++i) s += lds[i][lane];
-  if (!first) {
-    if constexpr (sizeof(Gt) == 4) s += out[c];
-    else s += bf16_to_f32(out[c]);
-  }
-  out[c] = round_to<Gt>(s);
+  out[c] = round_to<Gt>(first ? s : s + old);
 }
 
-// Rows of VEC-element pieces a shape holds.
-struct Shape {
-  int lpr, nv;
-};
+// Rows that are read and written by a call of more than this many bytes bypass
+// the caches: past the memory-side cache nothing of them is left for the next
+// kernel, and the plain accesses were slower (16384 rows of 8192 bf16, 537 MB:
+// 98.9 against 94.4 us; 8192 rows of 4096, 134 MB: 27.9 against 25.3), below
+// it faster (8192 rows of 768 fp32, 50 MB: 9.0 against 10.1 us).
+constexpr int64_t kStreamBytes = 100000000;
+// Workgroups (of 256 lanes) of the forward pass, 4 per CU, each walking over
+// its rows: 94 us for 16384 rows of 8192 bf16, against 98 with 768 and 100 or
+// more with 1280; 2048 were 1-2% faster there, but 14% slower for 8192 rows of
+// 768 fp32.
+constexpr int64_t kFwdSlots = 1024;
 constexpr int kVecBf16 = 8, kVecF32 = 4;
 
 template <typename T, typename W, int VEC>
 void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int64_t dim, float eps, T* y,
              int64_t y_ld, float* mean, float* rstd, hipStream_t s) {
   const int64_t nvec = (dim + VEC - 1) / VEC;
+  const bool nt = 2 * rows * dim * (int64_t)sizeof(T) > kStreamBytes;
   auto go = [&](auto lpr, auto nv) {
     constexpr int LPR = decltype(lpr)::value, NV = decltype(nv)::value, BS = LPR > 256 ? LPR : 256;
     const int64_t need = (rows + BS / LPR - 1) / (BS / LPR);
-    const int64_t grid = need < 2048 ? need : 2048;
-    hipLaunchKernelGGL((k_ln_fwd<T, W, LPR, NV, VEC>), dim3((unsigned)grid), dim3(BS), 0, s, x, x_ld, w, b, rows,
-                       dim, eps, y, y_ld, mean, rstd);
+    const int64_t slots = kFwdSlots * 256 / BS, grid = need < slots ? need : slots;
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(BS), 0, s, x, x_ld, w, b, rows, dim, eps, y, y_ld, mean,
+                         rstd);
+    };
+    if (nt) launch(k_ln_fwd<T, W, LPR, NV, VEC, true>);
+    else launch(k_ln_fwd<T, W, LPR, NV, VEC, false>);
   };
   using std::integral_constant;
+  // By width alone, so that a row gives the same bits whatever the number of
+  // rows. One piece a lane is the quickest for one row (8192 bf16: 3.7 us on
+  // 1024 or 512 lanes, 4.3 on 256), two to three the fastest for many, with
+  // fewer waves that have to meet (16384 rows of 4096 bf16: 48.5 us on 256
+  // lanes, 52.7 on 512; 16384 of 1024: 12.5 on 64, 14.1 on 128; 8192 of 768
+  // fp32: 9.1 on 64, 11.8 on 256; 16384 of 8192 bf16: 93 on 512 and on 256,
+  // 122 on 1024).
   if (nvec <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (nvec <= 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (nvec <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
   else if (nvec <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (nvec <= 256) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (nvec <= 192) go(integral_constant<int, 64>{}, integral_constant<int, 3>{});
+  else if (nvec <= 256) go(integral_constant<int, 128>{}, integral_constant<int, 2>{});
   else if (nvec <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (nvec <= 1024) go(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  else if (nvec <= 768) go(integral_constant<int, 256>{}, integral_constant<int, 3>{});
+  else if (nvec <= 1024) go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   else if (nvec <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   else {
     const int64_t grid = rows < 2048 ? rows : 2048;
@@ -447,22 +535,34 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
   }
 }
 
+// Returns the number of partial sums per column.
 template <typename T, typename W, int VEC>
-void run_bwd(const T* dy, int64_t dy_ld, const T* x, int64_t x_ld, const W* w, const float* mean, const float* rstd,
-             int64_t rows, int64_t dim, T* dx, int64_t dx_ld, float* partials, int parts, int64_t pitch,
-             hipStream_t s) {
+int run_bwd(const T* dy, int64_t dy_ld, const T* x, int64_t x_ld, const W* w, const float* mean, const float* rstd,
+             int64_t rows, int64_t dim, T* dx, int64_t dx_ld, float* partials, int64_t pitch, hipStream_t s) {
   const int64_t nvec = (dim + VEC - 1) / VEC;
+  const bool nt = 3 * rows * dim * (int64_t)sizeof(T) > kStreamBytes;
+  int parts = (int)(rows < kMaxParts ? rows : kMaxParts);
   auto go = [&](auto lpr, auto nv) {
-    constexpr int LPR = decltype(lpr)::value, NV = decltype(nv)::value, BS = LPR > 256 ? LPR : 256;
-    hipLaunchKernelGGL((k_ln_bwd<T, W, LPR, NV, VEC>), dim3((unsigned)parts), dim3(BS), 0, s, dy, dy_ld, x, x_ld, w,
-                       mean, rstd, rows, dim, dx, dx_ld, partials, pitch);
+    constexpr int LPR = decltype(lpr)::value, NV = decltype(nv)::value, BS = 1024;
+    const int64_t need = (rows + BS / LPR - 1) / (BS / LPR);
+    // long rows: two turns for each workgroup before there are more of them, as
+    // their partial sums cost more than the second turn
+    const int64_t want = LPR >= 512 && need >= 64 ? (need + 1) / 2 : need;
+    parts = (int)(want < kMaxParts ? want : kMaxParts);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)parts), dim3(BS), 0, s, dy, dy_ld, x, x_ld, w, mean, rstd, rows, dim,
+                         dx, dx_ld, partials, pitch);
+    };
+    if (nt) launch(k_ln_bwd<T, W, LPR, NV, VEC, BS, true>);
+    else launch(k_ln_bwd<T, W, LPR, NV, VEC, BS, false>);
   };
   using std::integral_constant;
   if (nvec <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (nvec <= 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (nvec <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (nvec <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (nvec <= 128) go(integral_constant<int, 128>{}, integral_constant<int, 1>{});
   else if (nvec <= 256) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (nvec <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (nvec <= 512) go(integral_constant<int, 512>{}, integral_constant<int, 1>{});
   else if (nvec <= 1024) go(integral_constant<int, 1024>{}, integral_constant<int, 1>{});
   else if (nvec <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   else {
@@ -475,6 +575,7 @@ void run_bwd(const T* dy, int64_t dy_ld, const T* x, int64_t x_ld, const W* w, c
                          x_ld, mean, rstd, rows, dim, partials, pitch, tiles);
     }
   }
+  return parts;
 }
 
 }  // namespace
@@ -482,7 +583,7 @@ void run_bwd(const T* dy, int64_t dy_ld, const T* x, int64_t x_ld, const W* w, c
 LnPlan ln_plan(int64_t rows, int64_t dim) {
   LnPlan p;
   p.pitch = (dim + 7) / 8 * 8;
-  p.parts = rows < 512 ? rows : 512;
+  p.parts = rows < kMaxParts ? rows : kMaxParts;
   return p;
 }
 
@@ -504,24 +605,24 @@ hipError_t launch_layer_norm_backward(const void* dy, int64_t dy_ld, const void*
                                       int64_t dim, void* dx, int64_t dx_ld, void* dw, void* db, int grad_dtype,
                                       bool first, void* workspace, hipStream_t s) {
   const LnPlan p = ln_plan(rows, dim);
+  int parts = 0;
   const bool grads = dw || db;
   float* partials = grads ? static_cast<float*>(workspace) : nullptr;
   if (rows > 0) {
-    const int parts = (int)p.parts;
     if (dtype == ZS_BF16) {
-      if (wdtype == ZS_BF16) run_bwd<uint16_t, uint16_t, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, parts, p.pitch, s);
-      else run_bwd<uint16_t, float, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, parts, p.pitch, s);
+      if (wdtype == ZS_BF16) parts = run_bwd<uint16_t, uint16_t, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, p.pitch, s);
+      else parts = run_bwd<uint16_t, float, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, p.pitch, s);
     } else {
-      if (wdtype == ZS_BF16) run_bwd<float, uint16_t, kVecBf16>((const float*)dy, dy_ld, (const float*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, parts, p.pitch, s);
-      else run_bwd<float, float, kVecF32>((const float*)dy, dy_ld, (const float*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, parts, p.pitch, s);
+      if (wdtype == ZS_BF16) parts = run_bwd<float, uint16_t, kVecBf16>((const float*)dy, dy_ld, (const float*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, p.pitch, s);
+      else parts = run_bwd<float, float, kVecF32>((const float*)dy, dy_ld, (const float*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, p.pitch, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (grads && (rows > 0 || first)) {  // without rows the sums are zero
     const dim3 gd((unsigned)(2 * ((dim + 63) / 64))), bd(kJoinWaves * 64);
-    if (grad_dtype == ZS_BF16) hipLaunchKernelGGL((k_ln_grads<uint16_t>), gd, bd, 0, s, partials, p.pitch, (int)p.parts, dim, (uint16_t*)dw, (uint16_t*)db, (int)first);
-    else hipLaunchKernelGGL((k_ln_grads<float>), gd, bd, 0, s, partials, p.pitch, (int)p.parts, dim, (float*)dw, (float*)db, (int)first);
+    if (grad_dtype == ZS_BF16) hipLaunchKernelGGL((k_ln_grads<uint16_t>), gd, bd, 0, s, partials, p.pitch, parts, dim, (uint16_t*)dw, (uint16_t*)db, (int)first);
+    else hipLaunchKernelGGL((k_ln_grads<float>), gd, bd, 0, s, partials, p.pitch, parts, dim, (float*)dw, (float*)db, (int)first);
   }
   return hipGetLastError();
 }

@@ -21,6 +21,13 @@ __device__ __forceinline__ u32x4 ld16(const void* p) {
 __device__ __forceinline__ void st16(u32x4 v, void* p) {
   *(__attribute__((address_space(1))) u32x4_any*)p = v;
 }
+// the same for memory that is touched once
+__device__ __forceinline__ u32x4 ld16_nt(const void* p) {
+  return __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4_any*)p);
+}
+__device__ __forceinline__ void st16_nt(u32x4 v, void* p) {
+  __builtin_nontemporal_store(v, (__attribute__((address_space(1))) u32x4_any*)p);
+}
 
 // VEC consecutive elements of a row as they lie in memory.
 template <typename T, int VEC>
@@ -37,12 +44,31 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = ld16(p + i * (16 / (int)sizeof(T)));
   }
+  __device__ __forceinline__ void load_nt(const T* p) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = ld16_nt(p + i * (16 / (int)sizeof(T)));
+  }
   // the first n (below VEC) elements, zeros behind them
   __device__ __forceinline__ void load_part(const T* p, int n) {
     clear();
 #pragma unroll
     for (int e = 0; e < VEC; ++e)
       if (e < n) put(e, ld_g(p + e));
+  }
+  // Keeps the piece as it lies in memory from here on: without it the compiler
+  // widens values that a loop only reads before the loop and holds them in
+  // twice the registers.
+  __device__ __forceinline__ void stay_packed() {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w = r[i][k];
+          asm volatile("" : "+v"(w));
+          r[i][k] = w;
+        }
+    }
   }
   __device__ __forceinline__ void put(int e, float x) { r[e / 4][e % 4] = __float_as_uint(x); }
   __device__ __forceinline__ void put(int e, uint16_t h) {
@@ -55,26 +81,40 @@ struct Piece {
   }
 };
 
+// fp32 -> bf16 by the hardware's conversion (round to nearest even, NaN stays a
+// quiet NaN): one instruction for two values, where the integer form takes
+// about eleven, which the layer norm kernels, near their VALU bound for bf16
+// rows, would feel.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 // One value rounded to the row's type.
 template <typename T>
 __device__ __forceinline__ T round_to(float x) {
   if constexpr (sizeof(T) == 4) return x;
-  else return (T)f32_to_bf16(x);
+  else return (T)pack_bf16(x, x);
 }
 
 // VEC fp32 values stored as a row's elements, each rounded once.
-template <typename T, int VEC>
+template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_piece(T* p, const float* v) {
+  auto st = [](u32x4 x, void* q) {
+    if constexpr (NT) st16_nt(x, q);
+    else st16(x, q);
+  };
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i)
-      st16(u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+      st(u32x4{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
                  __float_as_uint(v[4 * i + 3])}, p + 4 * i);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC / 8; ++i)
-      st16(u32x4{pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                 pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])}, p + 8 * i);
+      st(u32x4{pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                 pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7])}, p + 8 * i);
   }
 }
 template <typename T, int VEC>
@@ -84,12 +124,12 @@ __device__ __forceinline__ void store_part(T* p, const float* v, int n) {
     if (e < n) st_g(round_to<T>(v[e]), p + e);
 }
 
-// Sum over the wave's lanes (G = 64) or over each aligned group of 16 (G = 16),
+// Sum over the wave's lanes (G = 64) or over each aligned group of G lanes (16, 32),
 // the same bits in every lane of the group: pairs of lanes that mirror each
 // other are added, so both hold the same sum after each step.
 template <int G>
 __device__ __forceinline__ float lane_sum(float x) {
-  static_assert(G == 16 || G == 64, "a row of 16 lanes or the wave");
+  static_assert(G == 16 || G == 32 || G == 64, "16 lanes, half of the wave or the wave");
   auto dpp = [](float v, auto ctrl) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
   };
@@ -97,9 +137,11 @@ __device__ __forceinline__ float lane_sum(float x) {
   x += dpp(x, std::integral_constant<int, 0x4e>{});   // lane ^ 2
   x += dpp(x, std::integral_constant<int, 0x141>{});  // mirrored within 8
   x += dpp(x, std::integral_constant<int, 0x140>{});  // mirrored within 16
-  if constexpr (G == 64) {
+  if constexpr (G >= 32) {
     const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (G == 64) {
     const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
   }
