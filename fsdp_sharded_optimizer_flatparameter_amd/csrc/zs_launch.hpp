@@ -164,10 +164,10 @@ hipError_t launch_copy_out(const uint16_t* gathered, const zs_param_desc* d_desc
 // where each array starts (bytes from the workspace's start) and how the work
 // is cut. Depends on the sizes alone, so the sums have one order.
 struct EmbedPlan {
-  int chunk;         // sorted entries per chunk
+  int chunk;         // sorted entries per chunk (a workgroup's)
   int64_t chunks;    // chunks of the n entries
   int64_t pitch;     // fp32 values per partial row (dim rounded up to 8)
-  int bits, passes;  // bits of a key, and digits that the sort takes them in
+  int bits, passes;  // bits of a key, and digits of the sort
   int64_t tiles;     // tiles of the sort's passes
   int64_t keys[2], pos[2], counts, totals, partials, bytes;
 };
