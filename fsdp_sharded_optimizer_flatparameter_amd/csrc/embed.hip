@@ -23,39 +23,31 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int index_type, int64_
 }
 
 // The calling wave's number in the grid, in a scalar register.
+template <int BS = kThreads>
 __device__ __forceinline__ int64_t wave_id() {
-  return (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  return (int64_t)blockIdx.x * (BS / 64) + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 }
 // a / b for a below 2^32 in 32 bits, where the hardware has no 64-bit divide
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_cols(Piece<T, VEC>& p, const T* row, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) p.load(row + c);
-  else if (c < dim) p.load_part(row + c, (int)(dim - c));
-  else p.clear();
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_cols(T* row, const float* v, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) store_piece<T, VEC>(row + c, v);
-  else if (c < dim) store_part<T, VEC>(row + c, v, (int)(dim - c));
-}
-
 // ---------------------------------------------------------------- forward
 
 // One wave copies one tile of 64 U pieces of a row.
-template <typename T, typename O, int VEC, int U>
-__global__ __launch_bounds__(kThreads)
-void k_embed_fwd(const T* __restrict__ table, int64_t vocab, int64_t dim, int64_t table_ld,
+#ifndef EBS
+#define EBS 256
+#endif
+template <typename T, typename O, int VEC, int U, bool NT>
+__global__ __launch_bounds__(EBS)
+void k_embed_fwd(const T* __restrict__ table, int64_t vocab, uint32_t dim, int64_t table_ld,
                  const T* __restrict__ pos_table, int64_t pos_rows, int64_t pos_ld, const void* __restrict__ tokens,
                  const void* __restrict__ positions, int index_type, int64_t total, int64_t tiles, float scale,
                  O* __restrict__ out, int64_t out_ld) {
   const int lane = threadIdx.x & 63;
-  for (int64_t t = wave_id(); t < total; t += (int64_t)gridDim.x * (kThreads / 64)) {
+  for (int64_t t = wave_id<EBS>(); t < total; t += (int64_t)gridDim.x * (EBS / 64)) {
     const int64_t i = quot(t, tiles);
-    const int64_t c0 = (t - i * tiles) * (64 * U * VEC) + lane * VEC;
+    const uint32_t c0 = (uint32_t)(t - i * tiles) * (64 * U * VEC) + lane * VEC;
     const int64_t id = id_at(tokens, index_type, i);
     const bool in = (uint64_t)id < (uint64_t)vocab;  // an id outside of the table selects a row of zeros
     const T* row = table + (in ? id : 0) * table_ld;
@@ -81,15 +73,21 @@ void k_embed_fwd(const T* __restrict__ table, int64_t vocab, int64_t dim, int64_
       float v[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = with_pos ? fmaf(a[u].get(e), scale, p[u].get(e)) : a[u].get(e) * scale;
-      store_cols<O, VEC>(orow, v, c0 + u * 64 * VEC, dim);
+      store_cols<O, VEC, NT>(orow, v, c0 + u * 64 * VEC, dim);
     }
   }
 }
 
 // ---------------------------------------------------------------- sort
 
-#ifndef FILLG
-#define FILLG 512
+#ifndef EU
+#define EU 2
+#endif
+#ifndef ENT
+#define ENT -1
+#endif
+#ifndef FILLB
+#define FILLB 4096
 #endif
 #ifndef KW
 #define KW 8192
@@ -117,8 +115,12 @@ struct Keys {
 
 // counts[digit][tile]: entries of a tile with that digit
 __global__ __launch_bounds__(kThreads)
-void k_sort_count(Keys k, int64_t n, int shift, int64_t tiles, uint32_t* __restrict__ counts) {
+void k_sort_count(Keys k, int64_t n, int shift, int64_t tiles, uint32_t* __restrict__ counts,
+                  uint8_t* __restrict__ touched) {
   __shared__ uint32_t h[kBins];
+  if (touched)  // the first pass clears it
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < k.vocab; i += (int64_t)gridDim.x * kThreads * 16)
+      st16(u32x4{0u, 0u, 0u, 0u}, touched + i);  // the array's room is a multiple of 16
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     for (int b = threadIdx.x; b < kBins; b += kThreads) h[b] = 0;
     __syncthreads();
@@ -176,29 +178,34 @@ void k_sort_scan(uint32_t* __restrict__ counts, int64_t tiles, uint32_t* __restr
   if (threadIdx.x == 0) totals[blockIdx.x] = run;
 }
 
-// Rank of each lane's digit among the wave's earlier entries with the same
-// digit: `h` is the wave's own running count per digit. Lanes with live ==
-// false take no part.
-__device__ __forceinline__ uint32_t wave_rank(uint32_t d, bool live, uint32_t* h) {
-  uint64_t same = __ballot(live);
+// Lanes before this one, among those with live set, that hold the same digit;
+// *same gets all that do. A lane that is not live gets nothing of use.
+__device__ __forceinline__ uint32_t rank_in_wave(uint32_t d, bool live, uint64_t* same) {
+  uint64_t s = __ballot(live);
 #pragma unroll
   for (int b = 0; b < kBits; ++b) {
     const bool one = (d >> b) & 1u;
     const uint64_t m = __ballot(one);
-    same &= one ? m : ~m;
+    s &= one ? m : ~m;
   }
-  const int lane = threadIdx.x & 63;
+  *same = s;
+  return (uint32_t)__popcll(s & ((1ull << (threadIdx.x & 63)) - 1));
+}
+
+// The same over several rounds: `h` is the wave's own running count per digit.
+__device__ __forceinline__ uint32_t wave_rank(uint32_t d, bool live, uint32_t* h) {
+  uint64_t same;
+  const uint32_t rank = rank_in_wave(d, live, &same);
   const int leader = same ? __builtin_ctzll(same) : 0;
   uint32_t before = 0;
-  if (live && lane == leader) before = atomicAdd(&h[d], (uint32_t)__popcll(same));
-  before = __shfl(before, leader, 64);
-  return before + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+  if (live && rank == 0) before = atomicAdd(&h[d], (uint32_t)__popcll(same));
+  return __shfl(before, leader, 64) + rank;
 }
 
 __global__ __launch_bounds__(kThreads)
 void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int shift, int64_t tiles,
                     const uint32_t* __restrict__ counts, const uint32_t* __restrict__ totals,
-                    uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
+                    uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched) {
   constexpr int NW = kThreads / 64;
   __shared__ uint32_t hist[NW][kBins];
   __shared__ uint32_t base[kBins];
@@ -243,111 +250,158 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
         const uint32_t to = hist[wave][(key[r] >> shift) & (kBins - 1)] + rank[r];
         keys_out[to] = key[r];
         pos_out[to] = pos_in ? pos_in[i] : (uint32_t)i;
+        if (touched && key[r] < (uint32_t)k.vocab) touched[key[r]] = 1;  // the last pass sets it
       }
     }
     __syncthreads();
   }
 }
 
-// Zeros into all rows, by the workgroups that `part` of `parts` numbers: tiles
-// of kFillTile bytes of the whole table where its rows follow each other
-// without gaps, else of each row.
-constexpr int kFillTile = 16384;
-template <typename Gt, int BS>
-__device__ void fill_rows(Gt* grad, int64_t vocab, int64_t dim, int64_t ld, int64_t part, int64_t parts) {
-  constexpr int64_t TE = kFillTile / sizeof(Gt);
-  constexpr int VEC = 16 / sizeof(Gt);
-  if (ld == dim) {
-    dim *= vocab;
-    vocab = 1;
-  }
-  const int64_t per_row = (dim + TE - 1) / TE, total = vocab * per_row;
-  for (int64_t t = part; t < total; t += parts) {
-    const int64_t row = per_row == 1 ? t : t / per_row, c0 = (t - row * per_row) * TE;
-    Gt* out = grad + row * ld;
-    const int64_t end = c0 + TE < dim ? c0 + TE : dim;
-    for (int64_t c = c0 + (int64_t)threadIdx.x * VEC; c < end; c += (int64_t)BS * VEC) {
-      if (c + VEC <= end) st16_nt(u32x4{0u, 0u, 0u, 0u}, out + c);
-      else
-        for (int64_t k = c; k < end; ++k) st_g((Gt)0, out + k);
-    }
-  }
+// One pass over up to kPassSort entries in one launch: each workgroup counts the
+// digits of all entries itself (they lie in L2), those of the tiles before its
+// own apart, and then places its own tile, an entry per thread. Counting by
+// tiles in a launch of its own, their sums in a second and the placing in a
+// third (k_sort_count, k_sort_scan, k_sort_scatter) takes SORT_FIGURES.
+// The first pass clears `touched`, a byte per row of the gradient, with the
+// workgroups behind the tiles; the last one sets it for each token's row.
+constexpr int kPassBS = 1024;
+constexpr int kPassWaves = kPassBS / 64;
+#ifndef PSORT
+#define PSORT 32768
+#endif
+constexpr int64_t kPassSort = PSORT;
+// Copies of the counters, each for every kCopies-th lane and shifted by a bank:
+// frequent tokens have several lanes of a wave count in one place, one after
+// the other. A counter holds the entries before the tile in its lower half and
+// all in its upper half: a copy sees at most kPassSort / kCopies of them.
+#ifndef COPIES
+#define COPIES 8
+#endif
+constexpr int kCopies = COPIES;
+static_assert(kPassSort / kCopies < 65536, "16 bits hold a count");
+constexpr int kClearBytes = kPassBS * 16;  // of `touched`, per workgroup
+
+__device__ __forceinline__ void clear_touched(uint8_t* touched, int64_t vocab, int64_t block) {
+  const int64_t i = block * kClearBytes + (int64_t)threadIdx.x * 16;
+  if (i < vocab) st16(u32x4{0u, 0u, 0u, 0u}, touched + i);  // the array's room is a multiple of 16
 }
 
-// Up to 1024 R tokens: workgroup 0 sorts them in LDS, in one launch instead of
-// three per digit, while the others, where there are any, fill the gradient
-// with zeros (`first`).
-constexpr int kSmallBS = 1024;
-constexpr int kSmallWaves = kSmallBS / 64;
-constexpr int64_t kSmallSort = 16 * kSmallBS;
-template <int R, typename Gt>
-__global__ __launch_bounds__(kSmallBS)
-void k_sort_small(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
-                  Gt* __restrict__ grad, int64_t dim, int64_t grad_ld) {
-  if (blockIdx.x > 0) {
-    fill_rows<Gt, kSmallBS>(grad, k.vocab, dim, grad_ld, blockIdx.x - 1, gridDim.x - 1);
+__global__ __launch_bounds__(kPassBS)
+void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int tiles, int last,
+                 uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched) {
+  __shared__ uint32_t counts[kCopies][kBins + 1];
+  __shared__ uint32_t hist[kPassWaves][kBins];
+  __shared__ uint32_t lds[kPassWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if ((int)blockIdx.x >= tiles) {
+    clear_touched(touched, k.vocab, blockIdx.x - tiles);
     return;
   }
-  __shared__ uint32_t skey[R * kSmallBS];
-  __shared__ uint16_t spos[R * kSmallBS];  // positions below 2^14
-  __shared__ uint32_t hist[kSmallWaves][kBins];
-  __shared__ uint32_t base[kBins];
-  __shared__ uint32_t lds[kSmallWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t key[R], pos[R];
-  // places behind the last token take a key behind all others: they stay last
+  auto digit = [&](uint32_t key) { return (key >> shift) & (kBins - 1); };
+  const int tile0 = blockIdx.x * kPassBS, i = tile0 + threadIdx.x;
+  constexpr int U = 8;  // entries on their way per thread
+  uint32_t kk[U];
+  auto fetch = [&](int j0) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = (wave * R + r) * 64 + lane;
-    pos[r] = i;
-    key[r] = i < n ? k.at(i) : 0xffffffffu;
+    for (int u = 0; u < U; ++u) kk[u] = j0 + u * kPassBS < n ? k.at(j0 + u * kPassBS) : 0;
+  };
+  fetch(threadIdx.x);
+  const uint32_t key = i < n ? k.at(i) : 0;
+  const uint32_t pos = i < n ? (pos_in ? pos_in[i] : (uint32_t)i) : 0;
+  for (int b = threadIdx.x; b < kCopies * (kBins + 1); b += kPassBS) (&counts[0][0])[b] = 0;
+#pragma unroll
+  for (int b = 0; b < kBins / 64; ++b) hist[wave][b * 64 + lane] = 0;
+  __syncthreads();
+  for (int j0 = threadIdx.x; j0 < n; j0 += U * kPassBS) {
+    if (j0 != (int)threadIdx.x) fetch(j0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * kPassBS;
+      if (j < n) atomicAdd(&counts[lane % kCopies][digit(kk[u])], j < tile0 ? 0x10001u : 0x10000u);
+    }
   }
+  // rank within the wave, and the wave's count of each digit
+  const uint32_t d = digit(key);
+  uint64_t same;
+  const uint32_t rank = rank_in_wave(d, i < n, &same);
+  if (i < n && rank == 0) hist[wave][d] = (uint32_t)__popcll(same);
+  __syncthreads();
+  uint32_t sum = 0, mine = 0;
+  if (threadIdx.x < kBins) {
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      mine += counts[c][threadIdx.x] & 0xffffu;
+      sum += counts[c][threadIdx.x] >> 16;
+    }
+  }
+  uint32_t all;
+  uint32_t at = block_scan<kPassBS>(sum, lds, &all) + mine;
+  if (threadIdx.x < kBins) {
+    uint32_t c[kPassWaves];
+#pragma unroll
+    for (int w = 0; w < kPassWaves; ++w) c[w] = hist[w][threadIdx.x];
+#pragma unroll
+    for (int w = 0; w < kPassWaves; ++w) {
+      hist[w][threadIdx.x] = at;
+      at += c[w];
+    }
+  }
+  __syncthreads();
+  if (i < n) {
+    const uint32_t to = hist[wave][d] + rank;
+    keys_out[to] = key;
+    pos_out[to] = pos;
+    if (last && touched && key < (uint32_t)k.vocab) touched[key] = 1;
+  }
+}
+
+// Up to 1024 entries: all passes in one launch of one workgroup, an entry per
+// thread, keys and positions handed on in LDS.
+__global__ __launch_bounds__(kPassBS)
+void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
+  __shared__ uint32_t hist[kPassWaves][kBins];
+  __shared__ uint32_t skey[kPassBS], spos[kPassBS];
+  __shared__ uint32_t lds[kPassWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
+  uint32_t key = i < n ? k.at(i) : 0, pos = i;
   for (int p = 0; p < passes; ++p) {
-    const int shift = p * kBits;
-    uint32_t rank[R];
 #pragma unroll
     for (int b = 0; b < kBins / 64; ++b) hist[wave][b * 64 + lane] = 0;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-#pragma unroll
-    for (int r = 0; r < R; ++r) rank[r] = wave_rank((key[r] >> shift) & (kBins - 1), true, hist[wave]);
+    const uint32_t d = (key >> (p * kBits)) & (kBins - 1);
+    uint64_t same;
+    const uint32_t rank = rank_in_wave(d, i < n, &same);
     __syncthreads();
-    // where each digit starts, and each wave's entries within it
-    uint32_t run = 0;
+    if (i < n && rank == 0) hist[wave][d] = (uint32_t)__popcll(same);
+    __syncthreads();
+    uint32_t c[kPassWaves], sum = 0;
     if (threadIdx.x < kBins) {
 #pragma unroll
-      for (int w = 0; w < kSmallWaves; ++w) {
-        const uint32_t c = hist[w][threadIdx.x];
-        hist[w][threadIdx.x] = run;
-        run += c;
-      }
+      for (int w = 0; w < kPassWaves; ++w) sum += c[w] = hist[w][threadIdx.x];
     }
     uint32_t all;
-    const uint32_t before = block_scan<kSmallBS>(run, lds, &all);
-    if (threadIdx.x < kBins) base[threadIdx.x] = before;
-    __syncthreads();
+    uint32_t at = block_scan<kPassBS>(sum, lds, &all);
+    if (threadIdx.x < kBins) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const uint32_t d = (key[r] >> shift) & (kBins - 1);
-      const uint32_t to = base[d] + hist[wave][d] + rank[r];
-      skey[to] = key[r];
-      spos[to] = (uint16_t)pos[r];
+      for (int w = 0; w < kPassWaves; ++w) {
+        hist[w][threadIdx.x] = at;
+        at += c[w];
+      }
     }
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = (wave * R + r) * 64 + lane;
-      key[r] = skey[i];
-      pos[r] = spos[i];
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = (wave * R + r) * 64 + lane;
     if (i < n) {
-      keys_out[i] = key[r];
-      pos_out[i] = pos[r];
+      const uint32_t to = hist[wave][d] + rank;
+      skey[to] = key;
+      spos[to] = pos;
     }
+    __syncthreads();
+    if (i < n) {
+      key = skey[i];
+      pos = spos[i];
+    }
+  }
+  if (i < n) {
+    keys_out[i] = key;
+    pos_out[i] = pos;
   }
 }
 
@@ -361,25 +415,68 @@ void k_sort_small(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, ui
 // in order; one that comes from the chunk before, or goes on behind the chunk,
 // leaves one partial sum in the workspace (rows 2c and 2c + 1 of chunk c),
 // joined by k_embed_join.
-constexpr int kWaves = 16;
+#ifndef KWV
+#define KWV 8
+#endif
+constexpr int kWaves = KWV;
+
+// Zeros into the rows that no token selects (all of them without `touched`):
+// `step` (up to 64) consecutive rows per workgroup, whose marks are read at
+// once, a wave for a row.
+#ifndef NOFNT
+#define FST st16_nt
+#else
+#define FST st16
+#endif
+#ifndef FBS
+#define FBS 64
+#endif
+template <typename Gt>
+__global__ __launch_bounds__(FBS)
+void k_embed_fill(const uint8_t* __restrict__ touched, int64_t vocab, uint32_t dim, int64_t total, int step,
+                  int pieces, uint32_t width, Gt* __restrict__ grad, int64_t ld) {
+  constexpr uint32_t VEC = 16 / sizeof(Gt);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+    const int64_t g = quot(t, pieces), r0 = g * step, row = r0 + lane;
+    const uint32_t c0 = (uint32_t)(t - g * pieces) * width, c1 = c0 + width < dim ? c0 + width : dim;
+    uint64_t empty = __ballot(lane < step && row < vocab && !(touched && touched[row]));
+    for (int j = 0; empty; empty &= empty - 1, ++j) {
+      if (FBS > 64 && j % (FBS / 64) != wave) continue;
+      Gt* out = grad + (r0 + __builtin_ctzll(empty)) * ld;
+      for (uint32_t c = c0 + lane * VEC; c < c1; c += 64 * VEC) {
+        if (c + VEC <= c1) FST(u32x4{0u, 0u, 0u, 0u}, out + c);
+        else
+          for (uint32_t k = c; k < c1; ++k) st_g((Gt)0, out + k);
+      }
+    }
+  }
+}
 
 template <typename Gt, int VEC>
 __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale, bool add, const Piece<Gt, VEC>& old,
-                                         int64_t c, int64_t dim) {
+                                         uint32_t c, uint32_t dim) {
   float v[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) v[e] = add ? old.get(e) + sum[e] * scale : sum[e] * scale;
   store_cols<Gt, VEC>(row, v, c, dim);
 }
 
+#ifndef W1
+#define W1 4
+#endif
+#ifndef W0
+#define W0 4
+#endif
 template <typename T, typename Gt, int VEC, int K, bool FIRST>
-__global__ __launch_bounds__(kWaves * 64)
+__global__ __launch_bounds__(kWaves * 64, FIRST ? W1 : W0)
 void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, uint32_t vocab,
-                    int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, int64_t dim,
+                    int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, uint32_t dim,
                     float scale, Gt* __restrict__ grad, int64_t grad_ld, float* __restrict__ partials,
-                    int64_t pitch) {
+                    uint32_t pitch) {
   // rows on their way at once; with them go the gradient's old rows
-  constexpr int U = K < 8 ? K : (FIRST || sizeof(Gt) == 2 ? 8 : 4);
+  constexpr int U = K < 8 || sizeof(T) * VEC > 16 ? 4 : 8;
   static_assert(K + 2 <= 64 && K % U == 0, "a lane for each entry and its two neighbours");
   __shared__ __align__(16) float heads[kWaves][64 * VEC];
   __shared__ int through[kWaves];
@@ -387,7 +484,7 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   for (int64_t item = blockIdx.x; item < chunks * coltiles; item += gridDim.x) {
     const int64_t ch = quot(item, coltiles);
-    const int64_t c = ((item - ch * coltiles) * 64 + lane) * VEC;
+    const uint32_t c = ((uint32_t)(item - ch * coltiles) * 64 + lane) * VEC;
     const int64_t e0 = (ch * kWaves + wave) * K;
     // lane i holds entry e0 - 1 + i; what lies outside the list matches no key
     uint32_t kk = 0xffffffffu, pp = 0;
@@ -414,11 +511,12 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
       Piece<Gt, VEC> old[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (u0 + u < cnt) {
-          const int64_t row = (uint32_t)__builtin_amdgcn_readlane((int)pp, u0 + u + 1);
-          load_cols<T, VEC>(v[u], dout + row * dout_ld, c, dim);
-          if (!FIRST && key_at(u0 + u + 1) != key_at(u0 + u))
-            load_cols<Gt, VEC>(old[u], grad + (int64_t)key_at(u0 + u) * grad_ld, c, dim);
+        const int at = u0 + u < cnt ? u0 + u : cnt - 1;  // clamped: the last one again
+        const int64_t row = (uint32_t)__builtin_amdgcn_readlane((int)pp, at + 1);
+        load_cols<T, VEC>(v[u], dout + row * dout_ld, c, dim);
+        if (!FIRST) {
+          if (key_at(at + 1) != key_at(at)) load_cols<Gt, VEC>(old[u], grad + (int64_t)key_at(at) * grad_ld, c, dim);
+          else old[u].clear();
         }
       }
 #pragma unroll
@@ -464,7 +562,7 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
     };
     if (goes && !whole) {  // a run that starts in this wave and goes on
       if (follow(wave + 1)) {
-        if (c < pitch) store_piece<float, VEC>(partials + (2 * ch + 1) * pitch + c, acc);
+        if (c < pitch) store_piece<float, VEC>(partials + (2 * ch + 1) * (int64_t)pitch + c, acc);
       } else {
         Piece<Gt, VEC> old;
         Gt* row = grad + (int64_t)key_at(K - 1) * grad_ld;
@@ -476,7 +574,7 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
       follow(0);
-      if (c < pitch) store_piece<float, VEC>(partials + 2 * ch * pitch + c, acc);
+      if (c < pitch) store_piece<float, VEC>(partials + 2 * ch * (int64_t)pitch + c, acc);
     }
     __syncthreads();
   }
@@ -487,12 +585,12 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
 template <typename Gt, int VEC>
 __global__ __launch_bounds__(kThreads)
 void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, int chunk, int64_t chunks,
-                  int64_t coltiles, int64_t dim, float scale, Gt* __restrict__ grad, int64_t grad_ld, int first,
-                  const float* __restrict__ partials, int64_t pitch) {
+                  int64_t coltiles, uint32_t dim, float scale, Gt* __restrict__ grad, int64_t grad_ld, int first,
+                  const float* __restrict__ partials, uint32_t pitch) {
   const int lane = threadIdx.x & 63;
   for (int64_t wv = wave_id(); wv < chunks * coltiles; wv += (int64_t)gridDim.x * (kThreads / 64)) {
     const int64_t ch = quot(wv, coltiles);
-    const int64_t c = ((wv - ch * coltiles) * 64 + lane) * VEC;
+    const uint32_t c = ((uint32_t)(wv - ch * coltiles) * 64 + lane) * VEC;
     const int64_t e1 = (ch + 1) * chunk;
     if (e1 >= n) continue;
     const uint32_t key = keys[e1 - 1], behind = keys[e1], ahead = ch > 0 ? keys[ch * chunk - 1] : 0xffffffffu;
@@ -502,7 +600,7 @@ void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, 
     Piece<Gt, VEC> old;
     if (!first) load_cols<Gt, VEC>(old, row, c, dim);
     Piece<float, VEC> p;
-    if (live) p.load(partials + (2 * ch + 1) * pitch + c);
+    if (live) p.load(partials + (2 * ch + 1) * (int64_t)pitch + c);
     else p.clear();
     float sum[VEC];
 #pragma unroll
@@ -516,7 +614,7 @@ void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, 
         Piece<float, VEC> q[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (i + u < more && live) q[u].load(partials + 2 * (b + i + u) * pitch + c);
+          if (i + u < more && live) q[u].load(partials + 2 * (b + i + u) * (int64_t)pitch + c);
           else q[u].clear();
         }
 #pragma unroll
@@ -530,101 +628,82 @@ void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, 
   }
 }
 
-// Zeros into the rows that no token selects. A workgroup takes R (a power of
-// two up to 64) rows; each lane below R looks one of them up in the sorted keys.
-template <typename Gt, int VEC>
-__global__ __launch_bounds__(kThreads)
-void k_embed_fill(const uint32_t* __restrict__ keys, int64_t n, int64_t vocab, int R, int64_t groups, int64_t dim,
-                  Gt* __restrict__ grad, int64_t grad_ld) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-    const int64_t row = g * R + lane;
-    bool empty = false;
-    if (lane < R && row < vocab) {
-      int64_t lo = 0, hi = n;  // first entry not below `row`
-      while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (keys[mid] < (uint32_t)row) lo = mid + 1;
-        else hi = mid;
-      }
-      empty = lo == n || keys[lo] != (uint32_t)row;
-    }
-    uint64_t mask = __ballot(empty);
-    float z[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) z[e] = 0.0f;
-    for (int j = 0; mask; mask &= mask - 1, ++j) {
-      if (j % (kThreads / 64) != wave) continue;
-      Gt* out = grad + (g * R + __builtin_ctzll(mask)) * grad_ld;
-      for (int64_t c = (int64_t)lane * VEC; c < dim; c += 64 * VEC) store_cols<Gt, VEC>(out, z, c, dim);
-    }
-  }
-}
-
-template <typename T, typename Gt>
-constexpr int vec_of() { return sizeof(T) == 2 || sizeof(Gt) == 2 ? 8 : 4; }
+// Elements of a lane's piece: 16 bytes of what is written, so that a wave's
+// store covers whole lines. (16384 rows of 4096 bf16 into fp32, 8 elements a
+// lane: two stores with gaps took 71 us, 99 past the caches; 4: VEC_FIGURES.)
+template <typename O>
+constexpr int vec_of() { return 16 / sizeof(O); }
 
 template <typename T, typename O>
 void run_embed_fwd(const T* table, int64_t vocab, int64_t dim, int64_t table_ld, const T* pos_table, int64_t pos_rows,
                    int64_t pos_ld, const void* tokens, const void* positions, int index_type, int64_t n, float scale,
                    O* out, int64_t out_ld, hipStream_t s) {
-  constexpr int VEC = vec_of<T, O>();
+  constexpr int VEC = vec_of<O>();
+  const bool nt = n * dim * (int64_t)sizeof(O) > ENT;
   auto go = [&](auto uu) {
     constexpr int U = decltype(uu)::value;
     const int64_t tiles = (dim + 64 * U * VEC - 1) / (64 * U * VEC), total = n * tiles;
-    hipLaunchKernelGGL((k_embed_fwd<T, O, VEC, U>), dim3((unsigned)grid_for(total, kThreads / 64)), dim3(kThreads), 0,
-                       s, table, vocab, dim, table_ld, pos_table, pos_rows, pos_ld, tokens, positions, index_type,
-                       total, tiles, scale, out, out_ld);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(total, EBS / 64, EBS)), dim3(EBS), 0, s, table, vocab,
+                         (uint32_t)dim, table_ld, pos_table, pos_rows, pos_ld, tokens, positions, index_type, total,
+                         tiles, scale, out, out_ld);
+    };
+    if (nt) launch(k_embed_fwd<T, O, VEC, U, true>);
+    else launch(k_embed_fwd<T, O, VEC, U, false>);
   };
   const int64_t pieces = (dim + 64 * VEC - 1) / (64 * VEC);
-  if (pieces == 1) go(std::integral_constant<int, 1>{});
-  else go(std::integral_constant<int, 2>{});
+  if (pieces < EU) go(std::integral_constant<int, 1>{});
+  else go(std::integral_constant<int, EU>{});
 }
 
 template <typename T, typename Gt>
 void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys, uint32_t* const* pos,
-                   uint32_t* counts, uint32_t* totals, float* partials, const T* dout, int64_t dout_ld, int64_t n,
+                   uint32_t* counts, uint32_t* totals, uint8_t* touched, float* partials, const T* dout, int64_t dout_ld, int64_t n,
                    int64_t vocab, int64_t dim, float scale, Gt* grad, int64_t grad_ld, bool first, hipStream_t s) {
-  constexpr int VEC = vec_of<T, Gt>();
+  constexpr int VEC = vec_of<Gt>();
   int last = 0;
-  if (n <= kSmallSort) {
-    // the zeros: a workgroup per CU and a half, or fewer for a small table
-    const int64_t tiles = first ? (vocab * dim * (int64_t)sizeof(Gt) + kFillTile - 1) / kFillTile : 0;
-    const dim3 gd((unsigned)(1 + (tiles < FILLG ? tiles : FILLG))), bd(kSmallBS);
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, gd, bd, 0, s, tokens, (int)n, p.passes, keys[0], pos[0], grad, dim, grad_ld);
-    };
-    if (n <= kSmallBS) go(k_sort_small<1, Gt>);
-    else if (n <= 4 * kSmallBS) go(k_sort_small<4, Gt>);
-    else if (n <= 8 * kSmallBS) go(k_sort_small<8, Gt>);
-    else go(k_sort_small<16, Gt>);
-  } else {
-    const dim3 gd((unsigned)grid_for(p.tiles, 1)), bd(kThreads);
-    for (int i = 0; i < p.passes; ++i) {
-      const int src = (i + 1) & 1, dst = i & 1;
-      Keys k = tokens;
-      if (i) k.keys = keys[src];
-      hipLaunchKernelGGL(k_sort_count, gd, bd, 0, s, k, n, i * kBits, p.tiles, counts);
+  // Which rows a token selects is marked for the fill, except where few tokens
+  // leave few rows to spare it. The first pass clears the marks, the last one
+  // sets them.
+  uint8_t* mark = first && n > kPassBS ? touched : nullptr;
+  const int passes = mark && p.passes < 2 ? 2 : p.passes;
+  if (n > 0 && n <= kPassBS)
+    hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kPassBS), 0, s, tokens, (int)n, passes, keys[0], pos[0]);
+  for (int i = 0; n > kPassBS && i < passes; ++i) {
+    const int src = (i + 1) & 1, dst = i & 1;
+    Keys k = tokens;
+    if (i) k.keys = keys[src];
+    const uint32_t* pos_in = i ? pos[src] : nullptr;
+    const bool final = i + 1 == passes;
+    if (n <= kPassSort) {
+      const int tiles = (int)((n + kPassBS - 1) / kPassBS);
+      const int clears = i == 0 && mark ? (int)((vocab + kClearBytes - 1) / kClearBytes) : 0;
+      hipLaunchKernelGGL(k_sort_pass, dim3((unsigned)(tiles + clears)), dim3(kPassBS), 0, s, k, pos_in, (int)n,
+                         i * kBits, tiles, (int)final, keys[dst], pos[dst], mark);
+    } else {
+      const dim3 gd((unsigned)grid_for(p.tiles, 1)), bd(kThreads);
+      hipLaunchKernelGGL(k_sort_count, gd, bd, 0, s, k, n, i * kBits, p.tiles, counts, i == 0 ? mark : nullptr);
       hipLaunchKernelGGL(k_sort_scan, dim3(kBins), bd, 0, s, counts, p.tiles, totals);
-      hipLaunchKernelGGL(k_sort_scatter, gd, bd, 0, s, k, i ? pos[src] : nullptr, n, i * kBits, p.tiles, counts,
-                         totals, keys[dst], pos[dst]);
-      last = dst;
+      hipLaunchKernelGGL(k_sort_scatter, gd, bd, 0, s, k, pos_in, n, i * kBits, p.tiles, counts, totals, keys[dst],
+                         pos[dst], final ? mark : nullptr);
     }
-    if (first) {
-      int R = 1;
-      while (R < 64 && vocab / (2 * R) >= 2048) R *= 2;
-      const int64_t groups = (vocab + R - 1) / R;
-      hipLaunchKernelGGL((k_embed_fill<Gt, VEC>), dim3((unsigned)grid_for(groups, 1)), dim3(kThreads), 0, s,
-                         keys[last], n, vocab, R, groups, dim, grad, grad_ld);
-    }
+    last = dst;
+  }
+  if (first) {
+    const int64_t row_bytes = dim * (int64_t)sizeof(Gt), fit = FILLB / row_bytes;
+    const int step = (int)(fit < 1 ? 1 : fit > 64 ? 64 : fit);
+    const int pieces = (int)((row_bytes + FILLB - 1) / FILLB);
+    const uint32_t width = pieces == 1 ? (uint32_t)dim : FILLB / sizeof(Gt);
+    const int64_t total = (vocab + step - 1) / step * pieces;
+    hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(total, 1, FBS)), dim3(FBS), 0, s,
+                       mark, vocab, (uint32_t)dim, total, step, pieces, width, grad, grad_ld);
   }
   if (n == 0) return;
   const int64_t coltiles = (dim + 64 * VEC - 1) / (64 * VEC), items = p.chunks * coltiles;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(items, 1, kWaves * 64)), dim3(kWaves * 64), 0, s, keys[last],
-                       pos[last], n, (uint32_t)vocab, p.chunks, coltiles, dout, dout_ld, dim, scale, grad, grad_ld,
-                       partials, p.pitch);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(items, 1, kWaves * 64)), dim3(kWaves * 64), 0, s,
+                       keys[last], pos[last], n, (uint32_t)vocab, p.chunks, coltiles, dout, dout_ld, (uint32_t)dim, scale, grad,
+                       grad_ld, partials, (uint32_t)p.pitch);
   };
   auto pick = [&](auto f) {
     constexpr bool F = decltype(f)::value;
@@ -636,8 +715,8 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   else pick(std::false_type{});
   if (p.chunks > 1)
     hipLaunchKernelGGL((k_embed_join<Gt, VEC>), dim3((unsigned)grid_for(items, kThreads / 64)), dim3(kThreads), 0, s,
-                       keys[last], n, (uint32_t)vocab, p.chunk, p.chunks, coltiles, dim, scale, grad, grad_ld,
-                       (int)first, partials, p.pitch);
+                       keys[last], n, (uint32_t)vocab, p.chunk, p.chunks, coltiles, (uint32_t)dim, scale, grad,
+                       grad_ld, (int)first, partials, (uint32_t)p.pitch);
 }
 
 }  // namespace
@@ -666,6 +745,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
   }
   p.counts = take(4 * p.tiles * kBins);
   p.totals = take(4 * kBins);
+  p.touched = take(vocab);
   p.partials = take(4 * 2 * p.chunks * p.pitch);
   p.bytes = at;
   return p;
@@ -699,10 +779,11 @@ hipError_t launch_embed_backward(const void* dout, int dtype, int64_t dout_ld, c
   }
   uint32_t* counts = reinterpret_cast<uint32_t*>(ws + p.counts);
   uint32_t* totals = reinterpret_cast<uint32_t*>(ws + p.totals);
+  uint8_t* touched = reinterpret_cast<uint8_t*>(ws + p.touched);
   float* partials = reinterpret_cast<float*>(ws + p.partials);
   const Keys k{tokens, nullptr, index_type, vocab, padding_idx};
   auto go = [&](auto* t, auto* g) {
-    run_embed_bwd(p, k, keys, pos, counts, totals, partials,
+    run_embed_bwd(p, k, keys, pos, counts, totals, touched, partials,
                   static_cast<const std::remove_pointer_t<decltype(t)>*>(dout), dout_ld, n, vocab, dim, scale,
                   static_cast<decltype(g)>(grad), grad_ld, first, s);
   };

@@ -23,27 +23,13 @@ namespace {
 // Columns of piece j of lane l of a row's LPR lanes: consecutive lanes take
 // consecutive pieces, so a wave's access is one contiguous span.
 template <int LPR, int VEC>
-__device__ __forceinline__ int64_t col_of(int j, int l) {
-  return (int64_t)(j * LPR + l) * VEC;
-}
-
-template <typename T, int VEC, bool NT = false>
-__device__ __forceinline__ void load_cols(Piece<T, VEC>& p, const T* row, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) {
-    if constexpr (NT) p.load_nt(row + c);
-    else p.load(row + c);
-  } else if (c < dim) p.load_part(row + c, (int)(dim - c));
-  else p.clear();
-}
-template <typename T, int VEC, bool NT = false>
-__device__ __forceinline__ void store_cols(T* row, const float* v, int64_t c, int64_t dim) {
-  if (c + VEC <= dim) store_piece<T, VEC, NT>(row + c, v);
-  else if (c < dim) store_part<T, VEC>(row + c, v, (int)(dim - c));
+__device__ __forceinline__ uint32_t col_of(int j, int l) {
+  return (uint32_t)(j * LPR + l) * VEC;
 }
 
 // Weight or bias values of a piece; `missing` where the caller passes none.
 template <typename W, int VEC>
-__device__ __forceinline__ void load_affine(Piece<W, VEC>& r, const W* p, float missing, int64_t c, int64_t dim) {
+__device__ __forceinline__ void load_affine(Piece<W, VEC>& r, const W* p, float missing, uint32_t c, uint32_t dim) {
   if (p) {
     load_cols<W, VEC>(r, p, c, dim);
   } else {
@@ -63,7 +49,7 @@ struct Part {
 template <typename T, typename W, int LPR, int NV, int VEC, bool NT>
 __global__ __launch_bounds__(LPR > 256 ? LPR : 256)
 void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, const W* __restrict__ b,
-              int64_t rows, int64_t dim, float eps, T* __restrict__ y, int64_t y_ld,
+              int64_t rows, uint32_t dim, float eps, T* __restrict__ y, int64_t y_ld,
               float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   constexpr int BS = LPR > 256 ? LPR : 256;
   constexpr int RPB = BS / LPR;         // rows in flight per workgroup
@@ -91,7 +77,7 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
   float cnt = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int64_t left = dim - col_of<LPR, VEC>(j, l);
+    const int left = (int)dim - (int)col_of<LPR, VEC>(j, l);
     cnt += (float)(left >= VEC ? VEC : (left > 0 ? left : 0));
   }
   cnt = lane_sum<G>(cnt);
@@ -116,7 +102,7 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
     float m2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t left = dim - col_of<LPR, VEC>(j, l);
+      const int left = (int)dim - (int)col_of<LPR, VEC>(j, l);
       if (left >= VEC) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -187,14 +173,14 @@ constexpr int kMaxParts = 256;  // partial sums of the backward pass: a workgrou
 template <typename T, typename W, int VEC>
 __global__ __launch_bounds__(kLongBS)
 void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, const W* __restrict__ b,
-                   int64_t rows, int64_t dim, float eps, T* __restrict__ y, int64_t y_ld,
+                   int64_t rows, uint32_t dim, float eps, T* __restrict__ y, int64_t y_ld,
                    float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   __shared__ float lds[kLongBS / 64];
   const float inv_dim = 1.0f / (float)dim;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T* xr = x + row * x_ld;
     float s = 0.0f;
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
+    for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> p;
       load_cols<T, VEC>(p, xr, c, dim);
       float t = 0.0f;
@@ -204,7 +190,7 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
     }
     const float mean = block_sum<kLongBS>(s, lds) * inv_dim;
     float m2 = 0.0f;
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
+    for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> p;
       load_cols<T, VEC>(p, xr, c, dim);
       float t = 0.0f;
@@ -220,7 +206,7 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
     }
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
+    for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> p;
       Piece<W, VEC> wf, bf;
       float v[VEC];
@@ -242,8 +228,8 @@ template <typename T, typename W, int LPR, int NV, int VEC, int BS, bool NT>
 __global__ __launch_bounds__(BS)
 void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, int64_t x_ld,
               const W* __restrict__ w, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
-              int64_t rows, int64_t dim, T* __restrict__ dx, int64_t dx_ld, float* __restrict__ partials,
-              int64_t pitch) {
+              int64_t rows, uint32_t dim, T* __restrict__ dx, int64_t dx_ld, float* __restrict__ partials,
+              uint32_t pitch) {
   constexpr int RPB = BS / LPR;
   constexpr int NW = LPR / 64;
   constexpr int G = LPR < 64 ? LPR : 64;
@@ -347,7 +333,7 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
               k ? f32x4{db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]}
                 : f32x4{dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]};
       __syncthreads();
-      for (int c = threadIdx.x; c < COLS && c < dim; c += BS) {
+      for (uint32_t c = threadIdx.x; c < COLS && c < dim; c += BS) {
         float t = joined[c];
 #pragma unroll
         for (int g = 1; g < RPB; ++g) t += joined[g * COLS + c];
@@ -357,7 +343,7 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t c = col_of<LPR, VEC>(j, l);
+      const uint32_t c = col_of<LPR, VEC>(j, l);
       if (c < pitch) {  // pitch is a multiple of VEC
         store_piece<float, VEC>(pw + c, dw[j]);
         store_piece<float, VEC>(pw + pitch + c, db[j]);
@@ -371,14 +357,14 @@ template <typename T, typename W, int VEC>
 __global__ __launch_bounds__(kLongBS)
 void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, int64_t x_ld,
                    const W* __restrict__ w, const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
-                   int64_t rows, int64_t dim, T* __restrict__ dx, int64_t dx_ld) {
+                   int64_t rows, uint32_t dim, T* __restrict__ dx, int64_t dx_ld) {
   __shared__ float lds[kLongBS / 64];
   const float inv_dim = 1.0f / (float)dim;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T *xr = x + row * x_ld, *gr = dy + row * dy_ld;
     const float mean = mean_in[row], rstd = rstd_in[row];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
+    for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> px, pg;
       Piece<W, VEC> wf;
       float t1 = 0.0f, t2 = 0.0f;
@@ -395,7 +381,7 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
       s2 += t2;
     }
     const float a = block_sum<kLongBS>(s1, lds) * inv_dim, k = block_sum<kLongBS>(s2, lds) * inv_dim;
-    for (int64_t c = (int64_t)threadIdx.x * VEC; c < dim; c += (int64_t)kLongBS * VEC) {
+    for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> px, pg;
       Piece<W, VEC> wf;
       float v[VEC];
@@ -414,10 +400,10 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
 template <typename T, int VEC>
 __global__ __launch_bounds__(kThreads)
 void k_ln_cols(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, int64_t x_ld,
-               const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t rows, int64_t dim,
-               float* __restrict__ partials, int64_t pitch, int64_t tiles) {
+               const float* __restrict__ mean_in, const float* __restrict__ rstd_in, int64_t rows, uint32_t dim,
+               float* __restrict__ partials, uint32_t pitch, int64_t tiles) {
   const int64_t parts = gridDim.x / tiles, tile = blockIdx.x % tiles, g = blockIdx.x / tiles;
-  const int64_t c = (tile * kThreads + threadIdx.x) * VEC;
+  const uint32_t c = ((uint32_t)tile * kThreads + threadIdx.x) * VEC;
   float dw[VEC], db[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) dw[e] = db[e] = 0.0f;
@@ -433,7 +419,7 @@ void k_ln_cols(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x,
       db[e] += d;
     }
   }
-  float* pw = partials + 2 * g * pitch;
+  float* pw = partials + 2 * g * (int64_t)pitch;
   if (c < pitch) {
     store_piece<float, VEC>(pw + c, dw);
     store_piece<float, VEC>(pw + pitch + c, db);
@@ -492,7 +478,7 @@ constexpr int64_t kStreamBytes = 100000000;
 // more with 1280; 2048 were 1-2% faster there, but 14% slower for 8192 rows of
 // 768 fp32.
 constexpr int64_t kFwdSlots = 1024;
-constexpr int kVecBf16 = 8, kVecF32 = 4;
+constexpr int kVecBf16 = 8, kVecF32 = 4;  // elements of x in 16 bytes
 
 template <typename T, typename W, int VEC>
 void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int64_t dim, float eps, T* y,
@@ -504,7 +490,7 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
     const int64_t need = (rows + BS / LPR - 1) / (BS / LPR);
     const int64_t slots = kFwdSlots * 256 / BS, grid = need < slots ? need : slots;
     auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(BS), 0, s, x, x_ld, w, b, rows, dim, eps, y, y_ld, mean,
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(BS), 0, s, x, x_ld, w, b, rows, (uint32_t)dim, eps, y, y_ld, mean,
                          rstd);
     };
     if (nt) launch(k_ln_fwd<T, W, LPR, NV, VEC, true>);
@@ -531,7 +517,7 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
   else {
     const int64_t grid = rows < 2048 ? rows : 2048;
     hipLaunchKernelGGL((k_ln_fwd_long<T, W, VEC>), dim3((unsigned)grid), dim3(kLongBS), 0, s, x, x_ld, w, b, rows,
-                       dim, eps, y, y_ld, mean, rstd);
+                       (uint32_t)dim, eps, y, y_ld, mean, rstd);
   }
 }
 
@@ -594,7 +580,7 @@ hipError_t launch_layer_norm_forward(const void* x, int dtype, int64_t x_ld, con
     if (wdtype == ZS_BF16) run_fwd<uint16_t, uint16_t, kVecBf16>((const uint16_t*)x, x_ld, (const uint16_t*)w, (const uint16_t*)b, rows, dim, eps, (uint16_t*)y, y_ld, mean, rstd, s);
     else run_fwd<uint16_t, float, kVecBf16>((const uint16_t*)x, x_ld, (const float*)w, (const float*)b, rows, dim, eps, (uint16_t*)y, y_ld, mean, rstd, s);
   } else {
-    if (wdtype == ZS_BF16) run_fwd<float, uint16_t, kVecBf16>((const float*)x, x_ld, (const uint16_t*)w, (const uint16_t*)b, rows, dim, eps, (float*)y, y_ld, mean, rstd, s);
+    if (wdtype == ZS_BF16) run_fwd<float, uint16_t, kVecF32>((const float*)x, x_ld, (const uint16_t*)w, (const uint16_t*)b, rows, dim, eps, (float*)y, y_ld, mean, rstd, s);
     else run_fwd<float, float, kVecF32>((const float*)x, x_ld, (const float*)w, (const float*)b, rows, dim, eps, (float*)y, y_ld, mean, rstd, s);
   }
   return hipGetLastError();
@@ -613,7 +599,7 @@ hipError_t launch_layer_norm_backward(const void* dy, int64_t dy_ld, const void*
       if (wdtype == ZS_BF16) parts = run_bwd<uint16_t, uint16_t, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, p.pitch, s);
       else parts = run_bwd<uint16_t, float, kVecBf16>((const uint16_t*)dy, dy_ld, (const uint16_t*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (uint16_t*)dx, dx_ld, partials, p.pitch, s);
     } else {
-      if (wdtype == ZS_BF16) parts = run_bwd<float, uint16_t, kVecBf16>((const float*)dy, dy_ld, (const float*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, p.pitch, s);
+      if (wdtype == ZS_BF16) parts = run_bwd<float, uint16_t, kVecF32>((const float*)dy, dy_ld, (const float*)x, x_ld, (const uint16_t*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, p.pitch, s);
       else parts = run_bwd<float, float, kVecF32>((const float*)dy, dy_ld, (const float*)x, x_ld, (const float*)w, mean, rstd, rows, dim, (float*)dx, dx_ld, partials, p.pitch, s);
     }
     const hipError_t e = hipGetLastError();

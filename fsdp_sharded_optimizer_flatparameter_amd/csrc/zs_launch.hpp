@@ -169,7 +169,7 @@ struct EmbedPlan {
   int64_t pitch;     // fp32 values per partial row (dim rounded up to 8)
   int bits, passes;  // bits of a key, and digits of the sort
   int64_t tiles;     // tiles of the sort's passes
-  int64_t keys[2], pos[2], counts, totals, partials, bytes;
+  int64_t keys[2], pos[2], counts, totals, touched, partials, bytes;
 };
 EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim);
 

@@ -12,6 +12,7 @@
 namespace zs {
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at a 2-byte aligned address
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 // 16 bytes at any element-aligned address of global memory. (Not through ld_g:
 // a template parameter would drop the typedef's alignment.)
@@ -29,24 +30,37 @@ __device__ __forceinline__ void st16_nt(u32x4 v, void* p) {
   __builtin_nontemporal_store(v, (__attribute__((address_space(1))) u32x4_any*)p);
 }
 
-// VEC consecutive elements of a row as they lie in memory.
+// VEC consecutive elements of a row as they lie in memory: 8 bytes, or whole
+// 16-byte vectors.
 template <typename T, int VEC>
 struct Piece {
-  static constexpr int N = VEC * (int)sizeof(T) / 16;
-  static_assert(N >= 1 && N * 16 == VEC * (int)sizeof(T), "whole 16-byte vectors");
-  u32x4 r[N];
+  static constexpr int B = VEC * (int)sizeof(T);
+  static constexpr int N = B / 4;
+  static_assert(B == 8 || B % 16 == 0, "an access of 8 or 16 bytes");
+  uint32_t r[N];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < N; ++i) r[i] = 0u;
   }
+  template <bool NT = false>
   __device__ __forceinline__ void load(const T* p) {
+    if constexpr (B == 8) {
+      const auto q = (const __attribute__((address_space(1))) u32x2_any*)p;
+      const u32x2 v = NT ? __builtin_nontemporal_load(q) : *q;
+      r[0] = v.x;
+      r[1] = v.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = ld16(p + i * (16 / (int)sizeof(T)));
-  }
-  __device__ __forceinline__ void load_nt(const T* p) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = ld16_nt(p + i * (16 / (int)sizeof(T)));
+      for (int i = 0; i < N / 4; ++i) {
+        const T* q = p + i * (16 / (int)sizeof(T));
+        const u32x4 v = NT ? ld16_nt(q) : ld16(q);
+        r[4 * i] = v.x;
+        r[4 * i + 1] = v.y;
+        r[4 * i + 2] = v.z;
+        r[4 * i + 3] = v.w;
+      }
+    }
   }
   // the first n (below VEC) elements, zeros behind them
   __device__ __forceinline__ void load_part(const T* p, int n) {
@@ -61,23 +75,18 @@ struct Piece {
   __device__ __forceinline__ void stay_packed() {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w = r[i][k];
-          asm volatile("" : "+v"(w));
-          r[i][k] = w;
-        }
+      for (int i = 0; i < N; ++i) {
+        uint32_t w = r[i];
+        asm volatile("" : "+v"(w));
+        r[i] = w;
+      }
     }
   }
-  __device__ __forceinline__ void put(int e, float x) { r[e / 4][e % 4] = __float_as_uint(x); }
-  __device__ __forceinline__ void put(int e, uint16_t h) {
-    r[e / 8][(e % 8) / 2] |= (uint32_t)h << (16 * (e & 1));
-  }
+  __device__ __forceinline__ void put(int e, float x) { r[e] = __float_as_uint(x); }
+  __device__ __forceinline__ void put(int e, uint16_t h) { r[e / 2] |= (uint32_t)h << (16 * (e & 1)); }
   __device__ __forceinline__ float get(int e) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(r[e / 4][e % 4]);
-    const uint32_t w = r[e / 8][(e % 8) / 2];
-    return (e & 1) ? bf16_hi(w) : bf16_lo(w);
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[e]);
+    else return (e & 1) ? bf16_hi(r[e / 2]) : bf16_lo(r[e / 2]);
   }
 };
 
@@ -122,6 +131,27 @@ __device__ __forceinline__ void store_part(T* p, const float* v, int n) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e)
     if (e < n) st_g(round_to<T>(v[e]), p + e);
+}
+
+// The piece of a row at column c; what lies at or past `dim` is zero, or is not
+// written. Columns are 32-bit (dim stays below 2^27): with a row's address the
+// same for the whole wave, an access then takes it from scalar registers and
+// one register of offset, instead of two registers of address for each piece
+// that is on its way.
+template <typename T, int VEC, bool NT = false>
+__device__ __forceinline__ void load_cols(Piece<T, VEC>& p, const T* row, uint32_t c, uint32_t dim) {
+  if (c + VEC <= dim) {
+    p.template load<NT>(row + c);
+  } else if (c < dim) {
+    p.load_part(row + c, (int)(dim - c));
+  } else {
+    p.clear();
+  }
+}
+template <typename T, int VEC, bool NT = false>
+__device__ __forceinline__ void store_cols(T* row, const float* v, uint32_t c, uint32_t dim) {
+  if (c + VEC <= dim) store_piece<T, VEC, NT>(row + c, v);
+  else if (c < dim) store_part<T, VEC>(row + c, v, (int)(dim - c));
 }
 
 // Sum over the wave's lanes (G = 64) or over each aligned group of G lanes (16, 32),
