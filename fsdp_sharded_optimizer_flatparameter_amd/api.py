@@ -395,48 +395,54 @@ _INDEX_TYPES = {torch.int32: L.ZS_I32, torch.int64: L.ZS_I64}
 def _rows2d(t, name, dev):
     """(rows, dim, row stride) of a tensor whose last dimension is a row: two
     dimensions with any stride between rows, or contiguous with any number."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in _DTYPES:
+        shape = t.shape
+        if len(shape) == 2:
+            rows, dim = shape
+            ld, unit = t.stride()
+            if unit == 1 and ld >= dim:
+                return rows, dim, ld
+            if (unit == 1 or dim <= 1) and (ld >= dim or rows <= 1):
+                return rows, dim, max(ld, dim)
+            raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
+        if not shape or not t.is_contiguous():
+            raise ValueError(f"{name} must have two dimensions or be contiguous")
+        dim = shape[-1]
+        return (t.numel() // dim if dim else 0), dim, dim
+    _on_device(t, name, dev)
+    raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+
+
+def _on_device(t, name, dev):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device")
-    if t.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
-    shape = t.shape
-    if len(shape) == 2:
-        rows, dim = shape
-        ld, unit = t.stride()
-        if (unit == 1 or dim <= 1) and (ld >= dim or rows <= 1):
-            return rows, dim, ld if ld >= dim else dim
-        raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
-    if not shape or not t.is_contiguous():
-        raise ValueError(f"{name} must have two dimensions or be contiguous")
-    dim = shape[-1]
-    return (t.numel() // dim if dim else 0), dim, dim
 
 
 def _ids(t, name, n, dev):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous device tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
-    if t.dtype not in _INDEX_TYPES:
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()):
+        _on_device(t, name, dev)
+        raise ValueError(f"{name} must be contiguous")
+    itype = _INDEX_TYPES.get(t.dtype)
+    if itype is None:
         raise ValueError(f"{name} must be int32 or int64, got {t.dtype}")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-    return _INDEX_TYPES[t.dtype]
+    return itype
 
 
 def _vector(t, name, n, dev, dtype=None):
     """Pointer of an optional contiguous vector of n elements on device `dev`."""
     if t is None:
         return None
-    _dev(t, name, dtype)
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()):
+        _on_device(t, name, dev)
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     return t.data_ptr()
@@ -448,11 +454,27 @@ def _device_index(t, name):
     return t.get_device()
 
 
+def _workspace(ws, dev):
+    if ws is None:
+        return None, 0
+    if not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
+        _on_device(ws, "workspace", dev)
+        raise ValueError("workspace must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+# The current stream's handle without a Stream object around it (1.1 us of a
+# call of 6) where this torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(name, dev, stream, *args):
     """One library call with device `dev` current: the null stream is the current device's."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError("the stream is another device's")
         stream = stream.cuda_stream
     fn = getattr(_lib(), name)
     if torch.cuda.current_device() == dev:
@@ -491,15 +513,6 @@ def zs_embed_forward(table, tokens, out, *, scale=1.0, pos_table=None, positions
 
 def zs_embed_workspace_bytes(n: int, vocab: int, dim: int) -> int:
     return int(_lib().zs_embed_workspace_bytes(int(n), int(vocab), int(dim)))
-
-
-def _workspace(ws, dev):
-    if ws is None:
-        return None, 0
-    _dev(ws, "workspace")
-    if ws.get_device() != dev:
-        raise ValueError("workspace is on another device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=False, workspace, stream=None):

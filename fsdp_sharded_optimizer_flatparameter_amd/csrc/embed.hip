@@ -23,9 +23,8 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int index_type, int64_
 }
 
 // The calling wave's number in the grid, in a scalar register.
-template <int BS = kThreads>
 __device__ __forceinline__ int64_t wave_id() {
-  return (int64_t)blockIdx.x * (BS / 64) + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  return (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
 }
 // a / b for a below 2^32 in 32 bits, where the hardware has no 64-bit divide
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
@@ -34,18 +33,18 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
 
 // ---------------------------------------------------------------- forward
 
-// One wave copies one tile of 64 U pieces of a row.
-#ifndef EBS
-#define EBS 256
-#endif
-template <typename T, typename O, int VEC, int U, bool NT>
-__global__ __launch_bounds__(EBS)
+// One wave copies one tile of 64 U pieces of a row. Bound by memory: 16384 rows
+// of 4096 bf16, drawn as a text's tokens are (191 MB), take 34 us. The output
+// is stored past the caches: 41 us with plain stores, and 9.3 against 9.9 for
+// 8192 rows of 768 with their positions.
+template <typename T, typename O, int VEC, int U>
+__global__ __launch_bounds__(kThreads)
 void k_embed_fwd(const T* __restrict__ table, int64_t vocab, uint32_t dim, int64_t table_ld,
                  const T* __restrict__ pos_table, int64_t pos_rows, int64_t pos_ld, const void* __restrict__ tokens,
                  const void* __restrict__ positions, int index_type, int64_t total, int64_t tiles, float scale,
                  O* __restrict__ out, int64_t out_ld) {
   const int lane = threadIdx.x & 63;
-  for (int64_t t = wave_id<EBS>(); t < total; t += (int64_t)gridDim.x * (EBS / 64)) {
+  for (int64_t t = wave_id(); t < total; t += (int64_t)gridDim.x * (kThreads / 64)) {
     const int64_t i = quot(t, tiles);
     const uint32_t c0 = (uint32_t)(t - i * tiles) * (64 * U * VEC) + lane * VEC;
     const int64_t id = id_at(tokens, index_type, i);
@@ -73,25 +72,72 @@ void k_embed_fwd(const T* __restrict__ table, int64_t vocab, uint32_t dim, int64
       float v[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = with_pos ? fmaf(a[u].get(e), scale, p[u].get(e)) : a[u].get(e) * scale;
-      store_cols<O, VEC, NT>(orow, v, c0 + u * 64 * VEC, dim);
+      store_cols<O, VEC, true>(orow, v, c0 + u * 64 * VEC, dim);
     }
   }
 }
 
+// ---------------------------------------------------------------- zeros
+
+// Stores past the caches from one-wave workgroups with a short piece each keep
+// the most writes on their way: the call that writes 128256 x 4096 bf16 takes
+// 233 us so, 248 with pieces of 8 KiB, 253 with 16 KiB, 240 with 2 KiB, and 250
+// with four-wave workgroups or plain stores.
+constexpr int64_t kFillBytes = 4096;
+// Up to this much of a gradient is zeroed by the first launch of the sort,
+// into all rows, beside the workgroups that sort; above it, after the sort, into the
+// rows that no token selects. 8192 tokens into 8192 x 1024 fp32 (34 MB): 29.3
+// against 31.6 us; 32000 x 1024 (131 MB): 43 against 47; 512 tokens into
+// 128256 x 4096 bf16 (1.05 GB): 210 against 187.
+constexpr int64_t kFillTogether = 200000000;
+
+// With `first` the rows that no token selects are zero. The table is cut into
+// pieces of about kFillBytes, a wave for each: `step` (up to 64) narrow rows,
+// or a part of a wide one.
+template <typename Gt>
+struct Fill {
+  Gt* grad;
+  int64_t vocab, ld;
+  uint32_t dim, width;  // columns of a piece
+  int step, across;     // rows of a piece, pieces across a row
+  int64_t total;        // pieces
+};
+template <typename Gt>
+Fill<Gt> fill_plan(Gt* grad, int64_t vocab, int64_t dim, int64_t ld) {
+  const int64_t row = dim * (int64_t)sizeof(Gt), fit = kFillBytes / row;
+  Fill<Gt> f{grad, vocab, ld, (uint32_t)dim, (uint32_t)dim, (int)(fit < 1 ? 1 : fit > 64 ? 64 : fit),
+             (int)((row + kFillBytes - 1) / kFillBytes), 0};
+  if (f.across > 1) f.width = kFillBytes / sizeof(Gt);
+  f.total = (vocab + f.step - 1) / f.step * f.across;
+  return f;
+}
+// Piece t, without the rows that `touched` marks (none are where it is null).
+template <typename Gt>
+__device__ __forceinline__ void fill_piece(const Fill<Gt>& f, int64_t t, const uint8_t* touched) {
+  constexpr uint32_t VEC = 16 / sizeof(Gt);
+  const int lane = threadIdx.x & 63;
+  const int64_t g = quot(t, f.across), r0 = g * f.step, row = r0 + lane;
+  const uint32_t c0 = (uint32_t)(t - g * f.across) * f.width, c1 = c0 + f.width < f.dim ? c0 + f.width : f.dim;
+  for (uint64_t empty = __ballot(lane < f.step && row < f.vocab && !(touched && touched[row])); empty;
+       empty &= empty - 1) {
+    Gt* out = f.grad + (r0 + __builtin_ctzll(empty)) * f.ld;
+    for (uint32_t c = c0 + lane * VEC; c < c1; c += 64 * VEC) {
+      if (c + VEC <= c1) st16_nt(u32x4{0u, 0u, 0u, 0u}, out + c);
+      else
+        for (uint32_t k = c; k < c1; ++k) st_g((Gt)0, out + k);
+    }
+  }
+}
+
+// One-wave workgroups, a piece each.
+template <typename Gt>
+__global__ __launch_bounds__(64)
+void k_embed_fill(Fill<Gt> f, const uint8_t* __restrict__ touched) {
+  for (int64_t t = blockIdx.x; t < f.total; t += gridDim.x) fill_piece(f, t, touched);
+}
+
 // ---------------------------------------------------------------- sort
 
-#ifndef EU
-#define EU 2
-#endif
-#ifndef ENT
-#define ENT -1
-#endif
-#ifndef FILLB
-#define FILLB 4096
-#endif
-#ifndef KW
-#define KW 8192
-#endif
 
 // Radix sort of (key, position) by digits of kBits bits, lowest first, each pass
 // stable. The key of a token that gets no gradient (outside
@@ -261,23 +307,19 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
 // digits of all entries itself (they lie in L2), those of the tiles before its
 // own apart, and then places its own tile, an entry per thread. Counting by
 // tiles in a launch of its own, their sums in a second and the placing in a
-// third (k_sort_count, k_sort_scan, k_sort_scatter) takes SORT_FIGURES.
+// third (k_sort_count, k_sort_scan, k_sort_scatter) takes 12 us a pass at any
+// of these sizes, this 5 us for 8192 entries and 10 for 32768; for 65536 it
+// takes 25 (32768 x 1024: 66 us with either way in the whole call).
 // The first pass clears `touched`, a byte per row of the gradient, with the
 // workgroups behind the tiles; the last one sets it for each token's row.
 constexpr int kPassBS = 1024;
 constexpr int kPassWaves = kPassBS / 64;
-#ifndef PSORT
-#define PSORT 32768
-#endif
-constexpr int64_t kPassSort = PSORT;
+constexpr int64_t kPassSort = 32768;
 // Copies of the counters, each for every kCopies-th lane and shifted by a bank:
 // frequent tokens have several lanes of a wave count in one place, one after
 // the other. A counter holds the entries before the tile in its lower half and
 // all in its upper half: a copy sees at most kPassSort / kCopies of them.
-#ifndef COPIES
-#define COPIES 8
-#endif
-constexpr int kCopies = COPIES;
+constexpr int kCopies = 8;
 static_assert(kPassSort / kCopies < 65536, "16 bits hold a count");
 constexpr int kClearBytes = kPassBS * 16;  // of `touched`, per workgroup
 
@@ -286,15 +328,20 @@ __device__ __forceinline__ void clear_touched(uint8_t* touched, int64_t vocab, i
   if (i < vocab) st16(u32x4{0u, 0u, 0u, 0u}, touched + i);  // the array's room is a multiple of 16
 }
 
+template <typename Gt>
 __global__ __launch_bounds__(kPassBS)
 void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int tiles, int last,
-                 uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched) {
+                 uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched,
+                 Fill<Gt> fill) {
   __shared__ uint32_t counts[kCopies][kBins + 1];
   __shared__ uint32_t hist[kPassWaves][kBins];
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= tiles) {
-    clear_touched(touched, k.vocab, blockIdx.x - tiles);
+    const int64_t b = (int)blockIdx.x - tiles, nb = (int)gridDim.x - tiles;
+    if (touched) clear_touched(touched, k.vocab, b);
+    else
+      for (int64_t t = b * kPassWaves + wave; t < fill.total; t += nb * kPassWaves) fill_piece(fill, t, nullptr);
     return;
   }
   auto digit = [&](uint32_t key) { return (key >> shift) & (kBins - 1); };
@@ -357,12 +404,19 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
 
 // Up to 1024 entries: all passes in one launch of one workgroup, an entry per
 // thread, keys and positions handed on in LDS.
+template <typename Gt>
 __global__ __launch_bounds__(kPassBS)
-void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out) {
+void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+                Fill<Gt> fill) {
   __shared__ uint32_t hist[kPassWaves][kBins];
   __shared__ uint32_t skey[kPassBS], spos[kPassBS];
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
+  if (blockIdx.x > 0) {
+    for (int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave; t < fill.total; t += (int64_t)(gridDim.x - 1) * kPassWaves)
+      fill_piece(fill, t, nullptr);
+    return;
+  }
   uint32_t key = i < n ? k.at(i) : 0, pos = i;
   for (int p = 0; p < passes; ++p) {
 #pragma unroll
@@ -407,6 +461,15 @@ void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint
 
 // ---------------------------------------------------------------- gradient
 
+// dout of more bytes than this is read past the caches: 65536 rows of 768 bf16
+// (101 MB) 74 instead of 86 us for the call, 32768 of 1024 (67 MB) 61 instead of
+// 65; 16384 of 768 (25 MB), which the caches can hold, 37.3 instead of 35.8.
+constexpr int64_t kStreamBytes = 60000000;
+// Entries per wave are doubled from 4 up to 16 while there are more waves than
+// this: 4 for all costs 243 instead of 202 us with 131072 tokens, whose partial
+// sums then weigh; fewer waves leave compute units without work.
+constexpr int64_t kChunkWaves = 8192;
+
 // The sorted entries are cut into chunks of kWaves K: a workgroup takes one chunk
 // and 64 pieces of columns, each of its waves K entries. A wave adds its rows
 // in registers and writes the gradient of each token whose run of entries ends
@@ -415,44 +478,7 @@ void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint
 // in order; one that comes from the chunk before, or goes on behind the chunk,
 // leaves one partial sum in the workspace (rows 2c and 2c + 1 of chunk c),
 // joined by k_embed_join.
-#ifndef KWV
-#define KWV 8
-#endif
-constexpr int kWaves = KWV;
-
-// Zeros into the rows that no token selects (all of them without `touched`):
-// `step` (up to 64) consecutive rows per workgroup, whose marks are read at
-// once, a wave for a row.
-#ifndef NOFNT
-#define FST st16_nt
-#else
-#define FST st16
-#endif
-#ifndef FBS
-#define FBS 64
-#endif
-template <typename Gt>
-__global__ __launch_bounds__(FBS)
-void k_embed_fill(const uint8_t* __restrict__ touched, int64_t vocab, uint32_t dim, int64_t total, int step,
-                  int pieces, uint32_t width, Gt* __restrict__ grad, int64_t ld) {
-  constexpr uint32_t VEC = 16 / sizeof(Gt);
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
-    const int64_t g = quot(t, pieces), r0 = g * step, row = r0 + lane;
-    const uint32_t c0 = (uint32_t)(t - g * pieces) * width, c1 = c0 + width < dim ? c0 + width : dim;
-    uint64_t empty = __ballot(lane < step && row < vocab && !(touched && touched[row]));
-    for (int j = 0; empty; empty &= empty - 1, ++j) {
-      if (FBS > 64 && j % (FBS / 64) != wave) continue;
-      Gt* out = grad + (r0 + __builtin_ctzll(empty)) * ld;
-      for (uint32_t c = c0 + lane * VEC; c < c1; c += 64 * VEC) {
-        if (c + VEC <= c1) FST(u32x4{0u, 0u, 0u, 0u}, out + c);
-        else
-          for (uint32_t k = c; k < c1; ++k) st_g((Gt)0, out + k);
-      }
-    }
-  }
-}
+constexpr int kWaves = 8;
 
 template <typename Gt, int VEC>
 __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale, bool add, const Piece<Gt, VEC>& old,
@@ -463,20 +489,14 @@ __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale,
   store_cols<Gt, VEC>(row, v, c, dim);
 }
 
-#ifndef W1
-#define W1 4
-#endif
-#ifndef W0
-#define W0 4
-#endif
-template <typename T, typename Gt, int VEC, int K, bool FIRST>
-__global__ __launch_bounds__(kWaves * 64, FIRST ? W1 : W0)
+template <typename T, typename Gt, int VEC, int K, bool FIRST, bool NT>
+__global__ __launch_bounds__(kWaves * 64)
 void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, uint32_t vocab,
                     int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, uint32_t dim,
                     float scale, Gt* __restrict__ grad, int64_t grad_ld, float* __restrict__ partials,
                     uint32_t pitch) {
   // rows on their way at once; with them go the gradient's old rows
-  constexpr int U = K < 8 || sizeof(T) * VEC > 16 ? 4 : 8;
+    constexpr int U = K < 8 || sizeof(T) * VEC > 16 ? 4 : 8;
   static_assert(K + 2 <= 64 && K % U == 0, "a lane for each entry and its two neighbours");
   __shared__ __align__(16) float heads[kWaves][64 * VEC];
   __shared__ int through[kWaves];
@@ -513,7 +533,7 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
       for (int u = 0; u < U; ++u) {
         const int at = u0 + u < cnt ? u0 + u : cnt - 1;  // clamped: the last one again
         const int64_t row = (uint32_t)__builtin_amdgcn_readlane((int)pp, at + 1);
-        load_cols<T, VEC>(v[u], dout + row * dout_ld, c, dim);
+        load_cols<T, VEC, NT>(v[u], dout + row * dout_ld, c, dim);
         if (!FIRST) {
           if (key_at(at + 1) != key_at(at)) load_cols<Gt, VEC>(old[u], grad + (int64_t)key_at(at) * grad_ld, c, dim);
           else old[u].clear();
@@ -630,7 +650,7 @@ void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, 
 
 // Elements of a lane's piece: 16 bytes of what is written, so that a wave's
 // store covers whole lines. (16384 rows of 4096 bf16 into fp32, 8 elements a
-// lane: two stores with gaps took 71 us, 99 past the caches; 4: VEC_FIGURES.)
+// lane: two stores with gaps took 71 us, 99 past the caches; 4: 50.)
 template <typename O>
 constexpr int vec_of() { return 16 / sizeof(O); }
 
@@ -639,21 +659,16 @@ void run_embed_fwd(const T* table, int64_t vocab, int64_t dim, int64_t table_ld,
                    int64_t pos_ld, const void* tokens, const void* positions, int index_type, int64_t n, float scale,
                    O* out, int64_t out_ld, hipStream_t s) {
   constexpr int VEC = vec_of<O>();
-  const bool nt = n * dim * (int64_t)sizeof(O) > ENT;
   auto go = [&](auto uu) {
     constexpr int U = decltype(uu)::value;
     const int64_t tiles = (dim + 64 * U * VEC - 1) / (64 * U * VEC), total = n * tiles;
-    auto launch = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(total, EBS / 64, EBS)), dim3(EBS), 0, s, table, vocab,
-                         (uint32_t)dim, table_ld, pos_table, pos_rows, pos_ld, tokens, positions, index_type, total,
-                         tiles, scale, out, out_ld);
-    };
-    if (nt) launch(k_embed_fwd<T, O, VEC, U, true>);
-    else launch(k_embed_fwd<T, O, VEC, U, false>);
+    hipLaunchKernelGGL((k_embed_fwd<T, O, VEC, U>), dim3((unsigned)grid_for(total, kThreads / 64)), dim3(kThreads), 0,
+                       s, table, vocab, (uint32_t)dim, table_ld, pos_table, pos_rows, pos_ld, tokens, positions,
+                       index_type, total, tiles, scale, out, out_ld);
   };
-  const int64_t pieces = (dim + 64 * VEC - 1) / (64 * VEC);
-  if (pieces < EU) go(std::integral_constant<int, 1>{});
-  else go(std::integral_constant<int, EU>{});
+  // Two pieces a lane: 65 us for 16384 rows of 8192 bf16 (one: 80, four: 70).
+  if (dim <= 64 * VEC) go(std::integral_constant<int, 1>{});
+  else go(std::integral_constant<int, 2>{});
 }
 
 template <typename T, typename Gt>
@@ -662,42 +677,39 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
                    int64_t vocab, int64_t dim, float scale, Gt* grad, int64_t grad_ld, bool first, hipStream_t s) {
   constexpr int VEC = vec_of<Gt>();
   int last = 0;
-  // Which rows a token selects is marked for the fill, except where few tokens
-  // leave few rows to spare it. The first pass clears the marks, the last one
-  // sets them.
-  uint8_t* mark = first && n > kPassBS ? touched : nullptr;
+  // In a launch of their own the zeros go by marks of the rows that tokens
+  // select, which the first pass clears and the last one sets.
+  const Fill<Gt> fill = fill_plan(grad, vocab, dim, grad_ld);
+  const bool together = first && n > 0 && n <= kPassSort && vocab * dim * (int64_t)sizeof(Gt) <= kFillTogether;
+  const int64_t fill_groups = together ? (fill.total + kPassWaves - 1) / kPassWaves : 0;
+  uint8_t* mark = first && n > 0 && !together ? touched : nullptr;
   const int passes = mark && p.passes < 2 ? 2 : p.passes;
-  if (n > 0 && n <= kPassBS)
-    hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kPassBS), 0, s, tokens, (int)n, passes, keys[0], pos[0]);
-  for (int i = 0; n > kPassBS && i < passes; ++i) {
-    const int src = (i + 1) & 1, dst = i & 1;
-    Keys k = tokens;
-    if (i) k.keys = keys[src];
-    const uint32_t* pos_in = i ? pos[src] : nullptr;
-    const bool final = i + 1 == passes;
-    if (n <= kPassSort) {
-      const int tiles = (int)((n + kPassBS - 1) / kPassBS);
-      const int clears = i == 0 && mark ? (int)((vocab + kClearBytes - 1) / kClearBytes) : 0;
-      hipLaunchKernelGGL(k_sort_pass, dim3((unsigned)(tiles + clears)), dim3(kPassBS), 0, s, k, pos_in, (int)n,
-                         i * kBits, tiles, (int)final, keys[dst], pos[dst], mark);
-    } else {
-      const dim3 gd((unsigned)grid_for(p.tiles, 1)), bd(kThreads);
-      hipLaunchKernelGGL(k_sort_count, gd, bd, 0, s, k, n, i * kBits, p.tiles, counts, i == 0 ? mark : nullptr);
-      hipLaunchKernelGGL(k_sort_scan, dim3(kBins), bd, 0, s, counts, p.tiles, totals);
-      hipLaunchKernelGGL(k_sort_scatter, gd, bd, 0, s, k, pos_in, n, i * kBits, p.tiles, counts, totals, keys[dst],
-                         pos[dst], final ? mark : nullptr);
+  if (n > 0 && n <= kPassBS && !mark)
+    hipLaunchKernelGGL((k_sort_one<Gt>), dim3((unsigned)grid_for(1 + fill_groups, 1, kPassBS)), dim3(kPassBS), 0, s,
+                       tokens, (int)n, passes, keys[0], pos[0], fill);
+  else
+    for (int i = 0; n > 0 && i < passes; ++i) {
+      const int src = (i + 1) & 1, dst = i & 1;
+      Keys k = tokens;
+      if (i) k.keys = keys[src];
+      const uint32_t* pos_in = i ? pos[src] : nullptr;
+      const bool final = i + 1 == passes;
+      if (n <= kPassSort) {
+        const int tiles = (int)((n + kPassBS - 1) / kPassBS);
+        const int64_t more = i > 0 ? 0 : mark ? (vocab + kClearBytes - 1) / kClearBytes : fill_groups;
+        hipLaunchKernelGGL((k_sort_pass<Gt>), dim3((unsigned)grid_for(tiles + more, 1, kPassBS)), dim3(kPassBS), 0, s,
+                           k, pos_in, (int)n, i * kBits, tiles, (int)final, keys[dst], pos[dst], mark, fill);
+      } else {
+        const dim3 gd((unsigned)grid_for(p.tiles, 1)), bd(kThreads);
+        hipLaunchKernelGGL(k_sort_count, gd, bd, 0, s, k, n, i * kBits, p.tiles, counts, i == 0 ? mark : nullptr);
+        hipLaunchKernelGGL(k_sort_scan, dim3(kBins), bd, 0, s, counts, p.tiles, totals);
+        hipLaunchKernelGGL(k_sort_scatter, gd, bd, 0, s, k, pos_in, n, i * kBits, p.tiles, counts, totals, keys[dst],
+                           pos[dst], final ? mark : nullptr);
+      }
+      last = dst;
     }
-    last = dst;
-  }
-  if (first) {
-    const int64_t row_bytes = dim * (int64_t)sizeof(Gt), fit = FILLB / row_bytes;
-    const int step = (int)(fit < 1 ? 1 : fit > 64 ? 64 : fit);
-    const int pieces = (int)((row_bytes + FILLB - 1) / FILLB);
-    const uint32_t width = pieces == 1 ? (uint32_t)dim : FILLB / sizeof(Gt);
-    const int64_t total = (vocab + step - 1) / step * pieces;
-    hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(total, 1, FBS)), dim3(FBS), 0, s,
-                       mark, vocab, (uint32_t)dim, total, step, pieces, width, grad, grad_ld);
-  }
+  if (first && !together)
+    hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(fill.total, 1, 64)), dim3(64), 0, s, fill, mark);
   if (n == 0) return;
   const int64_t coltiles = (dim + 64 * VEC - 1) / (64 * VEC), items = p.chunks * coltiles;
   auto go = [&](auto kernel) {
@@ -707,9 +719,10 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   };
   auto pick = [&](auto f) {
     constexpr bool F = decltype(f)::value;
-    if (p.chunk == 4 * kWaves) go(k_embed_chunks<T, Gt, VEC, 4, F>);
-    else if (p.chunk == 8 * kWaves) go(k_embed_chunks<T, Gt, VEC, 8, F>);
-    else go(k_embed_chunks<T, Gt, VEC, 16, F>);
+    if (p.chunk == 4 * kWaves) go(k_embed_chunks<T, Gt, VEC, 4, F, false>);
+    else if (p.chunk == 8 * kWaves) go(k_embed_chunks<T, Gt, VEC, 8, F, false>);
+    else if (n * dim * (int64_t)sizeof(T) <= kStreamBytes) go(k_embed_chunks<T, Gt, VEC, 16, F, false>);
+    else go(k_embed_chunks<T, Gt, VEC, 16, F, true>);
   };
   if (first) pick(std::true_type{});
   else pick(std::false_type{});
@@ -726,7 +739,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
   p.pitch = (dim + 7) / 8 * 8;
   const int64_t coltiles = (dim + 511) / 512;
   int k = 4;  // entries per wave
-  while (k < 16 && n / k * coltiles > KW) k *= 2;
+  while (k < 16 && n / k * coltiles > kChunkWaves) k *= 2;
   p.chunk = k * kWaves;
   p.chunks = (n + p.chunk - 1) / p.chunk;
   p.bits = 1;  // keys are 0 .. vocab
