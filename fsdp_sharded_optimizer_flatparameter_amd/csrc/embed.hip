@@ -139,10 +139,13 @@ void k_embed_fill(Fill<Gt> f, const uint8_t* __restrict__ touched) {
 // ---------------------------------------------------------------- sort
 
 
-// Radix sort of (key, position) by digits of kBits bits, lowest first, each pass
-// stable. The key of a token that gets no gradient (outside
+// Radix sort of (key, position) by digits of up to kBits bits, lowest first, each
+// pass stable. The key of a token that gets no gradient (outside
 // of the vocabulary, or the padding token) is `vocab`, behind all others.
 constexpr int kBits = 9;
+// In the passes of up to kPassSort entries also of up to kWideBits, where that
+// saves a pass: position tables of up to 2047 rows, small vocabularies.
+constexpr int kWideBits = 11;
 constexpr int kBins = 1 << kBits;
 constexpr int kSortRounds = 8;
 constexpr int kSortTile = kThreads * kSortRounds;  // entries per workgroup and pass
@@ -226,10 +229,12 @@ void k_sort_scan(uint32_t* __restrict__ counts, int64_t tiles, uint32_t* __restr
 
 // Lanes before this one, among those with live set, that hold the same digit;
 // *same gets all that do. A lane that is not live gets nothing of use.
-__device__ __forceinline__ uint32_t rank_in_wave(uint32_t d, bool live, uint64_t* same) {
+template <int MAXB>
+__device__ __forceinline__ uint32_t rank_in_wave(uint32_t d, int bits, bool live, uint64_t* same) {
   uint64_t s = __ballot(live);
 #pragma unroll
-  for (int b = 0; b < kBits; ++b) {
+  for (int b = 0; b < MAXB; ++b) {
+    if (b >= bits) break;
     const bool one = (d >> b) & 1u;
     const uint64_t m = __ballot(one);
     s &= one ? m : ~m;
@@ -241,7 +246,7 @@ __device__ __forceinline__ uint32_t rank_in_wave(uint32_t d, bool live, uint64_t
 // The same over several rounds: `h` is the wave's own running count per digit.
 __device__ __forceinline__ uint32_t wave_rank(uint32_t d, bool live, uint32_t* h) {
   uint64_t same;
-  const uint32_t rank = rank_in_wave(d, live, &same);
+  const uint32_t rank = rank_in_wave<kBits>(d, kBits, live, &same);
   const int leader = same ? __builtin_ctzll(same) : 0;
   uint32_t before = 0;
   if (live && rank == 0) before = atomicAdd(&h[d], (uint32_t)__popcll(same));
@@ -315,12 +320,6 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
 constexpr int kPassBS = 1024;
 constexpr int kPassWaves = kPassBS / 64;
 constexpr int64_t kPassSort = 32768;
-// Copies of the counters, each for every kCopies-th lane and shifted by a bank:
-// frequent tokens have several lanes of a wave count in one place, one after
-// the other. A counter holds the entries before the tile in its lower half and
-// all in its upper half: a copy sees at most kPassSort / kCopies of them.
-constexpr int kCopies = 8;
-static_assert(kPassSort / kCopies < 65536, "16 bits hold a count");
 constexpr int kClearBytes = kPassBS * 16;  // of `touched`, per workgroup
 
 __device__ __forceinline__ void clear_touched(uint8_t* touched, int64_t vocab, int64_t block) {
@@ -328,13 +327,48 @@ __device__ __forceinline__ void clear_touched(uint8_t* touched, int64_t vocab, i
   if (i < vocab) st16(u32x4{0u, 0u, 0u, 0u}, touched + i);  // the array's room is a multiple of 16
 }
 
-template <typename Gt>
+// Start of each wave's entries of each digit: hist holds the waves' counts and
+// gets the places, `sum` are the thread's digits' entries in the whole list and
+// `mine` those before the tile. Digits t and t + kPassBS belong to thread t.
+template <int BINS>
+__device__ __forceinline__ void place_digits(uint16_t (*hist)[BINS], int bins, const uint32_t* sum,
+                                             const uint32_t* mine, uint32_t* lds) {
+  constexpr int D = BINS > kPassBS ? BINS / kPassBS : 1;
+  uint32_t start = 0;
+#pragma unroll
+  for (int q = 0; q < D; ++q) {
+    const int b = q * kPassBS + threadIdx.x;
+    uint32_t all;
+    uint32_t at = start + block_scan<kPassBS>(sum[q], lds, &all) + mine[q];
+    start += all;
+    if (b < bins) {
+      uint32_t c[kPassWaves];
+#pragma unroll
+      for (int w = 0; w < kPassWaves; ++w) c[w] = hist[w][b];
+#pragma unroll
+      for (int w = 0; w < kPassWaves; ++w) {
+        hist[w][b] = (uint16_t)at;  // places stay below 2^15
+        at += c[w];
+      }
+    }
+  }
+}
+
+template <typename Gt, int MAXB>
 __global__ __launch_bounds__(kPassBS)
-void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int tiles, int last,
+void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int bits, int tiles, int last,
                  uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched,
                  Fill<Gt> fill) {
-  __shared__ uint32_t counts[kCopies][kBins + 1];
-  __shared__ uint32_t hist[kPassWaves][kBins];
+  // Copies of the counters, each for every so many-th lane and shifted by a
+  // bank: frequent tokens have several lanes of a wave count in one place, one
+  // after the other (16384 entries: 37.5 us for the call with 8 copies, 42 with
+  // one). A counter holds the entries before the tile in its lower half and all
+  // in its upper half.
+  constexpr int BINS = 1 << MAXB, ROOM = 4096 + 8;
+  constexpr int D = BINS > kPassBS ? BINS / kPassBS : 1;
+  static_assert(kPassSort < 65536, "16 bits hold a count and a place");
+  __shared__ uint32_t counts[ROOM];
+  __shared__ uint16_t hist[kPassWaves][BINS];
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= tiles) {
@@ -344,7 +378,8 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
       for (int64_t t = b * kPassWaves + wave; t < fill.total; t += nb * kPassWaves) fill_piece(fill, t, nullptr);
     return;
   }
-  auto digit = [&](uint32_t key) { return (key >> shift) & (kBins - 1); };
+  const int bins = 1 << bits, copies = bins <= 512 ? 8 : 4096 / bins;
+  auto digit = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
   const int tile0 = blockIdx.x * kPassBS, i = tile0 + threadIdx.x;
   constexpr int U = 8;  // entries on their way per thread
   uint32_t kk[U];
@@ -355,44 +390,37 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
   fetch(threadIdx.x);
   const uint32_t key = i < n ? k.at(i) : 0;
   const uint32_t pos = i < n ? (pos_in ? pos_in[i] : (uint32_t)i) : 0;
-  for (int b = threadIdx.x; b < kCopies * (kBins + 1); b += kPassBS) (&counts[0][0])[b] = 0;
-#pragma unroll
-  for (int b = 0; b < kBins / 64; ++b) hist[wave][b * 64 + lane] = 0;
+  for (int b = threadIdx.x; b < copies * (bins + 1); b += kPassBS) counts[b] = 0;
+  for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
   __syncthreads();
+  uint32_t* own = counts + (lane & (copies - 1)) * (bins + 1);
   for (int j0 = threadIdx.x; j0 < n; j0 += U * kPassBS) {
     if (j0 != (int)threadIdx.x) fetch(j0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * kPassBS;
-      if (j < n) atomicAdd(&counts[lane % kCopies][digit(kk[u])], j < tile0 ? 0x10001u : 0x10000u);
+      if (j < n) atomicAdd(&own[digit(kk[u])], j < tile0 ? 0x10001u : 0x10000u);
     }
   }
   // rank within the wave, and the wave's count of each digit
   const uint32_t d = digit(key);
   uint64_t same;
-  const uint32_t rank = rank_in_wave(d, i < n, &same);
-  if (i < n && rank == 0) hist[wave][d] = (uint32_t)__popcll(same);
+  const uint32_t rank = rank_in_wave<MAXB>(d, bits, i < n, &same);
+  if (i < n && rank == 0) hist[wave][d] = (uint16_t)__popcll(same);
   __syncthreads();
-  uint32_t sum = 0, mine = 0;
-  if (threadIdx.x < kBins) {
+  uint32_t sum[D], mine[D];
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) {
-      mine += counts[c][threadIdx.x] & 0xffffu;
-      sum += counts[c][threadIdx.x] >> 16;
-    }
+  for (int q = 0; q < D; ++q) {
+    sum[q] = mine[q] = 0;
+    const int b = q * kPassBS + threadIdx.x;
+    if (b < bins)
+      for (int c = 0; c < copies; ++c) {
+        const uint32_t v = counts[c * (bins + 1) + b];
+        mine[q] += v & 0xffffu;
+        sum[q] += v >> 16;
+      }
   }
-  uint32_t all;
-  uint32_t at = block_scan<kPassBS>(sum, lds, &all) + mine;
-  if (threadIdx.x < kBins) {
-    uint32_t c[kPassWaves];
-#pragma unroll
-    for (int w = 0; w < kPassWaves; ++w) c[w] = hist[w][threadIdx.x];
-#pragma unroll
-    for (int w = 0; w < kPassWaves; ++w) {
-      hist[w][threadIdx.x] = at;
-      at += c[w];
-    }
-  }
+  place_digits<BINS>(hist, bins, sum, mine, lds);
   __syncthreads();
   if (i < n) {
     const uint32_t to = hist[wave][d] + rank;
@@ -403,12 +431,15 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
 }
 
 // Up to 1024 entries: all passes in one launch of one workgroup, an entry per
-// thread, keys and positions handed on in LDS.
-template <typename Gt>
+// thread, keys and positions handed on in LDS. (512 tokens: 12.0 us for the
+// call instead of 15.)
+template <typename Gt, int MAXB>
 __global__ __launch_bounds__(kPassBS)
-void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
                 Fill<Gt> fill) {
-  __shared__ uint32_t hist[kPassWaves][kBins];
+  constexpr int BINS = 1 << MAXB;
+  constexpr int D = BINS > kPassBS ? BINS / kPassBS : 1;
+  __shared__ uint16_t hist[kPassWaves][BINS];
   __shared__ uint32_t skey[kPassBS], spos[kPassBS];
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
@@ -417,30 +448,27 @@ void k_sort_one(Keys k, int n, int passes, uint32_t* __restrict__ keys_out, uint
       fill_piece(fill, t, nullptr);
     return;
   }
+  const int bins = 1 << bits;
   uint32_t key = i < n ? k.at(i) : 0, pos = i;
   for (int p = 0; p < passes; ++p) {
-#pragma unroll
-    for (int b = 0; b < kBins / 64; ++b) hist[wave][b * 64 + lane] = 0;
-    const uint32_t d = (key >> (p * kBits)) & (kBins - 1);
+    for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
+    const uint32_t d = (key >> (p * bits)) & (bins - 1);
     uint64_t same;
-    const uint32_t rank = rank_in_wave(d, i < n, &same);
+    const uint32_t rank = rank_in_wave<MAXB>(d, bits, i < n, &same);
     __syncthreads();
-    if (i < n && rank == 0) hist[wave][d] = (uint32_t)__popcll(same);
+    if (i < n && rank == 0) hist[wave][d] = (uint16_t)__popcll(same);
     __syncthreads();
-    uint32_t c[kPassWaves], sum = 0;
-    if (threadIdx.x < kBins) {
+    uint32_t sum[D], none[D];
 #pragma unroll
-      for (int w = 0; w < kPassWaves; ++w) sum += c[w] = hist[w][threadIdx.x];
-    }
-    uint32_t all;
-    uint32_t at = block_scan<kPassBS>(sum, lds, &all);
-    if (threadIdx.x < kBins) {
+    for (int q = 0; q < D; ++q) {
+      sum[q] = none[q] = 0;
+      const int b = q * kPassBS + threadIdx.x;
+      if (b < bins) {
 #pragma unroll
-      for (int w = 0; w < kPassWaves; ++w) {
-        hist[w][threadIdx.x] = at;
-        at += c[w];
+        for (int w = 0; w < kPassWaves; ++w) sum[q] += hist[w][b];
       }
     }
+    place_digits<BINS>(hist, bins, sum, none, lds);
     __syncthreads();
     if (i < n) {
       const uint32_t to = hist[wave][d] + rank;
@@ -684,10 +712,15 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   const int64_t fill_groups = together ? (fill.total + kPassWaves - 1) / kPassWaves : 0;
   uint8_t* mark = first && n > 0 && !together ? touched : nullptr;
   const int passes = mark && p.passes < 2 ? 2 : p.passes;
-  if (n > 0 && n <= kPassBS && !mark)
-    hipLaunchKernelGGL((k_sort_one<Gt>), dim3((unsigned)grid_for(1 + fill_groups, 1, kPassBS)), dim3(kPassBS), 0, s,
-                       tokens, (int)n, passes, keys[0], pos[0], fill);
-  else
+  const bool wide = p.digit > kBits;
+  if (n > 0 && n <= kPassBS && !mark) {
+    auto one = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fill_groups)), dim3(kPassBS), 0, s, tokens,
+                         (int)n, passes, p.digit, keys[0], pos[0], fill);
+    };
+    if (wide) one(k_sort_one<Gt, kWideBits>);
+    else one(k_sort_one<Gt, kBits>);
+  } else {
     for (int i = 0; n > 0 && i < passes; ++i) {
       const int src = (i + 1) & 1, dst = i & 1;
       Keys k = tokens;
@@ -697,8 +730,12 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
       if (n <= kPassSort) {
         const int tiles = (int)((n + kPassBS - 1) / kPassBS);
         const int64_t more = i > 0 ? 0 : mark ? (vocab + kClearBytes - 1) / kClearBytes : fill_groups;
-        hipLaunchKernelGGL((k_sort_pass<Gt>), dim3((unsigned)grid_for(tiles + more, 1, kPassBS)), dim3(kPassBS), 0, s,
-                           k, pos_in, (int)n, i * kBits, tiles, (int)final, keys[dst], pos[dst], mark, fill);
+        auto pass = [&](auto kernel) {
+          hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles + more)), dim3(kPassBS), 0, s, k,
+                             pos_in, (int)n, i * p.digit, p.digit, tiles, (int)final, keys[dst], pos[dst], mark, fill);
+        };
+        if (wide) pass(k_sort_pass<Gt, kWideBits>);
+        else pass(k_sort_pass<Gt, kBits>);
       } else {
         const dim3 gd((unsigned)grid_for(p.tiles, 1)), bd(kThreads);
         hipLaunchKernelGGL(k_sort_count, gd, bd, 0, s, k, n, i * kBits, p.tiles, counts, i == 0 ? mark : nullptr);
@@ -708,6 +745,7 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
       }
       last = dst;
     }
+  }
   if (first && !together)
     hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(fill.total, 1, 64)), dim3(64), 0, s, fill, mark);
   if (n == 0) return;
@@ -745,6 +783,12 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
   p.bits = 1;  // keys are 0 .. vocab
   while (p.bits < 32 && (vocab >> p.bits) != 0) ++p.bits;
   p.passes = (p.bits + kBits - 1) / kBits;
+  p.digit = kBits;
+  if (n <= kPassSort) {
+    const int fewer = (p.bits + kWideBits - 1) / kWideBits;
+    if (fewer < p.passes) p.passes = fewer;
+    p.digit = (p.bits + p.passes - 1) / p.passes;
+  }
   p.tiles = (n + kSortTile - 1) / kSortTile;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {

@@ -167,7 +167,7 @@ struct EmbedPlan {
   int chunk;         // sorted entries per chunk (a workgroup's)
   int64_t chunks;    // chunks of the n entries
   int64_t pitch;     // fp32 values per partial row (dim rounded up to 8)
-  int bits, passes;  // bits of a key, and digits of the sort
+  int bits, passes, digit;  // bits of a key, passes of the sort, bits of a pass's digit
   int64_t tiles;     // tiles of the sort's passes
   int64_t keys[2], pos[2], counts, totals, touched, partials, bytes;
 };

@@ -16,6 +16,7 @@ import pytest
 import torch
 
 import fsdp_sharded_optimizer_flatparameter_amd as zs
+from oracle import bf16 as obf16
 from oracle import embedding as oe
 
 pytestmark = pytest.mark.gpu
@@ -69,6 +70,24 @@ def test_forward(n, dim, dtype, out):
         err = np.abs(f64(o) - want)
         assert np.all(err <= (U + h + U * h) * np.abs(want)), (scale, float(err.max()))
         assert gaps_untouched(big, dim)
+
+
+def test_forward_rounds_every_pattern_to_nearest_even():
+    # all upper halves of an fp32 pattern with lower halves around the ties: subnormals, overflow, NaN
+    hi = torch.arange(65536, device="cuda", dtype=torch.int64) << 16
+    low = torch.tensor([0, 1, 0x7FFF, 0x8000, 0x8001, 0xFFFF], device="cuda")
+    table = (hi[:, None] + low[None, :]).to(torch.uint32).view(torch.float32)
+    ids = torch.arange(65536, device="cuda", dtype=torch.int32)
+    out = torch.empty(65536, 6, device="cuda", dtype=torch.bfloat16)
+    zs.zs_embed_forward(table, ids, out)
+    got = out.view(torch.int16).cpu().numpy().view(np.uint16)
+    x = table.cpu().numpy()
+    nan = np.isnan(x)
+    assert np.array_equal(got[~nan], obf16.to_bf16_bits(x)[~nan])
+    assert np.all((got[nan] & 0x7FC0) == 0x7FC0) and np.all((got[nan] & 0x7F) != 0)
+    same = torch.empty(65536, 6, device="cuda")
+    zs.zs_embed_forward(table, ids, same)
+    assert np.array_equal(bits(same).cpu().numpy()[~nan], x.view(np.int32)[~nan])
 
 
 def test_forward_shapes_and_nothing_to_do():
@@ -176,6 +195,70 @@ def test_backward_many_tokens(n, kind):
     grad = torch.empty(vocab, dim, device="cuda")
     run_backward(dout, tokens, grad, first=True)
     check_backward(dout, tokens, grad, None, 1.0, -1, True)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("n", [1, 1023, 1024, 1025, 32767, 32768, 32769])
+@pytest.mark.parametrize("vocab", [255, 510, 511, 512, 2046, 2047, 2048, 262143, 262144])
+def test_backward_around_the_sorts_limits(n, vocab, first):
+    # where the sort changes its launches, its digits and their number
+    g = gen(n + vocab)
+    _, dout = matrix(g, n, 3, "f32")
+    tokens = make_tokens(g, n, vocab, "mixed", "i32" if vocab % 2 else "i64")
+    tokens[n // 2] = vocab - 1  # the largest key
+    _, grad = matrix(g, vocab, 3, "f32", fill=float("nan") if first else None)
+    before = grad.clone()
+    run_backward(dout, tokens, grad, first=first)
+    check_backward(dout, tokens, grad, before, 1.0, -1, first)
+
+
+def reference_on_the_gpu(dout, tokens, grad_shape, before, scale):
+    """The gradient and sum of magnitudes in fp64 (adding in another order is 2^-53 of the magnitudes)."""
+    keep = (tokens >= 0) & (tokens < grad_shape[0])
+    want, size = (torch.zeros(grad_shape, device="cuda", dtype=torch.float64) for _ in range(2))
+    rows = dout.double()[keep] * scale
+    want.index_add_(0, tokens[keep].long(), rows)
+    size.index_add_(0, tokens[keep].long(), rows.abs())
+    if before is not None:
+        want += before.double()
+        size += before.double().abs()
+    m = torch.bincount(tokens[keep].long(), minlength=grad_shape[0])[:, None]
+    return want, size, m
+
+
+@pytest.mark.parametrize("n,vocab,dim,dtype,gdt,first", [
+    (700, 70001, 801, "f32", "f32", True),      # a table above 200 MB: zeros after the sort, by marks
+    (5000, 70001, 800, "bf16", "f32", True),
+    (40000, 30001, 2000, "bf16", "bf16", True),  # 160 MB of rows: streamed
+    (40000, 9001, 1600, "bf16", "f32", False),
+    (33000, 500, 1030, "f32", "f32", False),
+])
+def test_backward_large(n, vocab, dim, dtype, gdt, first):
+    g = gen(n + dim)
+    _, dout = matrix(g, n, dim, dtype)
+    tokens = make_tokens(g, n, vocab, "mixed", "i64")
+    tokens[: n // 10] = 7  # a frequent one
+    _, grad = matrix(g, vocab, dim, gdt, fill=float("nan") if first else None)
+    before = None if first else grad.clone()
+    run_backward(dout, tokens, grad, scale=0.5, first=first)
+    want, size, m = reference_on_the_gpu(dout, tokens, (vocab, dim), before, 0.5)
+    tol = ((m + 2) * U * size + HALF[grad.dtype] * want.abs()) * (1 + 2.0 ** -7)
+    assert bool(((grad.double() - want).abs() <= tol).all())
+    if first:
+        assert torch.count_nonzero(bits(grad[m[:, 0] == 0])) == 0
+
+
+@pytest.mark.parametrize("vocab,dim", [(1024, 768), (2048, 64)])
+def test_backward_of_a_position_table(vocab, dim):
+    # every position many times, in order: the wpe gradient of a batch
+    g = gen(vocab)
+    _, dout = matrix(g, 4 * vocab, dim, "bf16")
+    positions = torch.arange(4 * vocab, device="cuda", dtype=torch.int32) % vocab
+    grad = torch.empty(vocab, dim, device="cuda")
+    run_backward(dout, positions, grad, first=True)
+    # four rows in order, fp32: the same bits
+    r = dout.float().view(4, vocab, dim)
+    assert torch.equal(grad, ((r[0] + r[1]) + r[2]) + r[3])
 
 
 @pytest.mark.parametrize("dtype,gdt", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])

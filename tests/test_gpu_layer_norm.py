@@ -219,6 +219,31 @@ def test_backward_many_rows(dim, rows):
         assert torch.equal(bits(dw2), bits(dw)) and torch.equal(bits(db2), bits(db))
 
 
+@pytest.mark.parametrize("rows,dim,dtype", [(4099, 8192, "bf16"), (9001, 1601, "f32")])
+def test_large_calls_past_the_caches(rows, dim, dtype):
+    # more than 100 MB: the streaming variants, against the same rows in smaller calls
+    g = gen(dim)
+    _, x = matrix(g, rows, dim, dtype, 0, 0.25)
+    _, dy = matrix(g, rows, dim, dtype)
+    w, b = matrix(g, 1, dim, dtype)[1][0], matrix(g, 1, dim, dtype)[1][0]
+    y, dx, y2, dx2 = (torch.empty_like(x) for _ in range(4))
+    mean, rstd, mean2, rstd2 = (torch.empty(rows, device="cuda") for _ in range(4))
+    dw, db = torch.empty(dim, device="cuda"), torch.empty(dim, device="cuda")
+    zs.zs_layer_norm_forward(x, w, b, y, mean=mean, rstd=rstd)
+    run_backward(dy, x, w, mean, rstd, dx, dw, db, True)
+    for i in range(0, rows, 1000):
+        j = slice(i, i + 1000)
+        zs.zs_layer_norm_forward(x[j], w, b, y2[j], mean=mean2[j], rstd=rstd2[j])
+        zs.zs_layer_norm_backward(dy[j], x[j], w, mean[j], rstd[j], dx2[j])
+    for p, q in ((y, y2), (mean, mean2), (rstd, rstd2), (dx, dx2)):
+        assert torch.equal(bits(p), bits(q))
+    check_forward(x[:50], w, b, y[:50], mean[:50], rstd[:50], 1e-5)
+    xh = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for got, terms in ((dw, dy.double() * xh), (db, dy.double())):
+        err = (got.double() - terms.sum(0)).abs()
+        assert bool((err <= (rows + 6) * U * terms.abs().sum(0) * (1 + 2.0 ** -7)).all())
+
+
 def test_backward_against_differences():
     # fp32 at small sizes: the loss sum(y c) along a direction v, from the library's own forward pass
     g = gen(3)
