@@ -59,13 +59,6 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
   const int l = threadIdx.x % LPR;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-  Piece<T, VEC> next[NV];  // the next row is on its way while this one is worked on
-  auto fetch = [&](int64_t r) {
-    if (r < rows)
-#pragma unroll
-      for (int j = 0; j < NV; ++j) load_cols<T, VEC, NT>(next[j], x + r * x_ld, col_of<LPR, VEC>(j, l), dim);
-  };
-  fetch(row);
   Piece<W, VEC> wf[NV], bf[NV];  // as they lie in memory: half the registers for bf16
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -82,17 +75,20 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
   }
   cnt = lane_sum<G>(cnt);
   const float inv_cnt = 1.0f / (cnt > 0.0f ? cnt : 1.0f);
+  Piece<T, VEC> raw[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) raw[j].clear();
   // every row group of the workgroup takes the same number of turns (barriers)
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step, row += step, turn ^= 1) {
-    Piece<T, VEC> raw[NV];
+    if (row < rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_cols<T, VEC, NT>(raw[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       wf[j].stay_packed();
       bf[j].stay_packed();
-      raw[j] = next[j];
     }
-    fetch(row + step);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -474,9 +470,11 @@ void k_ln_grads(const float* __restrict__ partials, int64_t pitch, int parts, in
 // it faster (8192 rows of 768 fp32, 50 MB: 9.0 against 10.1 us).
 constexpr int64_t kStreamBytes = 100000000;
 // Workgroups (of 256 lanes) of the forward pass, 4 per CU, each walking over
-// its rows: 94 us for 16384 rows of 8192 bf16, against 98 with 768 and 100 or
-// more with 1280; 2048 were 1-2% faster there, but 14% slower for 8192 rows of
-// 768 fp32.
+// its rows: 88 us for 16384 rows of 8192 bf16 (6.1 TB/s), against 95 with 768,
+// 103 with 1280 and 99 with 2048. A row is loaded when the one before it is
+// done: with the next row always on its way the same takes 92 us (16384 rows
+// of 4096: 49 instead of 45), only 8192 fp32 rows of 8192 gain by it (91
+// instead of 93).
 constexpr int64_t kFwdSlots = 1024;
 constexpr int kVecBf16 = 8, kVecF32 = 4;  // elements of x in 16 bytes
 
