@@ -31,7 +31,7 @@ __device__ __forceinline__ uint32_t col_of(int j, int l) {
 template <typename W, int VEC>
 __device__ __forceinline__ void load_affine(Piece<W, VEC>& r, const W* p, float missing, uint32_t c, uint32_t dim) {
   if (p) {
-    load_cols<W, VEC>(r, p, c, dim);
+    take_cols<W, VEC>(r, p, c, dim);
   } else {
     r.clear();
 #pragma unroll
@@ -89,6 +89,9 @@ void k_ln_fwd(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, co
       wf[j].stay_packed();
       bf[j].stay_packed();
     }
+    if (ragged(dim, VEC) && row < rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) settle_cols<T, VEC>(raw[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -178,7 +181,7 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
     float s = 0.0f;
     for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> p;
-      load_cols<T, VEC>(p, xr, c, dim);
+      take_cols<T, VEC>(p, xr, c, dim);
       float t = 0.0f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) t += p.get(e);
@@ -188,7 +191,7 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
     float m2 = 0.0f;
     for (uint32_t c = threadIdx.x * VEC; c < dim; c += kLongBS * VEC) {
       Piece<T, VEC> p;
-      load_cols<T, VEC>(p, xr, c, dim);
+      take_cols<T, VEC>(p, xr, c, dim);
       float t = 0.0f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -206,7 +209,7 @@ void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ 
       Piece<T, VEC> p;
       Piece<W, VEC> wf, bf;
       float v[VEC];
-      load_cols<T, VEC>(p, xr, c, dim);
+      take_cols<T, VEC>(p, xr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
       load_affine<W, VEC>(bf, b, 0.0f, c, dim);
 #pragma unroll
@@ -274,6 +277,12 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
     rstd = nrstd;
     const bool live = row < rows;
     if (AHEAD) fetch(row + step);
+    if (ragged(dim, VEC) && row < rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        settle_cols<T, VEC>(rx[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
+        settle_cols<T, VEC>(rg[j], dy + row * dy_ld, col_of<LPR, VEC>(j, l), dim);
+      }
     float s1 = 0.0f, s2 = 0.0f;
     if (live) {
 #pragma unroll
@@ -364,8 +373,8 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
       Piece<T, VEC> px, pg;
       Piece<W, VEC> wf;
       float t1 = 0.0f, t2 = 0.0f;
-      load_cols<T, VEC>(px, xr, c, dim);
-      load_cols<T, VEC>(pg, gr, c, dim);
+      take_cols<T, VEC>(px, xr, c, dim);
+      take_cols<T, VEC>(pg, gr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -381,8 +390,8 @@ void k_ln_bwd_long(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict_
       Piece<T, VEC> px, pg;
       Piece<W, VEC> wf;
       float v[VEC];
-      load_cols<T, VEC>(px, xr, c, dim);
-      load_cols<T, VEC>(pg, gr, c, dim);
+      take_cols<T, VEC>(px, xr, c, dim);
+      take_cols<T, VEC>(pg, gr, c, dim);
       load_affine<W, VEC>(wf, w, 1.0f, c, dim);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = rstd * (fmaf(pg.get(e), wf.get(e), -a) - (px.get(e) - mean) * rstd * k);
@@ -405,8 +414,8 @@ void k_ln_cols(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x,
   for (int e = 0; e < VEC; ++e) dw[e] = db[e] = 0.0f;
   for (int64_t row = g; row < rows; row += parts) {
     Piece<T, VEC> px, pg;
-    load_cols<T, VEC>(px, x + row * x_ld, c, dim);
-    load_cols<T, VEC>(pg, dy + row * dy_ld, c, dim);
+    take_cols<T, VEC>(px, x + row * x_ld, c, dim);
+    take_cols<T, VEC>(pg, dy + row * dy_ld, c, dim);
     const float mean = mean_in[row], rstd = rstd_in[row];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {

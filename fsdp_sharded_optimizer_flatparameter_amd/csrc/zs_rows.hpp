@@ -82,6 +82,14 @@ struct Piece {
       }
     }
   }
+  // every element one place down, a zero behind the last
+  __device__ __forceinline__ void drop_first() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t up = i + 1 < N ? r[i + 1] : 0u;
+      r[i] = sizeof(T) == 4 ? up : (r[i] >> 16) | (up << 16);
+    }
+  }
   __device__ __forceinline__ void put(int e, float x) { r[e] = __float_as_uint(x); }
   __device__ __forceinline__ void put(int e, uint16_t h) { r[e / 2] |= (uint32_t)h << (16 * (e & 1)); }
   __device__ __forceinline__ float get(int e) const {
@@ -138,15 +146,37 @@ __device__ __forceinline__ void store_part(T* p, const float* v, int n) {
 // same for the whole wave, an access then takes it from scalar registers and
 // one register of offset, instead of two registers of address for each piece
 // that is on its way.
+//
+// load_cols sends the loads off. The zeros of the lanes behind the row are
+// written before the load: written behind it, into the same registers, they
+// would have to wait for it, and with them the wave (8192 backward rows of 5376
+// bf16, which end in the middle of a wave: 50 us, not 76). Where dim is not a
+// multiple of VEC the lane that the row ends in takes the row's last VEC
+// elements, and settle_cols, which callers run then where the pieces are
+// used, moves them to their places: that has to wait for them (16384 backward
+// rows of 4095: 96 us, 163 with its elements loaded one by one).
 template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void load_cols(Piece<T, VEC>& p, const T* row, uint32_t c, uint32_t dim) {
-  if (c + VEC <= dim) {
-    p.template load<NT>(row + c);
-  } else if (c < dim) {
-    p.load_part(row + c, (int)(dim - c));
-  } else {
-    p.clear();
+  p.clear();
+#pragma unroll
+  for (int i = 0; i < Piece<T, VEC>::N; ++i) asm volatile("" : "+v"(p.r[i]));  // now, not behind the load
+  const uint32_t end = dim >= VEC ? dim : 0, last = dim - VEC;
+  if (c < end) p.template load<NT>(row + (c < last ? c : last));
+}
+__device__ __forceinline__ bool ragged(uint32_t dim, int vec) { return dim % vec != 0; }
+template <typename T, int VEC>
+__device__ __forceinline__ void settle_cols(Piece<T, VEC>& p, const T* row, uint32_t c, uint32_t dim) {
+  if (dim < VEC) {
+    if (c == 0) p.load_part(row, (int)dim);
+  } else if (c < dim && c + VEC > dim) {
+    for (uint32_t n = c + VEC - dim; n > 0; --n) p.drop_first();
   }
+}
+// Both, for pieces that are used at once.
+template <typename T, int VEC>
+__device__ __forceinline__ void take_cols(Piece<T, VEC>& p, const T* row, uint32_t c, uint32_t dim) {
+  load_cols<T, VEC>(p, row, c, dim);
+  if (ragged(dim, VEC)) settle_cols<T, VEC>(p, row, c, dim);
 }
 template <typename T, int VEC, bool NT = false>
 __device__ __forceinline__ void store_cols(T* row, const float* v, uint32_t c, uint32_t dim) {
