@@ -162,10 +162,31 @@ struct Keys {
   const uint32_t* keys;  // later passes
   int index_type;
   int64_t vocab, padding;
-  __device__ __forceinline__ uint32_t at(int64_t i) const {
-    if (keys) return keys[i];
-    const int64_t id = id_at(tokens, index_type, i);
+  __device__ __forceinline__ uint32_t of(int64_t id) const {
     return (uint64_t)id < (uint64_t)vocab && id != padding ? (uint32_t)id : (uint32_t)vocab;
+  }
+  // The keys of entries i, i + step, ... (the last entry's for those at or past
+  // n, which is above 0): all loads are on their way before the first is
+  // looked at, without a branch between them.
+  template <int N>
+  __device__ __forceinline__ void load(uint32_t* out, int64_t i, int64_t step, int64_t n) const {
+    auto at = [&](int u) { return i + u * step < n ? i + u * step : n - 1; };
+    if (keys) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) out[u] = ld_g(keys + at(u));
+    } else if (index_type == ZS_I64) {
+      int64_t id[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u) id[u] = ld_g(static_cast<const int64_t*>(tokens) + at(u));
+#pragma unroll
+      for (int u = 0; u < N; ++u) out[u] = of(id[u]);
+    } else {
+      int32_t id[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u) id[u] = ld_g(static_cast<const int32_t*>(tokens) + at(u));
+#pragma unroll
+      for (int u = 0; u < N; ++u) out[u] = of(id[u]);
+    }
   }
 };
 
@@ -180,12 +201,12 @@ void k_sort_count(Keys k, int64_t n, int shift, int64_t tiles, uint32_t* __restr
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     for (int b = threadIdx.x; b < kBins; b += kThreads) h[b] = 0;
     __syncthreads();
-    const int64_t i0 = tile * kSortTile;
+    const int64_t i0 = tile * kSortTile + threadIdx.x;
+    uint32_t key[kSortRounds];
+    k.load<kSortRounds>(key, i0, kThreads, n);
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-      const int64_t i = i0 + r * kThreads + threadIdx.x;
-      if (i < n) atomicAdd(&h[(k.at(i) >> shift) & (kBins - 1)], 1u);
-    }
+    for (int r = 0; r < kSortRounds; ++r)
+      if (i0 + r * kThreads < n) atomicAdd(&h[(key[r] >> shift) & (kBins - 1)], 1u);
     __syncthreads();
     for (int b = threadIdx.x; b < kBins; b += kThreads) counts[b * tiles + tile] = h[b];
     __syncthreads();
@@ -283,10 +304,10 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
     __syncthreads();
     const int64_t i0 = tile * kSortTile + wave * (64 * kSortRounds);
     uint32_t key[kSortRounds], rank[kSortRounds];
+    k.load<kSortRounds>(key, i0 + lane, 64, n);
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
       const int64_t i = i0 + r * 64 + lane;
-      key[r] = i < n ? k.at(i) : 0;
       rank[r] = wave_rank((key[r] >> shift) & (kBins - 1), i < n, hist[wave]);
     }
     __syncthreads();
@@ -389,20 +410,16 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
   auto digit = [&](uint32_t key) { return (key >> shift) & (bins - 1); };
   const int tile0 = blockIdx.x * kPassBS, i = tile0 + threadIdx.x;
   constexpr int U = 8;  // entries on their way per thread
-  uint32_t kk[U];
-  auto fetch = [&](int j0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) kk[u] = j0 + u * kPassBS < n ? k.at(j0 + u * kPassBS) : 0;
-  };
-  fetch(threadIdx.x);
-  const uint32_t key = i < n ? k.at(i) : 0;
-  const uint32_t pos = i < n ? (pos_in ? pos_in[i] : (uint32_t)i) : 0;
+  uint32_t kk[U], key;
+  k.load<1>(&key, i, 0, n);
+  const uint32_t pos = pos_in ? ld_g(pos_in + (i < n ? i : n - 1)) : (uint32_t)i;
+  k.load<U>(kk, threadIdx.x, kPassBS, n);
   for (int b = threadIdx.x; b < copies * (bins + 1); b += kPassBS) counts[b] = 0;
   for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
   __syncthreads();
   uint32_t* own = counts + (lane & (copies - 1)) * (bins + 1);
   for (int j0 = threadIdx.x; j0 < n; j0 += U * kPassBS) {
-    if (j0 != (int)threadIdx.x) fetch(j0);
+    if (j0 != (int)threadIdx.x) k.load<U>(kk, j0, kPassBS, n);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u * kPassBS;
@@ -456,7 +473,8 @@ void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys
     return;
   }
   const int bins = 1 << bits;
-  uint32_t key = i < n ? k.at(i) : 0, pos = i;
+  uint32_t key, pos = i;
+  k.load<1>(&key, i, 0, n);
   for (int p = 0; p < passes; ++p) {
     for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
     const uint32_t d = (key >> (p * bits)) & (bins - 1);
