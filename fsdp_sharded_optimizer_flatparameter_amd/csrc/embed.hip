@@ -523,6 +523,9 @@ constexpr int64_t kStreamBytes = 60000000;
 // sums then weigh; fewer waves leave compute units without work.
 constexpr int64_t kChunkWaves = 8192;
 
+// Up to this many tokens make one chunk, and the call one launch.
+constexpr int64_t kFewTokens = 8 * 8;
+
 // The sorted entries are cut into chunks of kWaves K: a workgroup takes one chunk
 // and 64 pieces of columns, each of its waves K entries. A wave adds its rows
 // in registers and writes the gradient of each token whose run of entries ends
@@ -532,6 +535,7 @@ constexpr int64_t kChunkWaves = 8192;
 // leaves one partial sum in the workspace (rows 2c and 2c + 1 of chunk c),
 // joined by k_embed_join.
 constexpr int kWaves = 8;
+static_assert(kFewTokens == 8 * kWaves, "one chunk");
 
 template <typename Gt, int VEC>
 __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale, bool add, const Piece<Gt, VEC>& old,
@@ -542,9 +546,13 @@ __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale,
   store_cols<Gt, VEC>(row, v, c, dim);
 }
 
-template <typename T, typename Gt, int VEC, int K, bool FIRST, bool NT>
+// With SORT, for the few entries of one chunk, each workgroup sorts the tokens
+// itself by counting for each one those that come before it, and that is the
+// whole call: 3.2 us for one token instead of 8.1, 7.5 for 64 instead of 10.4 (128
+// would take 12.3 instead of 11.0).
+template <typename T, typename Gt, int VEC, int K, bool FIRST, bool NT, bool SORT>
 __global__ __launch_bounds__(kWaves * 64)
-void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, uint32_t vocab,
+void k_embed_chunks(Keys tokens, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, uint32_t vocab,
                     int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, uint32_t dim,
                     float scale, Gt* __restrict__ grad, int64_t grad_ld, float* __restrict__ partials,
                     uint32_t pitch) {
@@ -555,8 +563,31 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
   static_assert(K + 2 <= 64 && K % U == 0, "a lane for each entry and its two neighbours");
   __shared__ __align__(16) float heads[kWaves][64 * VEC];
   __shared__ int through[kWaves];
+  constexpr int M = SORT ? K * kWaves : 1;
+  __shared__ uint32_t skey[M], spos[M];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if constexpr (SORT) {
+    __shared__ __align__(16) uint32_t all[M];
+    const int t = threadIdx.x;
+    uint32_t key = 0xffffffffu;
+    if (t < M) {
+      tokens.load<1>(&key, t, 0, n);
+      all[t] = t < n ? key : 0xffffffffu;  // the places behind the last count for none
+    }
+    __syncthreads();
+    if (t < n) {
+      int rank = 0;
+      for (int j = 0; j < (int)n; j += 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(&all[j]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rank += v[q] < key || (v[q] == key && j + q < t);
+      }
+      skey[rank] = key;
+      spos[rank] = t;
+    }
+    __syncthreads();
+  }
   for (int64_t item = blockIdx.x; item < chunks * coltiles; item += gridDim.x) {
     const int64_t ch = quot(item, coltiles);
     const uint32_t c = ((uint32_t)(item - ch * coltiles) * 64 + lane) * VEC;
@@ -566,8 +597,8 @@ void k_embed_chunks(const uint32_t* __restrict__ keys, const uint32_t* __restric
     {
       const int64_t e = e0 - 1 + lane;
       if (lane < K + 2 && e >= 0 && e < n) {
-        kk = keys[e];
-        pp = pos[e];
+        kk = SORT ? skey[e] : keys[e];
+        pp = SORT ? spos[e] : pos[e];
       }
     }
     auto key_at = [&](int u) { return (uint32_t)__builtin_amdgcn_readlane((int)kk, u + 1); };
@@ -745,12 +776,15 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   // In a launch of their own the zeros go by marks of the rows that tokens
   // select, which the first pass clears and the last one sets.
   const Fill<Gt> fill = fill_plan(grad, vocab, dim, grad_ld);
-  const bool together = first && n > 0 && n <= kPassSort && vocab * dim * (int64_t)sizeof(Gt) <= kFillTogether;
+  const bool few = n <= kFewTokens;
+  const bool together = first && !few && n <= kPassSort && vocab * dim * (int64_t)sizeof(Gt) <= kFillTogether;
   const int64_t fill_groups = together ? (fill.total + kPassWaves - 1) / kPassWaves : 0;
-  uint8_t* mark = first && n > 0 && !together ? touched : nullptr;
+  uint8_t* mark = first && !few && !together ? touched : nullptr;
   const int passes = mark && p.passes < 2 ? 2 : p.passes;
   const bool wide = p.digit > kBits;
-  if (n > 0 && n <= kPassBS && !mark) {
+  if (few) {
+    // sorted where they are used
+  } else if (n <= kPassBS && !mark) {
     auto one = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fill_groups)), dim3(kPassBS), 0, s, tokens,
                          (int)n, passes, p.digit, keys[0], pos[0], fill);
@@ -758,7 +792,7 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
     if (wide) one(k_sort_one<Gt, kWideBits>);
     else one(k_sort_one<Gt, kBits>);
   } else {
-    for (int i = 0; n > 0 && i < passes; ++i) {
+    for (int i = 0; i < passes; ++i) {
       const int src = (i + 1) & 1, dst = i & 1;
       Keys k = tokens;
       if (i) k.keys = keys[src];
@@ -788,16 +822,24 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   if (n == 0) return;
   const int64_t coltiles = (dim + 64 * VEC - 1) / (64 * VEC), items = p.chunks * coltiles;
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(items, 1, kWaves * 64)), dim3(kWaves * 64), 0, s,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(items, 1, kWaves * 64)), dim3(kWaves * 64), 0, s, tokens,
                        keys[last], pos[last], n, (uint32_t)vocab, p.chunks, coltiles, dout, dout_ld, (uint32_t)dim, scale, grad,
                        grad_ld, partials, (uint32_t)p.pitch);
   };
   auto pick = [&](auto f) {
     constexpr bool F = decltype(f)::value;
-    if (p.chunk == 4 * kWaves) go(k_embed_chunks<T, Gt, VEC, 4, F, false>);
-    else if (p.chunk == 8 * kWaves) go(k_embed_chunks<T, Gt, VEC, 8, F, false>);
-    else if (n * dim * (int64_t)sizeof(T) <= kStreamBytes) go(k_embed_chunks<T, Gt, VEC, 16, F, false>);
-    else go(k_embed_chunks<T, Gt, VEC, 16, F, true>);
+    if (few) {
+      if (p.chunk == 4 * kWaves) go(k_embed_chunks<T, Gt, VEC, 4, F, false, true>);
+      else go(k_embed_chunks<T, Gt, VEC, 8, F, false, true>);
+    } else if (p.chunk == 4 * kWaves) {
+      go(k_embed_chunks<T, Gt, VEC, 4, F, false, false>);
+    } else if (p.chunk == 8 * kWaves) {
+      go(k_embed_chunks<T, Gt, VEC, 8, F, false, false>);
+    } else if (n * dim * (int64_t)sizeof(T) <= kStreamBytes) {
+      go(k_embed_chunks<T, Gt, VEC, 16, F, false, false>);
+    } else {
+      go(k_embed_chunks<T, Gt, VEC, 16, F, true, false>);
+    }
   };
   if (first) pick(std::true_type{});
   else pick(std::false_type{});
@@ -814,7 +856,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t dim) {
   p.pitch = (dim + 7) / 8 * 8;
   const int64_t coltiles = (dim + 511) / 512;
   int k = 4;  // entries per wave
-  while (k < 16 && n / k * coltiles > kChunkWaves) k *= 2;
+  while (k < 16 && (n / k * coltiles > kChunkWaves || (n <= kFewTokens && n > k * kWaves))) k *= 2;
   p.chunk = k * kWaves;
   p.chunks = (n + p.chunk - 1) / p.chunk;
   p.bits = 1;  // keys are 0 .. vocab
