@@ -389,13 +389,14 @@ def zs_clip_coefficient(partials, max_norm, coef_out, norm_out=None, stream=None
 
 # ---------------------------------------------------------------- embedding, layer norm
 
+_Tensor = torch.Tensor
 _INDEX_TYPES = {torch.int32: L.ZS_I32, torch.int64: L.ZS_I64}
 
 
 def _rows2d(t, name, dev):
     """(rows, dim, row stride) of a tensor whose last dimension is a row: two
     dimensions with any stride between rows, or contiguous with any number."""
-    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in _DTYPES:
+    if isinstance(t, _Tensor) and t.get_device() == dev and t.dtype in _DTYPES:
         shape = t.shape
         if len(shape) == 2:
             rows, dim = shape
@@ -414,7 +415,7 @@ def _rows2d(t, name, dev):
 
 
 def _on_device(t, name, dev):
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -423,7 +424,7 @@ def _on_device(t, name, dev):
 
 
 def _ids(t, name, n, dev):
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()):
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.is_contiguous()):
         _on_device(t, name, dev)
         raise ValueError(f"{name} must be contiguous")
     itype = _INDEX_TYPES.get(t.dtype)
@@ -438,7 +439,7 @@ def _vector(t, name, n, dev, dtype=None):
     """Pointer of an optional contiguous vector of n elements on device `dev`."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()):
+    if not (isinstance(t, _Tensor) and t.get_device() == dev and t.is_contiguous()):
         _on_device(t, name, dev)
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype:
@@ -449,7 +450,7 @@ def _vector(t, name, n, dev, dtype=None):
 
 
 def _device_index(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     return t.get_device()
 
@@ -457,15 +458,17 @@ def _device_index(t, name):
 def _workspace(ws, dev):
     if ws is None:
         return None, 0
-    if not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
+    if not (isinstance(ws, _Tensor) and ws.get_device() == dev and ws.is_contiguous()):
         _on_device(ws, "workspace", dev)
         raise ValueError("workspace must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 # The current stream's handle without a Stream object around it (1.1 us of a
-# call of 6) where this torch offers that.
+# call of 6), and the current device, straight from torch's bindings where this
+# torch has them there.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(name, dev, stream, *args):
@@ -476,12 +479,14 @@ def _call(name, dev, stream, *args):
         if stream.device_index != dev:
             raise ValueError("the stream is another device's")
         stream = stream.cuda_stream
+    else:
+        stream = int(stream)
     fn = getattr(_lib(), name)
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, int(stream))
+    if _current_device() == dev:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, int(stream))
+            st = fn(*args, stream)
     if st != 0:
         L.check(name, st)
 
