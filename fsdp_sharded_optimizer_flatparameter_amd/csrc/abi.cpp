@@ -78,10 +78,10 @@ inline bool index_type_ok(int32_t t) { return t == ZS_I32 || t == ZS_I64; }
 inline int64_t index_size(int32_t t) { return t == ZS_I32 ? 4 : 8; }
 
 // Sizes of the embedding and layer norm calls: counts stay in 31 bits (sorted
-// positions and keys are 32-bit), widths in 27 (column offsets are 32-bit in
-// places).
+// positions and keys are 32-bit), widths in 24 (columns are 32-bit, and the
+// launches over columns stay within a dispatch's 32-bit work-item count).
 constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxDim = (int64_t(1) << 27) - 1;
+constexpr int64_t kMaxDim = (int64_t(1) << 24) - 1;
 inline bool count_ok(int64_t n) { return n >= 0 && n <= kMaxCount; }
 inline bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
 
@@ -521,9 +521,10 @@ zs_status zs_embed_backward(const void* dout, int32_t dtype, int64_t dout_ld, co
   if (!aligned(grad, (uintptr_t)elem_size(grad_dtype)) ||
       (n > 0 && (!aligned(dout, (uintptr_t)elem_size(dtype)) || !aligned(tokens, (uintptr_t)index_size(index_type)))))
     return ZS_ERR_ALIGN;
-  if (!workspace || workspace_bytes < zs_embed_workspace_bytes(n, vocab, dim)) return ZS_ERR_WORKSPACE;
+  const size_t need = zs_embed_workspace_bytes(n, vocab, dim);
+  if (!workspace || workspace_bytes < need) return ZS_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
-  const Span g = rows_span(grad, vocab, dim, grad_ld, grad_dtype), ws = {workspace, (int64_t)workspace_bytes};
+  const Span g = rows_span(grad, vocab, dim, grad_ld, grad_dtype), ws = {workspace, (int64_t)need};
   const Span in[2] = {rows_span(dout, n, dim, dout_ld, dtype), {tokens, n * index_size(index_type)}};
   if (any_overlap(g, in, 2) || any_overlap(ws, in, 2) || any_overlap(g, &ws, 1)) return ZS_ERR_OVERLAP;
   return launch([&] {
@@ -539,7 +540,7 @@ zs_status zs_layer_norm_forward(const void* x, int32_t dtype, int64_t x_ld, cons
   if (!float_type(dtype) || !float_type(wdtype)) return ZS_ERR_DTYPE;
   if (!count_ok(rows) || !dim_ok(dim) || (rows > 0 && dim < 1)) return ZS_ERR_SIZE;
   if (!stride_ok(rows, dim, x_ld) || !stride_ok(rows, dim, y_ld)) return ZS_ERR_SIZE;
-  if (!std::isfinite(eps) || eps < 0) return ZS_ERR_HPARAM;
+  if (!std::isfinite((float)eps) || eps < 0) return ZS_ERR_HPARAM;
   if (rows == 0) return ZS_OK;
   if (!x || !y) return ZS_ERR_NULL;
   const uintptr_t es = (uintptr_t)elem_size(dtype), wsz = (uintptr_t)elem_size(wdtype);
@@ -579,15 +580,16 @@ zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, i
                    !aligned(weight, (uintptr_t)elem_size(wdtype))))
     return ZS_ERR_ALIGN;
   if (!aligned(dweight, gs) || !aligned(dbias, gs)) return ZS_ERR_ALIGN;
-  if (grads && rows > 0) {
-    if (!workspace || workspace_bytes < zs_layer_norm_workspace_bytes(rows, dim)) return ZS_ERR_WORKSPACE;
+  const size_t need = grads ? zs_layer_norm_workspace_bytes(rows, dim) : 0;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return ZS_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
   }
   const Span in[5] = {rows_span(dy, rows, dim, dy_ld, dtype), rows_span(x, rows, dim, x_ld, dtype),
                       rows_span(weight, rows > 0, dim, dim, wdtype), {mean, rows * 4}, {rstd, rows * 4}};
   const Span out[4] = {rows_span(dx, rows, dim, dx_ld, dtype), rows_span(dweight, 1, dim, dim, grad_dtype),
                        rows_span(dbias, 1, dim, dim, grad_dtype),
-                       {workspace, grads && rows > 0 ? (int64_t)workspace_bytes : 0}};
+                       {workspace, (int64_t)need}};
   for (int i = 0; i < 4; ++i)
     if (any_overlap(out[i], in, 5) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
   return launch([&] {

@@ -145,10 +145,9 @@ void k_embed_fill(Fill<Gt> f, const uint8_t* __restrict__ touched) {
 
 // ---------------------------------------------------------------- sort
 
-
 // Radix sort of (key, position) by digits of up to kBits bits, lowest first, each
-// pass stable. The key of a token that gets no gradient (outside
-// of the vocabulary, or the padding token) is `vocab`, behind all others.
+// pass stable. The key of a token that gets no gradient (outside of the
+// vocabulary, or the padding token) is `vocab`, behind all others.
 constexpr int kBits = 9;
 // In the passes of up to kPassSort entries also of up to kWideBits, where that
 // saves a pass: position tables of up to 2047 rows, small vocabularies.
@@ -196,7 +195,8 @@ void k_sort_count(Keys k, int64_t n, int shift, int64_t tiles, uint32_t* __restr
                   uint8_t* __restrict__ touched) {
   __shared__ uint32_t h[kBins];
   if (touched)  // the first pass clears it
-    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < k.vocab; i += (int64_t)gridDim.x * kThreads * 16)
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < k.vocab;
+         i += (int64_t)gridDim.x * kThreads * 16)
       st16(u32x4{0u, 0u, 0u, 0u}, touched + i);  // the array's room is a multiple of 16
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     for (int b = threadIdx.x; b < kBins; b += kThreads) h[b] = 0;
@@ -341,8 +341,9 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
 // own apart, and then places its own tile, an entry per thread. Counting by
 // tiles in a launch of its own, their sums in a second and the placing in a
 // third (k_sort_count, k_sort_scan, k_sort_scatter) takes 12 us a pass at any
-// of these sizes, this 5 us for 8192 entries and 10 for 32768; for 65536 it
-// takes 25 (32768 x 1024: 66 us with either way in the whole call).
+// of these sizes, this 6 us for 8192 entries and 25 for 65536 (the call for
+// 32768 rows of 1024: 80 us either way when the limit was set, 61 now; for
+// 65536 of 768: 120 us instead of 94).
 // The first pass clears `touched`, a byte per row of the gradient, with the
 // workgroups behind the tiles; the last one sets it for each token's row.
 constexpr int kPassBS = 1024;
@@ -468,7 +469,8 @@ void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
   if (blockIdx.x > 0) {
-    for (int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave; t < fill.total; t += (int64_t)(gridDim.x - 1) * kPassWaves)
+    for (int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave; t < fill.total;
+         t += (int64_t)(gridDim.x - 1) * kPassWaves)
       fill_piece(fill, t, nullptr);
     return;
   }
@@ -548,18 +550,18 @@ __device__ __forceinline__ void put_grad(Gt* row, const float* sum, float scale,
 
 // With SORT, for the few entries of one chunk, each workgroup sorts the tokens
 // itself by counting for each one those that come before it, and that is the
-// whole call: 3.2 us for one token instead of 8.1, 7.5 for 64 instead of 10.4 (128
-// would take 12.3 instead of 11.0).
+// whole call: 3.2 us for one token instead of 8.1, 7.5 for 64 instead of 10.4
+// (128 would take 12.3 instead of 11.0).
 template <typename T, typename Gt, int VEC, int K, bool FIRST, bool NT, bool SORT>
 __global__ __launch_bounds__(kWaves * 64)
-void k_embed_chunks(Keys tokens, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n, uint32_t vocab,
-                    int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, uint32_t dim,
+void k_embed_chunks(Keys tokens, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ pos, int64_t n,
+                    uint32_t vocab, int64_t chunks, int64_t coltiles, const T* __restrict__ dout, int64_t dout_ld, uint32_t dim,
                     float scale, Gt* __restrict__ grad, int64_t grad_ld, float* __restrict__ partials,
                     uint32_t pitch) {
   // Rows on their way at once; with them go the gradient's old rows (11408 rows
   // of 1728 bf16 into a bf16 accumulator: 34.6 us with 4, 40.0 with 8, which
   // take half of the registers).
-      constexpr int U = K < 8 || sizeof(T) * VEC > 16 || !FIRST ? 4 : 8;
+  constexpr int U = K < 8 || sizeof(T) * VEC > 16 || !FIRST ? 4 : 8;
   static_assert(K + 2 <= 64 && K % U == 0, "a lane for each entry and its two neighbours");
   __shared__ __align__(16) float heads[kWaves][64 * VEC];
   __shared__ int through[kWaves];
@@ -769,8 +771,8 @@ void run_embed_fwd(const T* table, int64_t vocab, int64_t dim, int64_t table_ld,
 
 template <typename T, typename Gt>
 void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys, uint32_t* const* pos,
-                   uint32_t* counts, uint32_t* totals, uint8_t* touched, float* partials, const T* dout, int64_t dout_ld, int64_t n,
-                   int64_t vocab, int64_t dim, float scale, Gt* grad, int64_t grad_ld, bool first, hipStream_t s) {
+                   uint32_t* counts, uint32_t* totals, uint8_t* touched, float* partials, const T* dout,
+                   int64_t dout_ld, int64_t n, int64_t vocab, int64_t dim, float scale, Gt* grad, int64_t grad_ld, bool first, hipStream_t s) {
   constexpr int VEC = vec_of<Gt>();
   int last = 0;
   // In a launch of their own the zeros go by marks of the rows that tokens
@@ -823,8 +825,8 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   const int64_t coltiles = (dim + 64 * VEC - 1) / (64 * VEC), items = p.chunks * coltiles;
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid_for(items, 1, kWaves * 64)), dim3(kWaves * 64), 0, s, tokens,
-                       keys[last], pos[last], n, (uint32_t)vocab, p.chunks, coltiles, dout, dout_ld, (uint32_t)dim, scale, grad,
-                       grad_ld, partials, (uint32_t)p.pitch);
+                       keys[last], pos[last], n, (uint32_t)vocab, p.chunks, coltiles, dout, dout_ld, (uint32_t)dim,
+                       scale, grad, grad_ld, partials, (uint32_t)p.pitch);
   };
   auto pick = [&](auto f) {
     constexpr bool F = decltype(f)::value;

@@ -142,7 +142,7 @@ __device__ __forceinline__ void store_part(T* p, const float* v, int n) {
 }
 
 // The piece of a row at column c; what lies at or past `dim` is zero, or is not
-// written. Columns are 32-bit (dim stays below 2^27): with a row's address the
+// written. Columns are 32-bit (dim stays below 2^24): with a row's address the
 // same for the whole wave, an access then takes it from scalar registers and
 // one register of offset, instead of two registers of address for each piece
 // that is on its way.

@@ -477,7 +477,9 @@ zs_status zs_copy_out_dim0(const uint16_t* gathered, int64_t gathered_numel,
  * accepted; rows on 16-byte boundaries are fastest. Arithmetic is fp32, each
  * result rounded once to its type. The sums over rows run in an order that
  * depends on the sizes (and on the tokens) alone: the same call gives the same
- * bits. Sizes: n, rows and vocab below 2^31, dim below 2^27 (else ZS_ERR_SIZE).
+ * bits. Sizes: n, rows and vocab below 2^31, dim below 2^24 (else ZS_ERR_SIZE).
+ * Overlap checks take rows with the gaps between them: two arguments may not
+ * interleave in one buffer. The stream's device must be the current one.
  */
 
 /*
@@ -542,7 +544,7 @@ zs_status zs_embed_backward(const void* dout, int32_t dtype, int64_t dout_ld, co
  *   weight[dim], bias[dim]
  *                      DEVICE, `wdtype` (ZS_F32 or ZS_BF16); either may be NULL
  *                      (ones, zeros)
- *   eps                finite, >= 0
+ *   eps                finite in fp32, >= 0
  *   y[rows, dim]       DEVICE, `dtype`, row stride y_ld:
  *                      y = (x - mean) * rstd * weight + bias with
  *                      mean = sum(x) / dim, rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps)
@@ -577,7 +579,7 @@ size_t zs_layer_norm_workspace_bytes(int64_t rows, int64_t dim);
  *                      dbias = (first ? 0 : dbias) + sum over rows of dy
  *   workspace          DEVICE scratch of at least zs_layer_norm_workspace_bytes(rows,
  *                      dim) bytes on a 16-byte boundary, required unless dweight and
- *                      dbias are both NULL; calls and graph replays that may run at
+ *                      dbias are both NULL or there are no rows; calls and graph replays that may run at
  *                      the same time need one each
  * rows == 0 with first != 0 sets dweight and dbias to zero. No output may
  * share bytes with an input, the workspace or another output. Errors:

@@ -37,7 +37,7 @@ def embed_fwd(lib, **kw):
 @pytest.mark.parametrize("kw,want", [
     (dict(dtype=2), DTYPE), (dict(out_dtype=7), DTYPE), (dict(itype=0), DTYPE), (dict(itype=4), DTYPE),
     (dict(n=-1), SIZE), (dict(vocab=-1), SIZE), (dict(dim=-1), SIZE), (dict(n=2 ** 31), SIZE),
-    (dict(vocab=2 ** 31), SIZE), (dict(dim=2 ** 27, table_ld=2 ** 27, out_ld=2 ** 27), SIZE),
+    (dict(vocab=2 ** 31), SIZE), (dict(dim=2 ** 24, table_ld=2 ** 24, out_ld=2 ** 24), SIZE),
     (dict(table_ld=63), SIZE), (dict(out_ld=63), SIZE), (dict(out_ld=2 ** 60), SIZE), (dict(table_ld=-64), SIZE),
     (dict(pos_table=at(3), positions=at(4), pos_rows=-1, pos_ld=64), SIZE),
     (dict(pos_table=at(3), positions=at(4), pos_rows=8, pos_ld=60), SIZE),
@@ -96,6 +96,7 @@ def norm_fwd(lib, **kw):
     (dict(dtype=2), DTYPE), (dict(wdtype=-1), DTYPE), (dict(rows=-1), SIZE), (dict(dim=0), SIZE), (dict(dim=-3), SIZE),
     (dict(rows=2 ** 31), SIZE), (dict(x_ld=63), SIZE), (dict(y_ld=1), SIZE),
     (dict(eps=-1e-9), HPARAM), (dict(eps=float("nan")), HPARAM), (dict(eps=float("inf")), HPARAM),
+    (dict(eps=1e39), HPARAM), (dict(dim=2 ** 24, x_ld=2 ** 24, y_ld=2 ** 24), SIZE),
     (dict(x=None), NULL), (dict(y=None), NULL),
     (dict(x=at(0, 1)), ALIGN), (dict(y=at(3, 1)), ALIGN), (dict(weight=at(1, 1)), ALIGN), (dict(bias=at(2, 1)), ALIGN),
     (dict(wdtype=0, bias=at(2, 2)), ALIGN), (dict(mean=at(4, 2)), ALIGN), (dict(rstd=at(5, 2)), ALIGN),
@@ -135,9 +136,9 @@ def test_layer_norm_backward_refusals(lib, kw, want):
 
 def test_workspace_sizes(lib):
     e, n = lib.zs_embed_workspace_bytes, lib.zs_layer_norm_workspace_bytes
-    for bad in ((-1, 10, 8), (10, -1, 8), (10, 10, -1), (2 ** 31, 10, 8), (10, 2 ** 31, 8), (10, 10, 2 ** 27)):
+    for bad in ((-1, 10, 8), (10, -1, 8), (10, 10, -1), (2 ** 31, 10, 8), (10, 2 ** 31, 8), (10, 10, 2 ** 24)):
         assert e(*bad) == 0
-    assert n(-1, 8) == 0 and n(8, -1) == 0 and n(2 ** 31, 8) == 0 and n(8, 2 ** 27) == 0
+    assert n(-1, 8) == 0 and n(8, -1) == 0 and n(2 ** 31, 8) == 0 and n(8, 2 ** 24) == 0
     # room for the two sorted arrays of keys and positions at the least, and it never shrinks with n
     sizes = [e(k, 50257, 768) for k in (0, 1, 100, 8192, 16384, 16385, 100000, 1 << 20)]
     assert all(s >= 8 * k for s, k in zip(sizes, (0, 1, 100, 8192, 16384, 16385, 100000, 1 << 20)))
