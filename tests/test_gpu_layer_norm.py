@@ -27,8 +27,8 @@ pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 U = 2.0 ** -24
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-DIMS = [1, 2, 7, 64, 127, 128, 129, 257, 512, 513, 768, 1024, 1031, 2048, 2056, 4095, 4096, 4104, 8192, 8200, 16384,
-        16391, 20001]
+DIMS = [1, 2, 7, 64, 127, 128, 129, 257, 512, 513, 768, 1024, 1031, 2048, 2056, 4095, 4096, 4104, 8192, 8200, 10240,
+        16384, 16391, 20001, 33003]
 
 
 def gen(seed):
