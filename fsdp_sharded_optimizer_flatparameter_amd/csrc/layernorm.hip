@@ -507,6 +507,9 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
     else launch(k_ln_fwd<T, W, LPR, NV, VEC, false>);
   };
   using std::integral_constant;
+  // Four pieces of bf16 rows with fp32 weights do not fit in 128 registers (4096
+  // rows of 28672: 174 us, 143 by the walk).
+  constexpr bool FITS = sizeof(T) == 4 || sizeof(W) == 2;
   // By width alone, so that a row gives the same bits whatever the number of
   // rows. One piece a lane is the quickest for one row (8192 bf16: 3.7 us on
   // 1024 or 512 lanes, 4.3 on 256), two to three the fastest for many, with
@@ -524,7 +527,7 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
   else if (nvec <= 768) go(integral_constant<int, 256>{}, integral_constant<int, 3>{});
   else if (nvec <= 1024) go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   else if (nvec <= 2048) go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
-  else if (nvec <= 4096) go(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+  else if (nvec <= 4096 && FITS) go(integral_constant<int, 1024>{}, integral_constant<int, FITS ? 4 : 2>{});
   else {
     const int64_t grid = rows < 2048 ? rows : 2048;
     hipLaunchKernelGGL((k_ln_fwd_long<T, W, VEC>), dim3((unsigned)grid), dim3(kLongBS), 0, s, x, x_ld, w, b, rows,
