@@ -512,7 +512,7 @@ def zs_embed_forward(table, tokens, out, *, scale=1.0, pos_table=None, positions
             raise ValueError("positions must have the tokens' dtype")
         pos_ptr, positions_ptr = pos_table.data_ptr(), positions.data_ptr()
     _call("zs_embed_forward", dev, stream, table.data_ptr(), _DTYPES[table.dtype], vocab, dim, table_ld,
-          pos_ptr, pos_rows, pos_ld, tokens.data_ptr(), positions_ptr, itype, n, scale, out.data_ptr(),
+          pos_ptr, pos_rows, pos_ld, tokens.data_ptr(), positions_ptr, itype, n, float(scale), out.data_ptr(),
           _DTYPES[out.dtype], out_ld)
 
 
@@ -521,7 +521,8 @@ def zs_embed_workspace_bytes(n: int, vocab: int, dim: int) -> int:
 
 
 def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=False, workspace, stream=None):
-    """grad[v] = (0 if first else grad[v]) + scale * sum of dout[i] over tokens[i] == v."""
+    """grad[v] = (0 if first else grad[v]) + scale * sum of dout[i] over tokens[i] == v; ids outside of
+    the table and padding_idx (None or an id outside: none) contribute nothing."""
     dev = _device_index(grad, "grad")
     vocab, dim, grad_ld = _rows2d(grad, "grad", dev)
     n, dout_dim, dout_ld = _rows2d(dout, "dout", dev)
@@ -530,7 +531,7 @@ def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=Fa
         raise ValueError(f"dout has rows of {dout_dim} elements, grad's have {dim}")
     ws, ws_bytes = _workspace(workspace, dev)
     _call("zs_embed_backward", dev, stream, dout.data_ptr(), _DTYPES[dout.dtype], dout_ld, tokens.data_ptr(),
-          itype, n, vocab, dim, padding_idx, scale, grad.data_ptr(), _DTYPES[grad.dtype], grad_ld,
+          itype, n, vocab, dim, -1 if padding_idx is None else int(padding_idx), float(scale), grad.data_ptr(), _DTYPES[grad.dtype], grad_ld,
           1 if first else 0, ws, ws_bytes)
 
 
@@ -550,7 +551,7 @@ def zs_layer_norm_forward(x, weight, bias, y, *, eps=1e-5, mean=None, rstd=None,
     if wdtype not in _DTYPES:
         raise ValueError(f"unsupported weight dtype {wdtype}")
     _call("zs_layer_norm_forward", dev, stream, x.data_ptr(), _DTYPES[x.dtype], x_ld, w, b, _DTYPES[wdtype],
-          rows, dim, eps, y.data_ptr(), y_ld, _vector(mean, "mean", rows, dev, torch.float32),
+          rows, dim, float(eps), y.data_ptr(), y_ld, _vector(mean, "mean", rows, dev, torch.float32),
           _vector(rstd, "rstd", rows, dev, torch.float32))
 
 

@@ -698,13 +698,60 @@ void k_embed_chunks(Keys tokens, const uint32_t* __restrict__ keys, const uint32
   }
 }
 
+// Adds the partial sums at rows 2b, 2(b + 1), ... (count of them) in order.
+template <int VEC>
+__device__ __forceinline__ void add_partials(float* sum, const float* __restrict__ partials, uint32_t pitch, int64_t b,
+                                             int count, uint32_t c, bool live) {
+  constexpr int U = 8;  // on their way at once
+  for (int i = 0; i < count; i += U) {
+    Piece<float, VEC> q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < count && live) q[u].load(partials + 2 * (b + i + u) * (int64_t)pitch + c);
+      else q[u].clear();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[e] += q[u].get(e);
+  }
+}
+
+// With many chunks, a run over very many of them (one token in a large part of a
+// large batch) would leave its join one long chain: first, a wave for each 64
+// chunks (64 g and on) and 64 pieces of columns adds up their partial sums where
+// all of them belong to a run from before, into the first one's place. (131072
+// tokens of one kind, 1024 wide: 103 us instead of 166; all different: 137.7
+// and 137.3. Up to kFoldChunks chunks the chain is no longer than the launch.)
+constexpr int kFold = 64;
+constexpr int64_t kFoldChunks = 256;
+template <int VEC>
+__global__ __launch_bounds__(kThreads)
+void k_embed_fold(const uint32_t* __restrict__ keys, uint32_t vocab, int chunk, int64_t groups, int64_t coltiles,
+                  float* __restrict__ partials, uint32_t pitch) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t wv = wave_id(); wv < groups * coltiles; wv += (int64_t)gridDim.x * (kThreads / 64)) {
+    const int64_t g = quot(wv, coltiles), b = g * kFold;
+    const uint32_t c = ((uint32_t)(wv - g * coltiles) * 64 + lane) * VEC;
+    const uint32_t key = keys[b * chunk];
+    if (key == vocab || b == 0 || keys[b * chunk - 1] != key) continue;
+    if (~__ballot(keys[(b + lane) * chunk] == key)) continue;
+    float sum[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
+    add_partials<VEC>(sum, partials, pitch, b, kFold, c, c < pitch);
+    if (c < pitch) store_piece<float, VEC>(partials + 2 * b * (int64_t)pitch + c, sum);
+  }
+}
+
 // One wave per chunk and 64 pieces of columns: a run that starts in this chunk
-// and goes on in later ones.
+// and goes on in later ones. `groups`: groups of kFold chunks that k_embed_fold
+// has been over.
 template <typename Gt, int VEC>
 __global__ __launch_bounds__(kThreads)
 void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, int chunk, int64_t chunks,
-                  int64_t coltiles, uint32_t dim, float scale, Gt* __restrict__ grad, int64_t grad_ld, int first,
-                  const float* __restrict__ partials, uint32_t pitch) {
+                  int64_t groups, int64_t coltiles, uint32_t dim, float scale, Gt* __restrict__ grad, int64_t grad_ld,
+                  int first, const float* __restrict__ partials, uint32_t pitch) {
   const int lane = threadIdx.x & 63;
   for (int64_t wv = wave_id(); wv < chunks * coltiles; wv += (int64_t)gridDim.x * (kThreads / 64)) {
     const int64_t ch = quot(wv, coltiles);
@@ -723,24 +770,14 @@ void k_embed_join(const uint32_t* __restrict__ keys, int64_t n, uint32_t vocab, 
     float sum[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sum[e] = p.get(e);
-    for (int64_t b = ch + 1; b < chunks; b += 64) {
-      // the next chunks that begin with this key, 64 at a time
-      const uint64_t m = __ballot(b + lane < chunks && keys[(b + lane < chunks ? b + lane : b) * chunk] == key);
+    for (int64_t b = ch + 1; b < chunks;) {
+      // the chunks up to the next group's start that begin with this key
+      const int64_t group = b / kFold, end = (group + 1) * kFold < chunks ? (group + 1) * kFold : chunks;
+      const uint64_t m = __ballot(b + lane < end && keys[(b + lane < end ? b + lane : b) * chunk] == key);
       const int more = ~m ? __builtin_ctzll(~m) : 64;
-      constexpr int U = 8;
-      for (int i = 0; i < more; i += U) {
-        Piece<float, VEC> q[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (i + u < more && live) q[u].load(partials + 2 * (b + i + u) * (int64_t)pitch + c);
-          else q[u].clear();
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sum[e] += q[u].get(e);
-      }
-      if (more < 64) break;
+      add_partials<VEC>(sum, partials, pitch, b, more == kFold && group < groups ? 1 : more, c, live);
+      if (b + more < end) break;
+      b = end;
     }
     put_grad<Gt, VEC>(row, sum, scale, !first, old, c, dim);
   }
@@ -845,10 +882,14 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   };
   if (first) pick(std::true_type{});
   else pick(std::false_type{});
+  const int64_t groups = p.chunks > kFoldChunks ? p.chunks / kFold : 0;
+  if (groups > 0)
+    hipLaunchKernelGGL((k_embed_fold<VEC>), dim3((unsigned)grid_for(groups * coltiles, kThreads / 64)), dim3(kThreads),
+                       0, s, keys[last], (uint32_t)vocab, p.chunk, groups, coltiles, partials, (uint32_t)p.pitch);
   if (p.chunks > 1)
     hipLaunchKernelGGL((k_embed_join<Gt, VEC>), dim3((unsigned)grid_for(items, kThreads / 64)), dim3(kThreads), 0, s,
-                       keys[last], n, (uint32_t)vocab, p.chunk, p.chunks, coltiles, (uint32_t)dim, scale, grad,
-                       grad_ld, (int)first, partials, (uint32_t)p.pitch);
+                       keys[last], n, (uint32_t)vocab, p.chunk, p.chunks, groups, coltiles, (uint32_t)dim, scale,
+                       grad, grad_ld, (int)first, partials, (uint32_t)p.pitch);
 }
 
 }  // namespace

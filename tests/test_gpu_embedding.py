@@ -186,7 +186,7 @@ def test_backward(kind, n, vocab, dim):
 
 
 @pytest.mark.parametrize("n", [4095, 4096, 4097, 16383, 16384, 16385, 40000, 140000])
-@pytest.mark.parametrize("kind", ["mixed", "runs"])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "equal"])
 def test_backward_many_tokens(n, kind):
     # both ways of sorting, around the sizes where one takes over from the other
     g = gen(n)
@@ -324,6 +324,44 @@ def test_backward_offsets_beyond_32_bits():
     grad = torch.empty(rows, dim, device="cuda")
     run_backward(wide, ids, grad, first=True)  # dout's rows that far apart
     assert torch.equal(grad, narrow.float())
+
+
+def test_extreme_sizes():
+    # the largest vocabulary, widest rows and many tokens, each alone
+    last = 2 ** 31 - 2
+    table = torch.zeros(2 ** 31 - 1, 1, device="cuda", dtype=torch.bfloat16)
+    table[last] = 3.0
+    ids = torch.tensor([last, 0, last + 1, 2 ** 40, -(2 ** 40)], device="cuda")
+    out = torch.empty(5, 1, device="cuda")
+    zs.zs_embed_forward(table, ids, out, scale=2.0)
+    assert out[:, 0].tolist() == [6.0, 0.0, 0.0, 0.0, 0.0]
+    run_backward(torch.ones(5, 1, device="cuda"), ids, table, padding_idx=None)
+    assert table[last].item() == 4.0 and table[0].item() == 1.0 and torch.count_nonzero(table) == 2
+    del table
+
+    dim = 2 ** 24 - 1
+    table = torch.randn(2, dim, device="cuda")
+    out = torch.empty(3, dim, device="cuda", dtype=torch.bfloat16)
+    ids = torch.tensor([1, 0, 1], device="cuda", dtype=torch.int32)
+    zs.zs_embed_forward(table, ids, out)
+    assert torch.equal(out, table[ids.long()].bfloat16())
+    grad = torch.empty(2, dim, device="cuda")
+    run_backward(out, ids, grad, first=True)
+    assert torch.equal(grad[1], out[0].float() + out[2].float()) and torch.equal(grad[0], out[1].float())
+
+    n, vocab = 20_000_003, 128256
+    g = gen(20)
+    ids = torch.randint(-3, vocab, (n,), generator=g, device="cuda", dtype=torch.int32)
+    ids[::7] = 11
+    dout = torch.randint(-3, 4, (n, 4), generator=g, device="cuda").float()  # small whole numbers: every sum is exact
+    grad = torch.empty(vocab, 4, device="cuda")
+    run_backward(dout, ids, grad, first=True)
+    keep = ids >= 0
+    order = torch.sort(ids[keep].long()).indices
+    counts = torch.bincount(ids[keep].long(), minlength=vocab)
+    sums = torch.cat([torch.zeros(1, 4, device="cuda", dtype=torch.float64), dout[keep][order].double().cumsum(0)])
+    ends = counts.cumsum(0)
+    assert torch.equal(grad.double(), sums[ends] - sums[ends - counts])
 
 
 def test_two_streams_at_once_and_another_than_the_current():

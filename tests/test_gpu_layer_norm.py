@@ -304,6 +304,31 @@ def test_rows_beyond_32_bits():
     assert torch.equal(bits(dx), bits(dxn)) and torch.equal(dw, dw2) and torch.equal(db, db2)
 
 
+def test_widest_rows_and_many_rows():
+    g = gen(9)
+    dim = 2 ** 24 - 1
+    _, x = matrix(g, 2, dim, "f32", 0, 1.0)
+    _, dy = matrix(g, 2, dim, "f32")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(2, device="cuda"), torch.empty(2, device="cuda")
+    dw, db = torch.empty(dim, device="cuda"), torch.empty(dim, device="cuda")
+    zs.zs_layer_norm_forward(x, None, None, y, mean=mean, rstd=rstd)
+    check_forward(x, None, None, y, mean, rstd, 1e-5)
+    run_backward(dy, x, None, mean, rstd, dx, dw, db, True)
+    check_backward(dy, x, None, mean, rstd, dx, dw, db, None, None)
+    # 40 million rows of two: y is +-1 up to eps, and the gradients' sums of whole numbers are exact
+    rows = 40_000_003
+    x = torch.tensor([[-1.0, 1.0]], device="cuda").repeat(rows, 1)
+    y = torch.empty_like(x)
+    zs.zs_layer_norm_forward(x, None, None, y, eps=0.0)
+    assert torch.equal(y, x)
+    dy = torch.randint(-1, 2, (rows, 2), generator=g, device="cuda").float()
+    ones, zeros = torch.ones(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    dw, db = torch.empty(2, device="cuda"), torch.empty(2, device="cuda")
+    run_backward(dy, x, None, zeros, ones, y, dw, db, True)
+    assert torch.equal(db.double(), dy.double().sum(0)) and torch.equal(dw.double(), (dy * x).double().sum(0))
+
+
 def test_streams_and_graph_replays():
     g = gen(6)
     rows, dim = 900, 1032
