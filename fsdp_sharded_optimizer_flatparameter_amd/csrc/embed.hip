@@ -87,16 +87,19 @@ void k_embed_fwd(const T* __restrict__ table, int64_t vocab, uint32_t dim, int64
 // ---------------------------------------------------------------- zeros
 
 // Stores past the caches from one-wave workgroups with a short piece each keep
-// the most writes on their way: the call that writes 128256 x 4096 bf16 takes
+// the most writes on their way: the call that writes 128256 x 4096 bf16 took
 // 233 us so, 248 with pieces of 8 KiB, 253 with 16 KiB, 240 with 2 KiB, and 250
 // with four-wave workgroups or plain stores.
 constexpr int64_t kFillBytes = 4096;
-// Up to this much of a gradient is zeroed by the first launch of the sort,
-// into all rows, beside the workgroups that sort; above it, after the sort, into the
-// rows that no token selects. 8192 tokens into 8192 x 1024 fp32 (34 MB): 29.3
-// against 31.6 us; 32000 x 1024 (131 MB): 43 against 47; 512 tokens into
-// 128256 x 4096 bf16 (1.05 GB): 210 against 187.
-constexpr int64_t kFillTogether = 200000000;
+// Up to kFillTogether bytes of a gradient are zeroed by the first launch of the
+// sort, in all rows, beside the workgroups that sort; of more, kFillBeside bytes
+// beside each launch, and after the sort the rows of the rest that no token
+// selects. 8192 tokens into 16384 x 1024 fp32 (67 MB): 32.5 us against 37 all after the
+// sort; into 50257 x 768 fp32 (154 MB): 38.3, 44.1 all in the first launch;
+// 16384 into 128256 x 4096 bf16 (1.05 GB): 211, 222 with nothing beside the
+// sort, 216 with 160 MB.
+constexpr int64_t kFillTogether = 100000000;
+constexpr int64_t kFillBeside = 60000000;
 
 // With `first` the rows that no token selects are zero. The table is cut into
 // pieces of about kFillBytes, a wave for each: `step` (up to 64) narrow rows,
@@ -107,15 +110,15 @@ struct Fill {
   int64_t vocab, ld;
   uint32_t dim, width;  // columns of a piece
   int step, across;     // rows of a piece, pieces across a row
-  int64_t total;        // pieces
+  int64_t begin, end;   // pieces to fill
 };
 template <typename Gt>
 Fill<Gt> fill_plan(Gt* grad, int64_t vocab, int64_t dim, int64_t ld) {
   const int64_t row = dim * (int64_t)sizeof(Gt), fit = kFillBytes / row;
   Fill<Gt> f{grad, vocab, ld, (uint32_t)dim, (uint32_t)dim, (int)(fit < 1 ? 1 : fit > 64 ? 64 : fit),
-             (int)((row + kFillBytes - 1) / kFillBytes), 0};
+             (int)((row + kFillBytes - 1) / kFillBytes), 0, 0};
   if (f.across > 1) f.width = kFillBytes / sizeof(Gt);
-  f.total = (vocab + f.step - 1) / f.step * f.across;
+  f.end = (vocab + f.step - 1) / f.step * f.across;
   return f;
 }
 // Piece t, without the rows that `touched` marks (none are where it is null).
@@ -140,7 +143,7 @@ __device__ __forceinline__ void fill_piece(const Fill<Gt>& f, int64_t t, const u
 template <typename Gt>
 __global__ __launch_bounds__(64)
 void k_embed_fill(Fill<Gt> f, const uint8_t* __restrict__ touched) {
-  for (int64_t t = blockIdx.x; t < f.total; t += gridDim.x) fill_piece(f, t, touched);
+  for (int64_t t = f.begin + blockIdx.x; t < f.end; t += gridDim.x) fill_piece(f, t, touched);
 }
 
 // ---------------------------------------------------------------- sort
@@ -344,8 +347,9 @@ void k_sort_scatter(Keys k, const uint32_t* __restrict__ pos_in, int64_t n, int 
 // of these sizes, this 6 us for 8192 entries and 25 for 65536 (the call for
 // 32768 rows of 1024: 80 us either way when the limit was set, 61 now; for
 // 65536 of 768: 120 us instead of 94).
-// The first pass clears `touched`, a byte per row of the gradient, with the
-// workgroups behind the tiles; the last one sets it for each token's row.
+// The first pass clears `touched`, a byte per row of the gradient, with `clears`
+// workgroups behind the tiles; the last one sets it for each token's row. The
+// workgroups behind those fill pieces of the gradient, one for each wave.
 constexpr int kPassBS = 1024;
 constexpr int kPassWaves = kPassBS / 64;
 constexpr int64_t kPassSort = 32768;
@@ -385,7 +389,7 @@ __device__ __forceinline__ void place_digits(uint16_t (*hist)[BINS], int bins, c
 
 template <typename Gt, int MAXB>
 __global__ __launch_bounds__(kPassBS)
-void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int bits, int tiles, int last,
+void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, int bits, int tiles, int clears, int last,
                  uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out, uint8_t* __restrict__ touched,
                  Fill<Gt> fill) {
   // Copies of the counters, each for every so many-th lane and shifted by a
@@ -401,10 +405,13 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if ((int)blockIdx.x >= tiles) {
-    const int64_t b = (int)blockIdx.x - tiles, nb = (int)gridDim.x - tiles;
-    if (touched) clear_touched(touched, k.vocab, b);
-    else
-      for (int64_t t = b * kPassWaves + wave; t < fill.total; t += nb * kPassWaves) fill_piece(fill, t, nullptr);
+    const int b = (int)blockIdx.x - tiles;
+    if (b < clears) {
+      clear_touched(touched, k.vocab, b);
+    } else {
+      const int64_t t = fill.begin + (int64_t)(b - clears) * kPassWaves + wave;
+      if (t < fill.end) fill_piece(fill, t, nullptr);
+    }
     return;
   }
   const int bins = 1 << bits, copies = bins <= 512 ? 8 : 4096 / bins;
@@ -469,9 +476,8 @@ void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys
   __shared__ uint32_t lds[kPassWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
   if (blockIdx.x > 0) {
-    for (int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave; t < fill.total;
-         t += (int64_t)(gridDim.x - 1) * kPassWaves)
-      fill_piece(fill, t, nullptr);
+    const int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave;
+    if (t < fill.end) fill_piece(fill, t, nullptr);
     return;
   }
   const int bins = 1 << bits;
@@ -812,21 +818,29 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
                    int64_t dout_ld, int64_t n, int64_t vocab, int64_t dim, float scale, Gt* grad, int64_t grad_ld, bool first, hipStream_t s) {
   constexpr int VEC = vec_of<Gt>();
   int last = 0;
-  // In a launch of their own the zeros go by marks of the rows that tokens
+  // What is left to a launch of its own goes by marks of the rows that tokens
   // select, which the first pass clears and the last one sets.
-  const Fill<Gt> fill = fill_plan(grad, vocab, dim, grad_ld);
+  Fill<Gt> fill = fill_plan(grad, vocab, dim, grad_ld);
+  const int64_t pieces = first ? fill.end : 0;
   const bool few = n <= kFewTokens;
   const bool together = first && !few && n <= kPassSort && vocab * dim * (int64_t)sizeof(Gt) <= kFillTogether;
-  const int64_t fill_groups = together ? (fill.total + kPassWaves - 1) / kPassWaves : 0;
   uint8_t* mark = first && !few && !together ? touched : nullptr;
   const int passes = mark && p.passes < 2 ? 2 : p.passes;
   const bool wide = p.digit > kBits;
+  fill.end = 0;
+  // The next pieces beside a launch of the sort, a workgroup for every kPassWaves.
+  auto beside = [&](int64_t count) {
+    fill.begin = fill.end;
+    fill.end = fill.begin + count < pieces ? fill.begin + count : pieces;
+    return (fill.end - fill.begin + kPassWaves - 1) / kPassWaves;
+  };
   if (few) {
     // sorted where they are used
   } else if (n <= kPassBS && !mark) {
+    const int64_t fills = beside(pieces);
     auto one = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fill_groups)), dim3(kPassBS), 0, s, tokens,
-                         (int)n, passes, p.digit, keys[0], pos[0], fill);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fills)), dim3(kPassBS), 0, s, tokens, (int)n, passes, p.digit,
+                         keys[0], pos[0], fill);
     };
     if (wide) one(k_sort_one<Gt, kWideBits>);
     else one(k_sort_one<Gt, kBits>);
@@ -839,10 +853,11 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
       const bool final = i + 1 == passes;
       if (n <= kPassSort) {
         const int tiles = (int)((n + kPassBS - 1) / kPassBS);
-        const int64_t more = i > 0 ? 0 : mark ? (vocab + kClearBytes - 1) / kClearBytes : fill_groups;
+        const int clears = i == 0 && mark ? (int)((vocab + kClearBytes - 1) / kClearBytes) : 0;
+        const int64_t fills = beside(together ? pieces : kFillBeside / kFillBytes);
         auto pass = [&](auto kernel) {
-          hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles + more)), dim3(kPassBS), 0, s, k,
-                             pos_in, (int)n, i * p.digit, p.digit, tiles, (int)final, keys[dst], pos[dst], mark, fill);
+          hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles + clears + fills)), dim3(kPassBS), 0, s, k, pos_in, (int)n,
+                             i * p.digit, p.digit, tiles, clears, (int)final, keys[dst], pos[dst], mark, fill);
         };
         if (wide) pass(k_sort_pass<Gt, kWideBits>);
         else pass(k_sort_pass<Gt, kBits>);
@@ -856,8 +871,12 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
       last = dst;
     }
   }
-  if (first && !together)
-    hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(fill.total, 1, 64)), dim3(64), 0, s, fill, mark);
+  if (fill.end < pieces) {
+    fill.begin = fill.end;
+    fill.end = pieces;
+    hipLaunchKernelGGL((k_embed_fill<Gt>), dim3((unsigned)grid_for(fill.end - fill.begin, 1, 64)), dim3(64), 0, s,
+                       fill, mark);
+  }
   if (n == 0) return;
   const int64_t coltiles = (dim + 64 * VEC - 1) / (64 * VEC), items = p.chunks * coltiles;
   auto go = [&](auto kernel) {
