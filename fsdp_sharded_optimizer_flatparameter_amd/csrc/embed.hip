@@ -462,34 +462,48 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
   }
 }
 
-// Up to 1024 entries: all passes in one launch of one workgroup, an entry per
-// thread, keys and positions handed on in LDS. (512 tokens: 12.0 us for the
-// call instead of 15.)
-template <typename Gt, int MAXB>
+// Up to 1024 R entries: all passes in one launch of one workgroup, R entries per
+// thread (a wave's are consecutive, in rounds of 64), keys and positions handed
+// on in LDS. 512 tokens of 768: 12.0 us for the call instead of 15, 2048: 14.8
+// instead of 17.7; with 4 entries per thread 4096 would take 20.1 instead of
+// 20.5, and 18.7 instead of 17.4 where a pass is enough.
+constexpr int64_t kOneSort = 2 * kPassBS;
+template <typename Gt, int MAXB, int R>
 __global__ __launch_bounds__(kPassBS)
 void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
                 Fill<Gt> fill) {
   constexpr int BINS = 1 << MAXB;
   constexpr int D = BINS > kPassBS ? BINS / kPassBS : 1;
   __shared__ uint16_t hist[kPassWaves][BINS];
-  __shared__ uint32_t skey[kPassBS], spos[kPassBS];
+  __shared__ uint32_t skey[R * kPassBS];
+  __shared__ uint16_t spos[R * kPassBS];
   __shared__ uint32_t lds[kPassWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = threadIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (blockIdx.x > 0) {
     const int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave;
     if (t < fill.end) fill_piece(fill, t, nullptr);
     return;
   }
-  const int bins = 1 << bits;
-  uint32_t key, pos = i;
-  k.load<1>(&key, i, 0, n);
+  const int bins = 1 << bits, i0 = wave * (R * 64) + lane;
+  uint32_t key[R], pos[R], rank[R];
+  k.load<R>(key, i0, 64, n);
+#pragma unroll
+  for (int r = 0; r < R; ++r) pos[r] = i0 + r * 64;
   for (int p = 0; p < passes; ++p) {
+    auto digit = [&](int r) { return (key[r] >> (p * bits)) & (bins - 1); };
     for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
-    const uint32_t d = (key >> (p * bits)) & (bins - 1);
-    uint64_t same;
-    const uint32_t rank = rank_in_wave<MAXB>(d, bits, i < n, &same);
     __syncthreads();
-    if (i < n && rank == 0) hist[wave][d] = (uint16_t)__popcll(same);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = i0 + r * 64 < n;
+      uint64_t same;
+      rank[r] = rank_in_wave<MAXB>(digit(r), bits, live, &same);
+      const uint32_t before = hist[wave][digit(r)];  // of the wave's rounds so far
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (live && rank[r] == 0) hist[wave][digit(r)] = (uint16_t)(before + __popcll(same));
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      rank[r] += before;
+    }
     __syncthreads();
     uint32_t sum[D], none[D];
 #pragma unroll
@@ -503,21 +517,27 @@ void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys
     }
     place_digits<BINS>(hist, bins, sum, none, lds);
     __syncthreads();
-    if (i < n) {
-      const uint32_t to = hist[wave][d] + rank;
-      skey[to] = key;
-      spos[to] = pos;
-    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i0 + r * 64 < n) {
+        const uint32_t to = hist[wave][digit(r)] + rank[r];
+        skey[to] = key[r];
+        spos[to] = (uint16_t)pos[r];
+      }
     __syncthreads();
-    if (i < n) {
-      key = skey[i];
-      pos = spos[i];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (i0 + r * 64 < n) {
+        key[r] = skey[i0 + r * 64];
+        pos[r] = spos[i0 + r * 64];
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (i0 + r * 64 < n) {
+      keys_out[i0 + r * 64] = key[r];
+      pos_out[i0 + r * 64] = pos[r];
     }
-  }
-  if (i < n) {
-    keys_out[i] = key;
-    pos_out[i] = pos;
-  }
 }
 
 // ---------------------------------------------------------------- gradient
@@ -836,14 +856,19 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   };
   if (few) {
     // sorted where they are used
-  } else if (n <= kPassBS && !mark) {
+  } else if (n <= kOneSort && !mark) {
     const int64_t fills = beside(pieces);
     auto one = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fills)), dim3(kPassBS), 0, s, tokens, (int)n, passes, p.digit,
                          keys[0], pos[0], fill);
     };
-    if (wide) one(k_sort_one<Gt, kWideBits>);
-    else one(k_sort_one<Gt, kBits>);
+    auto digits = [&](auto r) {
+      constexpr int R = decltype(r)::value;
+      if (wide) one(k_sort_one<Gt, kWideBits, R>);
+      else one(k_sort_one<Gt, kBits, R>);
+    };
+    if (n <= kPassBS) digits(std::integral_constant<int, 1>{});
+    else digits(std::integral_constant<int, 2>{});
   } else {
     for (int i = 0; i < passes; ++i) {
       const int src = (i + 1) & 1, dst = i & 1;

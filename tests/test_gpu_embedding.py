@@ -199,7 +199,7 @@ def test_backward_many_tokens(n, kind):
 
 
 @pytest.mark.parametrize("first", [True, False])
-@pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64, 65, 1023, 1024, 1025, 32767, 32768, 32769])
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64, 65, 1023, 1024, 1025, 2047, 2048, 2049, 32767, 32768, 32769])
 @pytest.mark.parametrize("vocab", [255, 510, 511, 512, 2046, 2047, 2048, 262143, 262144])
 def test_backward_around_the_sorts_limits(n, vocab, first):
     # where the sort changes its launches, its digits and their number
