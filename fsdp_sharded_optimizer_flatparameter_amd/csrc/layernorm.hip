@@ -235,25 +235,29 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
   constexpr int G = LPR < 64 ? LPR : 64;
   constexpr int COLS = LPR * NV * VEC;
   __shared__ float2 sums[2][BS / 64];
-  __shared__ __align__(16) float joined[RPB > 1 ? RPB * COLS : 1];
+  __shared__ __align__(16) float joined[2][RPB > 1 ? RPB * COLS : 4];
   const int l = threadIdx.x % LPR;
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-  Piece<T, VEC> nx[NV], ng[NV];  // the next row is on its way while this one is worked on
-  float mean = 0.0f, rstd = 0.0f, nmean = 0.0f, nrstd = 0.0f;
-  auto fetch = [&](int64_t r) {
+  struct Row {
+    Piece<T, VEC> x[NV], dy[NV];
+    float mean, rstd;
+  };
+  auto fetch = [&](int64_t r, Row& to) {
     if (r < rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        load_cols<T, VEC, NT>(nx[j], x + r * x_ld, col_of<LPR, VEC>(j, l), dim);
-        load_cols<T, VEC, NT>(ng[j], dy + r * dy_ld, col_of<LPR, VEC>(j, l), dim);
+        load_cols<T, VEC, NT>(to.x[j], x + r * x_ld, col_of<LPR, VEC>(j, l), dim);
+        load_cols<T, VEC, NT>(to.dy[j], dy + r * dy_ld, col_of<LPR, VEC>(j, l), dim);
       }
-      nmean = mean_in[r];
-      nrstd = rstd_in[r];
+      to.mean = mean_in[r];
+      to.rstd = rstd_in[r];
     }
   };
   constexpr bool AHEAD = NV == 1;  // two pieces a lane and a row ahead do not fit in 128 registers
-  if (AHEAD) fetch(row);
+  Row next;  // the next row is on its way while this one is worked on
+  next.mean = next.rstd = 0.0f;
+  if (AHEAD) fetch(row, next);
   Piece<W, VEC> wf[NV];
   float dw[NV][VEC], db[NV][VEC];
 #pragma unroll
@@ -266,24 +270,21 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
   // every row group of the workgroup takes the same number of turns (barriers)
   int turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < rows; base += step, row += step, turn ^= 1) {
-    if (!AHEAD) fetch(row);
-    Piece<T, VEC> rx[NV], rg[NV];
+    Row now;
+    if constexpr (AHEAD) now = next;
+    else fetch(row, now);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      wf[j].stay_packed();
-      rx[j] = nx[j];
-      rg[j] = ng[j];
-    }
-    mean = nmean;
-    rstd = nrstd;
+    for (int j = 0; j < NV; ++j) wf[j].stay_packed();
     const bool live = row < rows;
-    if (AHEAD) fetch(row + step);
-    if (ragged(dim, VEC) && row < rows)
+    if (AHEAD) fetch(row + step, next);
+    if (ragged(dim, VEC) && live)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        settle_cols<T, VEC>(rx[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
-        settle_cols<T, VEC>(rg[j], dy + row * dy_ld, col_of<LPR, VEC>(j, l), dim);
+        settle_cols<T, VEC>(now.x[j], x + row * x_ld, col_of<LPR, VEC>(j, l), dim);
+        settle_cols<T, VEC>(now.dy[j], dy + row * dy_ld, col_of<LPR, VEC>(j, l), dim);
       }
+    const float mean = now.mean, rstd = now.rstd;
+    const Piece<T, VEC>*rx = now.x, *rg = now.dy;
     float s1 = 0.0f, s2 = 0.0f;
     if (live) {
 #pragma unroll
@@ -327,24 +328,25 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
   if (!partials) return;  // uniform: an argument
   float* pw = partials + 2 * (int64_t)blockIdx.x * pitch;
   if constexpr (RPB > 1) {
+    const int mine = threadIdx.x / LPR * COLS;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float* mine = joined + threadIdx.x / LPR * COLS;
-      __syncthreads();
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; e += 4)
-          *reinterpret_cast<f32x4*>(mine + (j * LPR + l) * VEC + e) =
-              k ? f32x4{db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]}
-                : f32x4{dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]};
-      __syncthreads();
-      for (uint32_t c = threadIdx.x; c < COLS && c < dim; c += BS) {
-        float t = joined[c];
-#pragma unroll
-        for (int g = 1; g < RPB; ++g) t += joined[g * COLS + c];
-        pw[k * pitch + c] = t;
+      for (int e = 0; e < VEC; e += 4) {
+        const int at = mine + (j * LPR + l) * VEC + e;
+        *reinterpret_cast<f32x4*>(&joined[0][at]) = f32x4{dw[j][e], dw[j][e + 1], dw[j][e + 2], dw[j][e + 3]};
+        *reinterpret_cast<f32x4*>(&joined[1][at]) = f32x4{db[j][e], db[j][e + 1], db[j][e + 2], db[j][e + 3]};
       }
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < COLS && c < dim; c += BS) {
+      float tw = joined[0][c], tb = joined[1][c];
+#pragma unroll
+      for (int g = 1; g < RPB; ++g) {
+        tw += joined[0][g * COLS + c];
+        tb += joined[1][g * COLS + c];
+      }
+      pw[c] = tw;
+      pw[pitch + c] = tb;
     }
   } else {
 #pragma unroll
