@@ -462,82 +462,113 @@ void k_sort_pass(Keys k, const uint32_t* __restrict__ pos_in, int n, int shift, 
   }
 }
 
-// Up to 1024 R entries: all passes in one launch of one workgroup, R entries per
-// thread (a wave's are consecutive, in rounds of 64), keys and positions handed
-// on in LDS. 512 tokens of 768: 12.0 us for the call instead of 15, 2048: 14.8
-// instead of 17.7; with 4 entries per thread 4096 would take 20.1 instead of
-// 20.5, and 18.7 instead of 17.4 where a pass is enough.
-constexpr int64_t kOneSort = 2 * kPassBS;
-template <typename Gt, int MAXB, int R>
+// The whole sort in one launch. Each workgroup takes a range of up to kRangeBins
+// keys: it looks at all entries (they lie in L2), counts those of the ranges
+// before, leaves its own in LDS in their order and sorts these in one pass over
+// the whole of their digits. Entries without a gradient are in no range; the
+// last workgroup writes their keys behind the others. R: rounds of kPassBS
+// entries. The call for 8192 tokens of 768 into 50257 fp32 rows takes 19.7 us
+// against 24.4 with two passes, for 2048 12.9 against 15.1 with both passes in
+// one workgroup, for 16384 into 2048 rows of 1024 29.5 against 32.2.
+// It loses where every workgroup has too much to look at (32768 entries: 49.5
+// against 37.1 with 300 keys, 71 against 48 with 256000), or where there are more
+// of them than run at once: two per CU up to half of kRangeSort, then one for the
+// list's room (16384 entries, 256000 keys: 35.5 against 32.7); and with a table so large
+// that its zeros need the time of two passes beside them (16384 into
+// 128256 x 4096 bf16: 215 against 210).
+constexpr int64_t kRangeSort = 16 * kPassBS;
+constexpr int kRangeBits = 9, kRangeBins = 1 << kRangeBits;
+constexpr int64_t kRanges = 256;  // workgroups before a range gets more keys; 128 and 64: up to 0.3 us more
+constexpr bool by_ranges(int64_t n, int64_t vocab) {
+  return n <= kRangeSort && vocab <= kRangeBins * kRanges * (n <= kRangeSort / 2 ? 2 : 1);
+}
+template <typename Gt, int R>
 __global__ __launch_bounds__(kPassBS)
-void k_sort_one(Keys k, int n, int passes, int bits, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
-                Fill<Gt> fill) {
-  constexpr int BINS = 1 << MAXB;
-  constexpr int D = BINS > kPassBS ? BINS / kPassBS : 1;
-  __shared__ uint16_t hist[kPassWaves][BINS];
-  __shared__ uint32_t skey[R * kPassBS];
-  __shared__ uint16_t spos[R * kPassBS];
-  __shared__ uint32_t lds[kPassWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (blockIdx.x > 0) {
-    const int64_t t = (int64_t)(blockIdx.x - 1) * kPassWaves + wave;
+void k_sort_ranges(Keys k, int n, int bits, int ranges, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ pos_out,
+                   Fill<Gt> fill) {
+  static_assert(R * kPassBS <= 65536, "a position in 16 bits");
+  __shared__ uint32_t list[R * kPassBS];
+  __shared__ __align__(4) uint16_t hist[kPassWaves][kRangeBins];
+  __shared__ uint32_t lds[kPassWaves], within[kPassWaves], under[kPassWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if ((int)blockIdx.x >= ranges) {
+    const int64_t t = fill.begin + (int64_t)((int)blockIdx.x - ranges) * kPassWaves + wave;
     if (t < fill.end) fill_piece(fill, t, nullptr);
     return;
   }
-  const int bins = 1 << bits, i0 = wave * (R * 64) + lane;
-  uint32_t key[R], pos[R], rank[R];
-  k.load<R>(key, i0, 64, n);
+  const int bins = 1 << bits;
+  const uint32_t lo = blockIdx.x << bits, vocab = (uint32_t)k.vocab;
+  const uint32_t room = vocab - lo < (uint32_t)bins ? vocab - lo : (uint32_t)bins;  // keys of the range
+  // a wave's entries are consecutive, so that their order is that of waves, rounds and lanes
+  const int rounds = (n + kPassBS - 1) / kPassBS, i0 = wave * rounds * 64 + lane;
+  uint32_t key[R];
+  constexpr int U = R < 16 ? R : 16;  // entries on their way per thread
 #pragma unroll
-  for (int r = 0; r < R; ++r) pos[r] = i0 + r * 64;
-  for (int p = 0; p < passes; ++p) {
-    auto digit = [&](int r) { return (key[r] >> (p * bits)) & (bins - 1); };
-    for (int b = lane; b < bins; b += 64) hist[wave][b] = 0;
-    __syncthreads();
+  for (int r = 0; r < R; r += U)
+    if (r < rounds) k.load<U>(key + r, i0 + r * 64, 64, n);
+  for (int b = lane; b < bins / 2; b += 64) reinterpret_cast<uint32_t*>(hist[wave])[b] = 0;
+  auto live = [&](int r) { return r < rounds && i0 + r * 64 < n; };
+  int own = 0, less = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool live = i0 + r * 64 < n;
-      uint64_t same;
-      rank[r] = rank_in_wave<MAXB>(digit(r), bits, live, &same);
-      const uint32_t before = hist[wave][digit(r)];  // of the wave's rounds so far
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (live && rank[r] == 0) hist[wave][digit(r)] = (uint16_t)(before + __popcll(same));
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      rank[r] += before;
-    }
-    __syncthreads();
-    uint32_t sum[D], none[D];
+  for (int r = 0; r < R; ++r) {
+    own += __popcll(__ballot(live(r) && key[r] - lo < room));
+    less += __popcll(__ballot(live(r) && key[r] < lo));
+  }
+  if (lane == 0) {
+    within[wave] = own;
+    under[wave] = less;
+  }
+  __syncthreads();
+  int at = 0, count = 0;
+  uint32_t base = 0;
 #pragma unroll
-    for (int q = 0; q < D; ++q) {
-      sum[q] = none[q] = 0;
-      const int b = q * kPassBS + threadIdx.x;
-      if (b < bins) {
-#pragma unroll
-        for (int w = 0; w < kPassWaves; ++w) sum[q] += hist[w][b];
-      }
-    }
-    place_digits<BINS>(hist, bins, sum, none, lds);
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i0 + r * 64 < n) {
-        const uint32_t to = hist[wave][digit(r)] + rank[r];
-        skey[to] = key[r];
-        spos[to] = (uint16_t)pos[r];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (i0 + r * 64 < n) {
-        key[r] = skey[i0 + r * 64];
-        pos[r] = spos[i0 + r * 64];
-      }
+  for (int w = 0; w < kPassWaves; ++w) {
+    if (w < wave) at += within[w];
+    count += within[w];
+    base += under[w];
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (i0 + r * 64 < n) {
-      keys_out[i0 + r * 64] = key[r];
-      pos_out[i0 + r * 64] = pos[r];
+  for (int r = 0; r < R; ++r) {
+    const bool in = live(r) && key[r] - lo < room;
+    const uint64_t m = __ballot(in);
+    if (in) list[at + __popcll(m & ((1ull << lane) - 1))] = (key[r] - lo) << 16 | (uint32_t)(i0 + r * 64);
+    at += __popcll(m);
+  }
+  __syncthreads();
+  const int turns = (count + kPassBS - 1) / kPassBS, j0 = wave * turns * 64 + lane;
+  for (int j = j0, t = 0; t < turns; ++t, j += 64)
+    if (j < count) {
+      const uint32_t d = list[j] >> 16;
+      atomicAdd(reinterpret_cast<uint32_t*>(hist[wave]) + d / 2, 1u << (d % 2 * 16));
     }
+  __syncthreads();
+  uint32_t sum = 0;
+  if ((int)threadIdx.x < bins)
+#pragma unroll
+    for (int w = 0; w < kPassWaves; ++w) sum += hist[w][threadIdx.x];
+  place_digits<kRangeBins>(hist, bins, &sum, &base, lds);
+  __syncthreads();
+  for (int j = j0, t = 0; t < turns; ++t, j += 64) {
+    const bool on = j < count;
+    const uint32_t e = on ? list[j] : 0, d = e >> 16;
+    uint64_t same = __ballot(on);
+    if (same == 0) break;
+    uint32_t rank;
+    if (__ballot(on && d != (uint32_t)__builtin_amdgcn_readfirstlane((int)d)) == 0)  // (lane 0 is on)
+      rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
+    else
+      rank = rank_in_wave<kRangeBits>(d, bits, on, &same);
+    const uint32_t start = hist[wave][d];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (on && rank == 0) hist[wave][d] = (uint16_t)(start + __popcll(same));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (on) {
+      keys_out[start + rank] = lo + d;
+      pos_out[start + rank] = e & 0xffffu;
+    }
+  }
+  if ((int)blockIdx.x == ranges - 1)
+    for (int i = (int)base + count + (int)threadIdx.x; i < n; i += kPassBS) keys_out[i] = vocab;
 }
 
 // ---------------------------------------------------------------- gradient
@@ -856,19 +887,18 @@ void run_embed_bwd(const EmbedPlan& p, const Keys& tokens, uint32_t* const* keys
   };
   if (few) {
     // sorted where they are used
-  } else if (n <= kOneSort && !mark) {
+  } else if (by_ranges(n, vocab) && !mark) {
+    int bits = 3;  // of a range's keys
+    while (bits < kRangeBits && (vocab - 1) >> bits >= kRanges) ++bits;
+    const int ranges = (int)(((vocab - 1) >> bits) + 1);
     const int64_t fills = beside(pieces);
-    auto one = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3((unsigned)(1 + fills)), dim3(kPassBS), 0, s, tokens, (int)n, passes, p.digit,
-                         keys[0], pos[0], fill);
+    auto sort = [&](auto r) {
+      hipLaunchKernelGGL((k_sort_ranges<Gt, decltype(r)::value>), dim3((unsigned)(ranges + fills)), dim3(kPassBS), 0, s,
+                         tokens, (int)n, bits, ranges, keys[0], pos[0], fill);
     };
-    auto digits = [&](auto r) {
-      constexpr int R = decltype(r)::value;
-      if (wide) one(k_sort_one<Gt, kWideBits, R>);
-      else one(k_sort_one<Gt, kBits, R>);
-    };
-    if (n <= kPassBS) digits(std::integral_constant<int, 1>{});
-    else digits(std::integral_constant<int, 2>{});
+    if (n <= 2 * kPassBS) sort(std::integral_constant<int, 2>{});
+    else if (n <= 8 * kPassBS) sort(std::integral_constant<int, 8>{});
+    else sort(std::integral_constant<int, kRangeSort / kPassBS>{});
   } else {
     for (int i = 0; i < passes; ++i) {
       const int src = (i + 1) & 1, dst = i & 1;

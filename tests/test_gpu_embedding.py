@@ -213,6 +213,37 @@ def test_backward_around_the_sorts_limits(n, vocab, first):
     check_backward(dout, tokens, grad, before, 1.0, -1, first)
 
 
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("n", [66, 2047, 2049, 8191, 8192, 8193, 16383, 16385])
+@pytest.mark.parametrize("vocab", [1, 2, 8, 9, 2048, 2049, 65537, 131072, 131073, 262143, 262145])
+def test_backward_around_the_ranges_of_the_sort(n, vocab, first):
+    # where a range of keys grows, the last one is short, and one or two workgroups fit on a compute unit
+    g = gen(n + 3 * vocab)
+    _, dout = matrix(g, n, 2, "f32")
+    tokens = make_tokens(g, n, vocab, "mixed" if vocab % 2 else "distinct", "i32" if n % 2 else "i64")
+    tokens[n // 3: n // 3 + n // 4] = vocab // 2  # one that fills whole waves, and some without a row
+    tokens[n // 2 + n // 4:: 3] = -100
+    tokens[-1], tokens[0] = vocab - 1, 0
+    _, grad = matrix(g, vocab, 2, "f32", fill=float("nan") if first else None)
+    before = grad.clone()
+    run_backward(dout, tokens, grad, first=first)
+    check_backward(dout, tokens, grad, before, 1.0, -1, first)
+
+
+@pytest.mark.parametrize("n", [65, 1500, 2048, 5000, 8192, 12000, 16384])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "equal", "ignored"])
+def test_backward_has_one_order_however_it_is_sorted(n, kind):
+    # a vocabulary too large for the sort by ranges: the same entries, the same sums, bit for bit
+    g = gen(n + 11)
+    _, dout = matrix(g, n, 5, "f32")
+    tokens = make_tokens(g, n, 700, kind, "i64").clamp_(max=699)
+    grads = [torch.zeros(vocab, 5, device="cuda") for vocab in (700, 300001)]
+    for grad in grads:
+        run_backward(dout, tokens, grad)
+    assert torch.equal(bits(grads[0]), bits(grads[1][:700]))
+    assert torch.count_nonzero(grads[1][700:]) == 0
+
+
 def reference_on_the_gpu(dout, tokens, grad_shape, before, scale):
     """The gradient and sum of magnitudes in fp64 (adding in another order is 2^-53 of the magnitudes)."""
     keep = (tokens >= 0) & (tokens < grad_shape[0])
