@@ -94,8 +94,8 @@ constexpr int64_t kFillBytes = 4096;
 // Up to kFillTogether bytes of a gradient are zeroed by the first launch of the
 // sort, in all rows, beside the workgroups that sort; of more, kFillBeside bytes
 // beside each launch, and after the sort the rows of the rest that no token
-// selects. 8192 tokens into 16384 x 1024 fp32 (67 MB): 32.5 us against 37 all after the
-// sort; into 50257 x 768 fp32 (154 MB): 38.3, 44.1 all in the first launch;
+// selects. 8192 tokens into 16384 x 1024 fp32 (67 MB): 26.3 us against 29.9 the second
+// way; into 50257 x 768 fp32 (154 MB): 38.3, 39.0 all in the first launch;
 // 16384 into 128256 x 4096 bf16 (1.05 GB): 211, 222 with nothing beside the
 // sort, 216 with 160 MB.
 constexpr int64_t kFillTogether = 100000000;
