@@ -5,6 +5,7 @@
 
 #include "zs.h"
 #include "zs_launch.hpp"
+#include "zs_launch_rows.hpp"
 
 namespace {
 

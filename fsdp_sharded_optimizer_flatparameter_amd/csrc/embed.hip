@@ -12,6 +12,7 @@
 // token's run ends; a run that crosses chunks leaves one partial sum per chunk,
 // joined in chunk order by a second kernel.
 #include "zs_launch.hpp"
+#include "zs_launch_rows.hpp"
 #include "zs_rows.hpp"
 
 namespace zs {

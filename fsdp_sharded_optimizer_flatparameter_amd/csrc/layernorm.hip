@@ -15,6 +15,7 @@
 // walks over rows. Everything is computed in fp32 and rounded once when it is
 // stored.
 #include "zs_launch.hpp"
+#include "zs_launch_rows.hpp"
 #include "zs_rows.hpp"
 
 namespace zs {
