@@ -4,7 +4,8 @@
 
 Each source is compiled by hipcc in parallel; the objects are linked into
 fsdp_sharded_optimizer_flatparameter_amd/libzs.so, replaced atomically. The
-standalone C-ABI test driver (tests/c/zs_driver) is linked against it.
+standalone C-ABI test drivers (tests/c/zs_driver, zs_rows_driver) are linked
+against it.
 """
 from __future__ import annotations
 
@@ -71,25 +72,27 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    build_driver()
+    for name in DRIVERS:
+        build_driver(name)
     return LIB
 
 
-DRIVER_SRC = os.path.join(ROOT, "tests", "c", "zs_driver.cpp")
-DRIVER = os.path.join(ROOT, "tests", "c", "zs_driver")
+DRIVERS = ("zs_driver", "zs_rows_driver")
 
 
-def build_driver() -> str:
-    """The standalone C-ABI test driver (host code only), linked against the
+def build_driver(name: str) -> str:
+    """A standalone C-ABI test driver (host code only), linked against the
     in-tree libzs.so through a path relative to the binary."""
-    tmp = DRIVER + ".tmp"
-    cmd = [hipcc(), "-O2", "-std=c++17", "-Wall", f"-I{INCLUDE}", DRIVER_SRC, f"-L{PKG}", "-lzs",
+    folder = os.path.join(ROOT, "tests", "c")
+    path = os.path.join(folder, name)
+    tmp = path + ".tmp"
+    cmd = [hipcc(), "-O2", "-std=c++17", "-Wall", f"-I{INCLUDE}", path + ".cpp", f"-L{PKG}", "-lzs",
            "-Wl,-rpath,$ORIGIN/../../fsdp_sharded_optimizer_flatparameter_amd", "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True, cwd=os.path.dirname(DRIVER))
+    res = subprocess.run(cmd, capture_output=True, text=True, cwd=folder)
     if res.returncode != 0:
         raise RuntimeError(f"driver build failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, DRIVER)
-    return DRIVER
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":
