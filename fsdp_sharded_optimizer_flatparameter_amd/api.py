@@ -449,6 +449,12 @@ def _vector(t, name, n, dev, dtype=None):
     return t.data_ptr()
 
 
+def _int64(v):
+    """An integer as the library's 64-bit type, the nearest one where it does not fit: ctypes would
+    drop its upper bits, which makes an id of a table or a size that is accepted out of it."""
+    return max(-2 ** 63, min(2 ** 63 - 1, int(v)))
+
+
 def _device_index(t, name):
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
@@ -517,7 +523,7 @@ def zs_embed_forward(table, tokens, out, *, scale=1.0, pos_table=None, positions
 
 
 def zs_embed_workspace_bytes(n: int, vocab: int, dim: int) -> int:
-    return int(_lib().zs_embed_workspace_bytes(int(n), int(vocab), int(dim)))
+    return int(_lib().zs_embed_workspace_bytes(_int64(n), _int64(vocab), _int64(dim)))
 
 
 def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=False, workspace, stream=None):
@@ -531,8 +537,8 @@ def zs_embed_backward(dout, tokens, grad, *, scale=1.0, padding_idx=-1, first=Fa
         raise ValueError(f"dout has rows of {dout_dim} elements, grad's have {dim}")
     ws, ws_bytes = _workspace(workspace, dev)
     _call("zs_embed_backward", dev, stream, dout.data_ptr(), _DTYPES[dout.dtype], dout_ld, tokens.data_ptr(),
-          itype, n, vocab, dim, -1 if padding_idx is None else int(padding_idx), float(scale), grad.data_ptr(), _DTYPES[grad.dtype], grad_ld,
-          1 if first else 0, ws, ws_bytes)
+          itype, n, vocab, dim, -1 if padding_idx is None else _int64(padding_idx), float(scale), grad.data_ptr(),
+          _DTYPES[grad.dtype], grad_ld, 1 if first else 0, ws, ws_bytes)
 
 
 def zs_layer_norm_forward(x, weight, bias, y, *, eps=1e-5, mean=None, rstd=None, stream=None):
@@ -556,7 +562,7 @@ def zs_layer_norm_forward(x, weight, bias, y, *, eps=1e-5, mean=None, rstd=None,
 
 
 def zs_layer_norm_workspace_bytes(rows: int, dim: int) -> int:
-    return int(_lib().zs_layer_norm_workspace_bytes(int(rows), int(dim)))
+    return int(_lib().zs_layer_norm_workspace_bytes(_int64(rows), _int64(dim)))
 
 
 def zs_layer_norm_backward(dy, x, weight, mean, rstd, dx, *, dweight=None, dbias=None, first=False,
