@@ -98,7 +98,8 @@ constexpr int64_t kFillBytes = 4096;
 // selects. 8192 tokens into 16384 x 1024 fp32 (67 MB): 26.3 us against 29.9 the second
 // way; into 50257 x 768 fp32 (154 MB): 38.3, 39.0 all in the first launch;
 // 16384 into 128256 x 4096 bf16 (1.05 GB): 211, 222 with nothing beside the
-// sort, 216 with 160 MB.
+// sort, 216 with 160 MB. (Counted in pieces of kFillBytes: less where rows
+// below 64 bytes make them smaller.)
 constexpr int64_t kFillTogether = 100000000;
 constexpr int64_t kFillBeside = 60000000;
 
@@ -154,7 +155,8 @@ void k_embed_fill(Fill<Gt> f, const uint8_t* __restrict__ touched) {
 // vocabulary, or the padding token) is `vocab`, behind all others.
 constexpr int kBits = 9;
 // In the passes of up to kPassSort entries also of up to kWideBits, where that
-// saves a pass: position tables of up to 2047 rows, small vocabularies.
+// saves a pass: vocabularies of 2^9 to 2^11 (one pass), of 2^18 to 2^22 (two) and
+// from 2^27 (three), as far as the sort by ranges does not take them.
 constexpr int kWideBits = 11;
 constexpr int kBins = 1 << kBits;
 constexpr int kSortRounds = 8;

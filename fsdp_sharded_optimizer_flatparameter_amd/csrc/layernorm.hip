@@ -13,7 +13,9 @@
 // LPR lanes that own it (16 lanes, one wave, or several waves of a workgroup),
 // so each element is read once; weights are read once per workgroup, which
 // walks over rows. Everything is computed in fp32 and rounded once when it is
-// stored.
+// stored. Means are products with 1 / dim, one rounding more than quotients: a
+// row's three quotients in each of its lanes would take 93 instead of 88 us for
+// 16384 bf16 rows of 8192, the backward's two 77 instead of 73 for 16384 of 4096.
 #include "zs_launch.hpp"
 #include "zs_launch_rows.hpp"
 #include "zs_rows.hpp"
@@ -194,9 +196,10 @@ constexpr int kLongBS = 1024;
 constexpr int kMaxParts = 256;  // partial sums of the backward pass: a workgroup of 16 waves per CU
 
 // Rows longer than the registers of 1024 lanes hold (four pieces a lane: 32768
-// bf16, 16384 fp32): one workgroup walks over the row three times (sum, squared
-// distances, output); the second and third reading find most of it in the
-// caches. (4096 rows of 16384 fp32 took 143 us so, 95 in registers.)
+// bf16, 16384 fp32; two where bf16 rows have fp32 weights: 16384): one workgroup
+// walks over the row three times (sum, squared distances, output); the second
+// and third reading find most of it in the caches. (4096 rows of 16384 fp32 took
+// 143 us so, 95 in registers.)
 template <typename T, typename W, int VEC>
 __global__ __launch_bounds__(kLongBS)
 void k_ln_fwd_long(const T* __restrict__ x, int64_t x_ld, const W* __restrict__ w, const W* __restrict__ b,
@@ -287,7 +290,10 @@ void k_ln_bwd(const T* __restrict__ dy, int64_t dy_ld, const T* __restrict__ x, 
       to.rstd = rstd_in[r];
     }
   };
-  constexpr bool AHEAD = NV == 1;  // two pieces a lane and a row ahead do not fit in 128 registers
+  // Two pieces a lane and a row ahead do not fit in 128 registers for bf16 rows. For
+  // fp32 rows they do (112), to no clear end: 8192 rows of 8192 took 144 us so
+  // and 143 without, of 6144 104 and 108.
+  constexpr bool AHEAD = NV == 1;
   Row next;  // the next row is on its way while this one is worked on
   next.mean = next.rstd = 0.0f;
   if (AHEAD) fetch(row, next);
@@ -551,7 +557,9 @@ void run_fwd(const T* x, int64_t x_ld, const W* w, const W* b, int64_t rows, int
   // fewer waves that have to meet (16384 rows of 4096 bf16: 48.5 us on 256
   // lanes, 52.7 on 512; 16384 of 1024: 12.5 on 64, 14.1 on 128; 8192 of 768
   // fp32: 9.1 on 64, 11.8 on 256; 16384 of 8192 bf16: 93 on 512 and on 256,
-  // 122 on 1024).
+  // 122 on 1024). Four pieces of bf16 rows with bf16 weights spill 4 registers, and
+  // are faster all the same: 90 us for 4096 rows of 28672, where the walk takes
+  // over 140.
   if (nvec <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   else if (nvec <= 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (nvec <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
@@ -592,6 +600,10 @@ int run_bwd(const T* dy, int64_t dy_ld, const T* x, int64_t x_ld, const W* w, co
     else launch(k_ln_bwd<T, W, LPR, NV, VEC, BS, false>);
   };
   using std::integral_constant;
+  // The columns' sums come on top of the rows: two pieces of bf16 rows spill 10 registers
+  // (2 with fp32 weights), four of fp32 rows 5 (15 with bf16 weights). 8192 rows
+  // of 12288 bf16 take 148 us (1.6 times their floor), and 4096 rows of 16384 fp32
+  // half of what the walk takes.
   if (nvec <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
   else if (nvec <= 32) go(integral_constant<int, 32>{}, integral_constant<int, 1>{});
   else if (nvec <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
