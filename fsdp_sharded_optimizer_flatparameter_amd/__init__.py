@@ -26,6 +26,9 @@ from .api import (  # noqa: F401
     zs_layer_norm_backward,
     zs_layer_norm_forward,
     zs_layer_norm_workspace_bytes,
+    zs_linear_cross_entropy_backward,
+    zs_linear_cross_entropy_forward,
+    zs_linear_cross_entropy_workspace_bytes,
     zs_pack_shard,
     zs_pack_shard_dim0,
     zs_reduce_grads,

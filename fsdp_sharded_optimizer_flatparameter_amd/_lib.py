@@ -88,6 +88,15 @@ SIGNATURES = {
                                            C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
                                            C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p,
                                            C.c_size_t, C.c_void_p]),
+    "zs_linear_cross_entropy_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_int32]),
+    "zs_linear_cross_entropy_forward": (C.c_int32, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64,
+                                                    C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,
+                                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "zs_linear_cross_entropy_backward": (C.c_int32, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64,
+                                                     C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p, C.c_float,
+                                                     C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                                     C.c_void_p, C.c_int32, C.c_int64, C.c_int32, C.c_void_p,
+                                                     C.c_size_t, C.c_void_p]),
     "zs_status_string": (C.c_char_p, [C.c_int32]),
     "zs_version": (C.c_int32, []),
 }

@@ -597,5 +597,66 @@ def zs_layer_norm_backward(dy, x, weight, mean, rstd, dx, *, dweight=None, dbias
           _DTYPES[gdtype], 1 if first else 0, ws, ws_bytes)
 
 
+# ---------------------------------------------------------------- loss over a vocabulary
+
+def _float_code(dtype, name):
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported {name} {dtype}")
+    return _DTYPES[dtype]
+
+
+def zs_linear_cross_entropy_workspace_bytes(n: int, vocab: int, dim: int, dtype, grad_dtype=None) -> int:
+    """Workspace of the backward pass with a dweight of `grad_dtype`, or (None) of the forward pass,
+    for hidden states and weight of `dtype` (torch dtypes)."""
+    return int(_lib().zs_linear_cross_entropy_workspace_bytes(
+        _int64(n), _int64(vocab), _int64(dim), _float_code(dtype, "dtype"),
+        -1 if grad_dtype is None else _float_code(grad_dtype, "grad_dtype")))
+
+
+def _head(hidden, weight, labels):
+    """What both passes read: device, sizes, strides and the labels' type."""
+    dev = _device_index(weight, "weight")
+    vocab, dim, weight_ld = _rows2d(weight, "weight", dev)
+    n, hidden_dim, hidden_ld = _rows2d(hidden, "hidden", dev)
+    itype = _ids(labels, "labels", n if hidden_dim else None, dev)
+    if hidden_dim != dim:
+        raise ValueError(f"hidden has rows of {hidden_dim} elements, weight's have {dim}")
+    if hidden.dtype != weight.dtype:
+        raise ValueError("hidden and weight must have one dtype")
+    return dev, n, vocab, dim, hidden_ld, weight_ld, itype
+
+
+def zs_linear_cross_entropy_forward(hidden, weight, labels, loss, *, lse=None, workspace, stream=None):
+    """loss[i] = log(sum_v exp(z_iv)) - z_i,labels[i] for z = hidden @ weight.T, without keeping z; 0 for
+    tokens whose label is outside of the vocabulary. lse (the first term) is written where given."""
+    dev, n, vocab, dim, hidden_ld, weight_ld, itype = _head(hidden, weight, labels)
+    if loss is None:
+        raise ValueError("loss must be a device tensor")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("zs_linear_cross_entropy_forward", dev, stream, hidden.data_ptr(), hidden_ld, _DTYPES[hidden.dtype],
+          weight.data_ptr(), weight_ld, labels.data_ptr(), itype, n, vocab, dim,
+          _vector(loss, "loss", n, dev, torch.float32), _vector(lse, "lse", n, dev, torch.float32), ws, ws_bytes)
+
+
+def zs_linear_cross_entropy_backward(hidden, weight, labels, lse, dhidden, dweight, *, dloss=None, scale=1.0,
+                                     first=False, workspace, stream=None):
+    """dhidden, and (0 if first else the old value) + the head's gradient in dweight, for a loss whose
+    gradient is scale * dloss[i] for token i (dloss None: ones); lse is the forward pass's."""
+    dev, n, vocab, dim, hidden_ld, weight_ld, itype = _head(hidden, weight, labels)
+    dh_rows, dh_dim, dh_ld = _rows2d(dhidden, "dhidden", dev)
+    dw_rows, dw_dim, dw_ld = _rows2d(dweight, "dweight", dev)
+    if dh_rows != n or dh_dim != dim or dhidden.dtype != hidden.dtype:
+        raise ValueError("dhidden must have hidden's rows, width and dtype")
+    if dw_rows != vocab or dw_dim != dim:
+        raise ValueError("dweight must have weight's rows and width")
+    if lse is None:
+        raise ValueError("lse is that of the forward pass")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("zs_linear_cross_entropy_backward", dev, stream, hidden.data_ptr(), hidden_ld, _DTYPES[hidden.dtype],
+          weight.data_ptr(), weight_ld, labels.data_ptr(), itype, _vector(lse, "lse", n, dev, torch.float32),
+          _vector(dloss, "dloss", n, dev, torch.float32), float(scale), n, vocab, dim, dhidden.data_ptr(), dh_ld,
+          dweight.data_ptr(), _DTYPES[dweight.dtype], dw_ld, 1 if first else 0, ws, ws_bytes)
+
+
 def zs_version() -> int:
     return int(_lib().zs_version())

@@ -34,7 +34,7 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
           "-ffp-contract=off"]
 
 SOURCES = ["abi.cpp", "tuning.cpp", "reduce.hip", "adamw.hip", "fused.hip", "accumulate.hip",
-           "segments.hip", "embed.hip", "layernorm.hip"]
+           "segments.hip", "embed.hip", "layernorm.hip", "head_loss.hip"]
 
 
 def hipcc() -> str:

@@ -5,6 +5,7 @@
 
 #include "zs.h"
 #include "zs_launch.hpp"
+#include "zs_launch_head.hpp"
 #include "zs_launch_rows.hpp"
 
 namespace {
@@ -104,6 +105,13 @@ bool any_overlap(const Span& a, const Span* b, int n) {
   for (int i = 0; i < n; ++i)
     if (overlaps(a.p, a.bytes, b[i].p, b[i].bytes)) return true;
   return false;
+}
+
+// Sizes of the loss over a vocabulary: 256 rows of three planes within 32 bits of
+// offset, a grid of tiles within 31 bits.
+inline bool head_size_ok(int64_t n, int64_t vocab, int64_t dim) {
+  return count_ok(n) && count_ok(vocab) && dim >= 0 && dim <= (1 << 20) &&
+         (vocab / 128 + 1) * (n / 128 + 1) <= INT32_MAX;
 }
 
 }  // namespace
@@ -596,6 +604,75 @@ zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, i
   return launch([&] {
     return zs::launch_layer_norm_backward(dy, dy_ld, x, x_ld, dtype, weight, wdtype, mean, rstd, rows, dim, dx, dx_ld,
                                           dweight, dbias, grad_dtype, first != 0, workspace, stream);
+  });
+}
+
+size_t zs_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
+                                               int32_t grad_dtype) {
+  if (!float_type(dtype) || (grad_dtype != -1 && !float_type(grad_dtype)) || !head_size_ok(n, vocab, dim)) return 0;
+  return (size_t)zs::head_plan(n, vocab, dim, dtype, grad_dtype).bytes;
+}
+
+zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld, int32_t dtype,
+                                          const void* weight, int64_t weight_ld, const void* labels,
+                                          int32_t index_type, int64_t n, int64_t vocab, int64_t dim,
+                                          float* loss, float* lse, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream) {
+  if (!float_type(dtype) || !index_type_ok(index_type)) return ZS_ERR_DTYPE;
+  if (!head_size_ok(n, vocab, dim) || (n > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(n, dim, hidden_ld) || !stride_ok(vocab, dim, weight_ld)) return ZS_ERR_SIZE;
+  if (n == 0) return ZS_OK;
+  if (!hidden || (vocab > 0 && !weight) || !labels || !loss) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), is = (uintptr_t)index_size(index_type);
+  if (!aligned(hidden, es) || !aligned(weight, es) || !aligned(labels, is) || !aligned(loss, 4) || !aligned(lse, 4))
+    return ZS_ERR_ALIGN;
+  const size_t need = zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype, -1);
+  if (!workspace || workspace_bytes < need) return ZS_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
+  const Span in[3] = {rows_span(hidden, n, dim, hidden_ld, dtype), rows_span(weight, vocab, dim, weight_ld, dtype),
+                      {labels, n * (int64_t)is}};
+  const Span out[3] = {{loss, n * 4}, {lse, lse ? n * 4 : 0}, {workspace, (int64_t)need}};
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(out[i], in, 3) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_head_forward(hidden, hidden_ld, dtype, weight, weight_ld, labels, index_type, n, vocab, dim, loss,
+                                   lse, workspace, stream);
+  });
+}
+
+zs_status zs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_ld, int32_t dtype,
+                                           const void* weight, int64_t weight_ld, const void* labels,
+                                           int32_t index_type, const float* lse, const float* dloss,
+                                           float scale, int64_t n, int64_t vocab, int64_t dim,
+                                           void* dhidden, int64_t dhidden_ld, void* dweight,
+                                           int32_t grad_dtype, int64_t dweight_ld, int32_t first,
+                                           void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(grad_dtype) || !index_type_ok(index_type)) return ZS_ERR_DTYPE;
+  if (!head_size_ok(n, vocab, dim) || (n > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(n, dim, hidden_ld) || !stride_ok(vocab, dim, weight_ld) || !stride_ok(n, dim, dhidden_ld) ||
+      !stride_ok(vocab, dim, dweight_ld))
+    return ZS_ERR_SIZE;
+  if (!std::isfinite(scale)) return ZS_ERR_HPARAM;
+  if (n == 0 && (!first || vocab == 0 || dim == 0)) return ZS_OK;
+  if ((n > 0 && (!hidden || !labels || !lse || !dhidden)) || (vocab > 0 && (!weight || !dweight))) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), is = (uintptr_t)index_size(index_type);
+  if (!aligned(hidden, es) || !aligned(weight, es) || !aligned(dhidden, es) || !aligned(labels, is) ||
+      !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dweight, (uintptr_t)elem_size(grad_dtype)))
+    return ZS_ERR_ALIGN;
+  const bool scratch = n > 0 && vocab > 0;  // otherwise zeros are written, and nothing else
+  const size_t need = scratch ? zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype, grad_dtype) : 0;
+  if (scratch && (!workspace || workspace_bytes < need)) return ZS_ERR_WORKSPACE;
+  if (scratch && !aligned(workspace, 16)) return ZS_ERR_ALIGN;
+  const Span in[5] = {rows_span(hidden, n, dim, hidden_ld, dtype), rows_span(weight, vocab, dim, weight_ld, dtype),
+                      {labels, n * (int64_t)is}, {lse, n * 4}, {dloss, dloss ? n * 4 : 0}};
+  const Span out[3] = {rows_span(dhidden, n, dim, dhidden_ld, dtype),
+                       rows_span(dweight, vocab, dim, dweight_ld, grad_dtype), {workspace, (int64_t)need}};
+  for (int i = 0; i < 3; ++i)
+    if (any_overlap(out[i], in, 5) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_head_backward(hidden, hidden_ld, dtype, weight, weight_ld, labels, index_type, lse, dloss, scale,
+                                    n, vocab, dim, dhidden, dhidden_ld, dweight, grad_dtype, dweight_ld, first != 0,
+                                    workspace, stream);
   });
 }
 

@@ -1,0 +1,682 @@
+// Softmax cross entropy of a large vocabulary from the hidden states h_i and the
+// head's rows w_v, and its gradients, without keeping the logits:
+//
+//   z_iv = h_i . w_v,  lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_i,label_i
+//   g_iv = c_i (exp(z_iv - lse_i) - [v = label_i])      (c_i: the gradient of loss_i)
+//   dh_i = sum_v g_iv w_v,  dw_v = sum_i g_iv h_i
+//
+// All four sums are products on the matrix units (2 n vocab dim operations
+// each; the backward pass makes the logits again), which bound both passes for
+// more than some hundred tokens; below, reading the head does. The forward's
+// tiles leave the maximum and the sum of exponentials of their 128 or 256 rows
+// of the head for each token, which a second kernel joins. The backward takes a
+// piece of the vocabulary at a time: its g goes to the workspace, from which the
+// products for dh (added up in fp32 over the pieces) and for these rows' dw are
+// made.
+//
+// Tokens whose label is outside of the vocabulary count nowhere: those that
+// count are moved together first, so the others cost nothing, and nothing that
+// their hidden states hold reaches a sum.
+//
+// Rounding: bf16 products are exact and added in fp32. g is rounded to bf16 for
+// gradients in bf16, which are rounded as much themselves; for an fp32
+// gradient of a bf16 head it is a sum of two bf16 (17 bits), and all three
+// operands of an fp32 head are sums of three (24 bits), whose products below
+// 2^-24 of the largest are left out.
+#include <type_traits>
+
+#include "zs_gemm.hpp"
+#include "zs_launch.hpp"
+#include "zs_launch_head.hpp"
+#include "zs_rows.hpp"
+
+namespace zs {
+namespace {
+
+using Wide = GemmShape<256, 256, 2, 4>;
+using Square = GemmShape<128, 128, 2, 2>;
+using Narrow = GemmShape<256, 64, 4, 1>;  // at most 64 tokens: the head's rows stream past them
+
+constexpr Segments kOne{1, 0, 0};
+constexpr Segments kTwo{2, 0x00, 0x10};             // one plane times two
+constexpr Segments kThree{3, 0x100, 0x010};         // 2 x 2 planes without the last
+constexpr Segments kSix{6, 0x201100, 0x021010};     // 3 x 3 planes, those above 2^-24
+
+// What is kept of each token that counts, in the order in which they are moved
+// together: its label (-1: none), the gradient of its loss, its log sum of
+// exponentials and its row. inverse: the place of row i, -1 where it does not
+// count.
+struct Tokens {
+  int32_t *label, *map, *inverse, *count;
+  float *coef, *lse;
+};
+
+// ---------------------------------------------------------------- tokens
+
+constexpr int kTokBS = 1024;
+
+// One workgroup walks over the labels and numbers those that count (or, with
+// `gather` 0, keeps every row where it is). Rows that do not count get zeros in
+// loss and lse_out where given. Places behind the last one, up to a multiple of
+// 64, get a gradient of zero.
+template <typename I>
+__global__ __launch_bounds__(kTokBS)
+void k_tokens(const I* __restrict__ labels, int64_t n, int64_t vocab, int gather, const float* __restrict__ lse_in,
+              const float* __restrict__ dloss, float scale, Tokens t, float* __restrict__ loss,
+              float* __restrict__ lse_out) {
+  __shared__ int waves[2][kTokBS / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int base = 0, turn = 0;
+  for (int64_t at = 0; at < n; at += kTokBS, turn ^= 1) {
+    const int64_t i = at + threadIdx.x;
+    const int64_t id = i < n ? (int64_t)labels[i] : -1;
+    const bool counts = id >= 0 && id < vocab, takes = gather ? counts : i < n;
+    const uint64_t mask = __ballot(takes);
+    if (lane == 0) waves[turn][wave] = __popcll(mask);
+    __syncthreads();  // the other turn's entries are read by nobody any more
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kTokBS / 64; ++w) {
+      const int c = waves[turn][w];
+      before += w < wave ? c : 0;
+      all += c;
+    }
+    const int place = base + before + __popcll(mask & ((1ull << lane) - 1));
+    if (takes) {
+      t.label[place] = counts ? (int32_t)id : -1;
+      t.map[place] = (int32_t)i;
+      if (lse_in) {
+        t.lse[place] = lse_in[i];
+        t.coef[place] = counts ? (dloss ? scale * dloss[i] : scale) : 0.0f;
+      }
+    }
+    if (i < n) {
+      t.inverse[i] = counts ? place : -1;
+      if (!counts && loss) loss[i] = 0.0f;
+      if (!counts && lse_out) lse_out[i] = 0.0f;
+    }
+    base += all;
+  }
+  if (threadIdx.x == 0) *t.count = base;
+}
+
+// ---------------------------------------------------------------- layout
+
+__device__ __forceinline__ uint32_t bits_hi(uint32_t a, uint32_t b) {  // upper halves of a (low) and b (high)
+  return (a >> 16) | (b & 0xffff0000u);
+}
+
+// A value as three bf16 in the upper halves of p: the first cut off (a rounded one could overflow), the
+// others what is left, rounded: 24 bits together. Infinities and NaN are whole in the first.
+__device__ __forceinline__ void three_planes(float x, uint32_t (&p)[3]) {
+  const uint32_t u = __float_as_uint(x);
+  const bool whole = (u & 0x7f800000u) == 0x7f800000u;
+  p[0] = whole && (u & 0x007fffffu) ? u | 0x00400000u : u & 0xffff0000u;  // a NaN stays one without its lower half
+  const float r1 = whole ? 0.0f : x - __uint_as_float(u & 0xffff0000u);
+  p[1] = pack_bf16(r1, r1) & 0xffff0000u;
+  const float r2 = r1 - __uint_as_float(p[1]);
+  p[2] = pack_bf16(r2, r2) & 0xffff0000u;
+}
+
+// Rows of `dim` elements as bf16 planes of `dp` elements each, zeros behind dim.
+// With `map`, row r is row map[r] of the source, for r below *count, and zeros
+// for the rows up to the next multiple of 64.
+template <typename T>
+__global__ __launch_bounds__(kThreads)
+void k_layout(const T* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows, uint16_t* __restrict__ dst, int64_t dp,
+              const int32_t* __restrict__ map, const int32_t* __restrict__ count) {
+  constexpr int PLANES = sizeof(T) == 4 ? 3 : 1;
+  const int64_t per = dp / 8;  // pieces of a row
+  const int64_t live = count ? *count : rows, all = count ? (live + 63) / 64 * 64 : rows;
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < all * per; at += (int64_t)gridDim.x * kThreads) {
+    const int64_t r = at / per;
+    const uint32_t c = (uint32_t)(at % per) * 8;
+    Piece<T, 8> p;
+    p.clear();
+    if (r < live) take_cols<T, 8>(p, src + (map ? (int64_t)map[r] : r) * ld, c, dim);
+    uint16_t* to = dst + r * dp * PLANES + c;
+    if constexpr (sizeof(T) == 2) {
+      st16(u32x4{p.r[0], p.r[1], p.r[2], p.r[3]}, to);
+    } else {
+      uint32_t v[8][3];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) three_planes(p.get(e), v[e]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        st16(u32x4{bits_hi(v[0][k], v[1][k]), bits_hi(v[2][k], v[3][k]), bits_hi(v[4][k], v[5][k]),
+                   bits_hi(v[6][k], v[7][k])}, to + k * dp);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+
+// Which tile a workgroup takes. Workgroups go round robin over the 8 XCDs, each
+// with an L2 of its own: an XCD takes tiles that lie together, four rows of
+// tiles deep, so that its workgroups share both operands' panels.
+struct Tile {
+  int64_t m, n;
+};
+__device__ __forceinline__ Tile tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn) {
+  constexpr uint32_t DEEP = 4;
+  const uint32_t xcd = id & 7, per = total >> 3, rest = total & 7;
+  const uint32_t at = xcd * per + (xcd < rest ? xcd : rest) + (id >> 3);
+  const uint32_t g = at / (DEEP * tn), in = at % (DEEP * tn);
+  const uint32_t deep = tm - g * DEEP < DEEP ? tm - g * DEEP : DEEP;
+  return Tile{g * DEEP + in % deep, in / deep};
+}
+
+template <class S>
+__device__ __forceinline__ void clear(typename S::Acc& acc) {
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+__device__ __forceinline__ float join4(float x, bool take_max) {  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float a0 = __uint_as_float(a[0]), a1 = __uint_as_float(a[1]);
+  x = take_max ? fmaxf(a0, a1) : a0 + a1;
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const float b0 = __uint_as_float(b[0]), b1 = __uint_as_float(b[1]);
+  return take_max ? fmaxf(b0, b1) : b0 + b1;
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// Rows of the tile are rows of the head, columns tokens: a lane holds 4 TM
+// logits of each of its TN tokens.
+template <class S, bool GRAD>
+__global__ __launch_bounds__(S::THREADS)
+void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, uint32_t tm, uint32_t tn, int64_t v0, int64_t vocab,
+              Tokens tok, float2* __restrict__ parts, float* __restrict__ own, int64_t np, uint16_t* __restrict__ g,
+              int64_t gp, int gplanes) {
+  __shared__ __align__(1024) char lds[S::LDS];
+  const Tile at = tile_of(blockIdx.x, gridDim.x, tm, tn);
+  const int64_t count = *tok.count;
+  if (at.n * S::BN >= (GRAD ? (count + 63) / 64 * 64 : count)) return;  // uniform
+  typename S::Acc acc;
+  clear<S>(acc);
+  gemm_tile<S, K_IN_ROWS, K_IN_ROWS>(w, h, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps, lds, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
+  const int q4 = (lane >> 4) * 4;
+  const int row0 = wm * (S::BM / S::WM);                    // of the wave in the tile
+  const int64_t in_piece = at.m * S::BM + row0 + q4;        // of acc[0][.][0], from v0 on
+  const int left = (int)(w.rows - in_piece);                // rows of the head there are from it on
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) {
+    const int col = wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+    const int64_t token = at.n * S::BN + col;
+    const bool live = token < count;
+    const int label = live ? tok.label[token] : -1;
+    const int mine = label >= 0 ? (int)(label - v0 - in_piece) : -1;  // the label's place among the lane's rows
+    if constexpr (!GRAD) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + r < left) top = fmaxf(top, acc[i][j][r]);
+      top = join4(top, true);
+      const float from = top == -INFINITY ? 0.0f : top;  // no row, or none above it: exp(-inf) = 0, not of -inf + inf
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float z = acc[i][j][r];
+          if (16 * i + r < left) sum += exp_of(z - from);
+          if (mine == 16 * i + r) own[token] = z;
+        }
+      sum = join4(sum, false);
+      if (S::WM == 1) {
+        if (q4 == 0 && live) parts[at.m * np + token] = float2{top, sum};
+      } else {
+        float2* mine_of = reinterpret_cast<float2*>(lds) + wm * S::BN;  // behind the barrier below
+        if (j == 0) __syncthreads();  // nobody reads the last stage any more
+        if (q4 == 0) mine_of[col] = float2{top, sum};
+      }
+    } else {
+      const float lse = live ? tok.lse[token] : 0.0f, coef = live ? tok.coef[token] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i) {
+        const int64_t v = in_piece + 16 * i;
+        float d[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float p = exp_of(acc[i][j][r] - lse);
+          const float e = mine == 16 * i + r ? p - 1.0f : p;
+          d[r] = live && label >= 0 && 16 * i + r < left ? coef * e : 0.0f;
+        }
+        if (token < np && v < gp) {
+          uint16_t* to = g + token * gp * gplanes + v;
+          uint32_t lo[2], hi[2];
+          if (gplanes < 3) {
+            hi[0] = pack_bf16(d[0], d[1]);
+            hi[1] = pack_bf16(d[2], d[3]);
+            *(uint2*)to = uint2{hi[0], hi[1]};
+            if (gplanes == 2) {
+              lo[0] = pack_bf16(d[0] - bf16_lo(hi[0]), d[1] - bf16_hi(hi[0]));
+              lo[1] = pack_bf16(d[2] - bf16_lo(hi[1]), d[3] - bf16_hi(hi[1]));
+              *(uint2*)(to + gp) = uint2{lo[0], lo[1]};
+            }
+          } else {
+            uint32_t p[4][3];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) three_planes(d[r], p[r]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              *(uint2*)(to + k * gp) = uint2{bits_hi(p[0][k], p[1][k]), bits_hi(p[2][k], p[3][k])};
+          }
+        }
+      }
+    }
+  }
+  if constexpr (!GRAD && S::WM > 1) {
+    __syncthreads();
+    const float2* all = reinterpret_cast<const float2*>(lds);
+    for (int c = threadIdx.x; c < S::BN; c += S::THREADS) {
+      const int64_t token = at.n * S::BN + c;
+      if (token >= count) continue;
+      float top = all[c].x;
+#pragma unroll
+      for (int i = 1; i < S::WM; ++i) top = fmaxf(top, all[i * S::BN + c].x);
+      const float from = top == -INFINITY ? 0.0f : top;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::WM; ++i) sum += all[i * S::BN + c].y * exp_of(all[i * S::BN + c].x - from);
+      parts[at.m * np + token] = float2{top, sum};
+    }
+  }
+}
+
+// Joins the tiles' maxima and sums: 16 tokens and 16 groups of tiles to a workgroup.
+__global__ __launch_bounds__(kThreads)
+void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, const float* __restrict__ own, Tokens tok,
+                 float* __restrict__ loss, float* __restrict__ lse) {
+  __shared__ float2 lds[16][17];
+  const int c = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int64_t token = (int64_t)blockIdx.x * 16 + c, count = *tok.count;
+  if ((int64_t)blockIdx.x * 16 >= count) return;  // uniform
+  float top = -INFINITY, sum = 0.0f;
+  auto add = [&](float2 p) {
+    const float t = fmaxf(top, p.x), from = t == -INFINITY ? 0.0f : t;
+    sum = sum * exp_of(top - from) + p.y * exp_of(p.x - from);
+    top = t;
+  };
+  if (token < count)
+    for (int64_t t = group; t < tiles; t += 16 * 8) {
+      float2 p[8];  // on their way together
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        p[u] = t + 16 * u < tiles ? parts[(t + 16 * u) * np + token] : float2{-INFINITY, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) add(p[u]);
+    }
+  lds[group][c] = float2{top, sum};
+  __syncthreads();
+  if (group != 0 || token >= count) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) add(lds[i][c]);
+  const int64_t i = tok.map[token];
+  const bool counts = tok.label[token] >= 0;
+  const float log_sum = logf(sum);
+  loss[i] = counts ? log_sum + (top - own[token]) : 0.0f;  // exact where the label's logit is the largest
+  if (lse) lse[i] = counts ? top + log_sum : 0.0f;
+}
+
+// The hidden states' gradient over one piece: rows of the tile are columns of the
+// hidden states, columns tokens. Split i of the sum goes to fp32 rows of its own.
+template <class S>
+__global__ __launch_bounds__(S::THREADS)
+void k_dhidden(GemmSide w, GemmSide g, Segments segs, int steps, uint32_t tm, uint32_t tn, int splits, int add,
+               const int32_t* __restrict__ count_of, float* __restrict__ out, int64_t dq, int64_t np) {
+  __shared__ __align__(1024) char lds[S::LDS];
+  const uint32_t tiles = tm * tn, split = blockIdx.x / tiles;
+  const Tile at = tile_of(blockIdx.x % tiles, tiles, tm, tn);
+  const int64_t count = *count_of;
+  if (at.n * S::BN >= count) return;  // uniform
+  const int total = segs.count * steps;
+  const int s0 = (int)((int64_t)total * split / splits), s1 = (int)((int64_t)total * (split + 1) / splits);
+  typename S::Acc acc;
+  clear<S>(acc);
+  gemm_tile<S, K_IS_ROW, K_IN_ROWS>(w, g, at.m * S::BM, at.n * S::BN, segs, steps, s0, s1, lds, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
+  float* mine = out + (int64_t)split * np * dq;
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) {
+    const int64_t token = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+      const int64_t c = at.m * S::BM + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
+      if (token < count && c < dq) {
+        f32x4* to = (f32x4*)(mine + token * dq + c);
+        *to = add ? *to + acc[i][j] : acc[i][j];
+      }
+    }
+  }
+}
+
+// The head's gradient for one piece: rows of the tile are columns of the hidden
+// states, columns rows of the head.
+template <class S, typename Gt>
+__global__ __launch_bounds__(S::THREADS)
+void k_dweight(GemmSide h, GemmSide g, Segments segs, uint32_t tm, uint32_t tn, const int32_t* __restrict__ count_of,
+               int64_t v0, int64_t vc, uint32_t dim, Gt* __restrict__ dw, int64_t dw_ld, int first) {
+  __shared__ __align__(1024) char lds[S::LDS];
+  const Tile at = tile_of(blockIdx.x, gridDim.x, tm, tn);
+  const int steps = (int)((*count_of + 63) / 64);
+  typename S::Acc acc;
+  clear<S>(acc);
+  if (steps > 0)
+    gemm_tile<S, K_IS_ROW, K_IS_ROW>(h, g, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps, lds, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) {
+    const int64_t v = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+    Gt* row = dw + (v0 + v) * dw_ld;
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+      const uint32_t c = (uint32_t)(at.m * S::BM) + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
+      if (v >= vc || c >= dim) continue;
+      f32x4 x = acc[i][j];
+      if (c + 4 <= dim) {
+        if constexpr (sizeof(Gt) == 4) {
+          if (!first) {
+            const u32x4 old = ld16(row + c);
+            x += f32x4{__uint_as_float(old.x), __uint_as_float(old.y), __uint_as_float(old.z), __uint_as_float(old.w)};
+          }
+          st16(u32x4{__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)}, row + c);
+        } else {
+          const auto p = (__attribute__((address_space(1))) u32x2_any*)(row + c);
+          if (!first) {
+            const u32x2 old = *p;
+            x += f32x4{bf16_lo(old.x), bf16_hi(old.x), bf16_lo(old.y), bf16_hi(old.y)};
+          }
+          *p = u32x2{pack_bf16(x.x, x.y), pack_bf16(x.z, x.w)};
+        }
+      } else {
+        for (uint32_t e = 0; c + e < dim; ++e) {
+          float y = e == 0 ? x.x : e == 1 ? x.y : x.z;
+          if (!first) {
+            if constexpr (sizeof(Gt) == 4) y += row[c + e];
+            else y += bf16_to_f32(row[c + e]);
+          }
+          st_g(round_to<Gt>(y), row + c + e);
+        }
+      }
+    }
+  }
+}
+
+// The splits' sums, rounded once, back in the tokens' places; zeros where a token does not count.
+template <typename T>
+__global__ __launch_bounds__(kThreads)
+void k_join_dhidden(const float* __restrict__ sums, int splits, int64_t np, int64_t dq, const int32_t* __restrict__ inverse,
+                    int64_t n, uint32_t dim, T* __restrict__ out, int64_t ld) {
+  const int64_t per = (dim + 7) / 8;
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < n * per; at += (int64_t)gridDim.x * kThreads) {
+    const int64_t i = at / per;
+    const uint32_t c = (uint32_t)(at % per) * 8;
+    const int32_t place = inverse[i];
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (place >= 0)
+      for (int k = 0; k < splits; ++k) {
+        const float* from = sums + ((int64_t)k * np + place) * dq + c;
+        const f32x4 a = *(const f32x4*)from;
+        const f32x4 b = c + 4 < dq ? *(const f32x4*)(from + 4) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += a[e];
+          v[4 + e] += b[e];
+        }
+      }
+    store_cols<T, 8>(out + i * ld, v, c, dim);
+  }
+}
+
+// Zeros in a matrix's rows (a head's gradient without tokens, hidden states' without a vocabulary).
+template <typename T>
+__global__ __launch_bounds__(kThreads)
+void k_zero_rows(T* __restrict__ out, int64_t ld, int64_t rows, uint32_t dim) {
+  const int64_t per = (dim + 7) / 8;
+  const float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < rows * per; at += (int64_t)gridDim.x * kThreads)
+    store_cols<T, 8>(out + at / per * ld, v, (uint32_t)(at % per) * 8, dim);
+}
+
+// ---------------------------------------------------------------- host
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
+unsigned grid_of(int64_t pieces) { return (unsigned)least((pieces + kThreads - 1) / kThreads, 1 << 16); }
+
+// Rows that direct loads take as they lie: on 16-byte boundaries, whole stages
+// of k, and 256 of them within 32 bits of offset.
+bool as_it_lies(const void* p, int64_t ld, int64_t dim, int dtype) {
+  return dtype == ZS_BF16 && dim % kBK == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 &&
+         ld <= (1 << 22);
+}
+
+Tokens tokens_at(const HeadPlan& p, void* workspace) {
+  char* w = static_cast<char*>(workspace);
+  return Tokens{(int32_t*)(w + p.label), (int32_t*)(w + p.map), (int32_t*)(w + p.inverse), (int32_t*)(w + p.count),
+                (float*)(w + p.coef), (float*)(w + p.lse)};
+}
+
+// The tiles of a product of `m` by `n`: the time of a round of workgroups on
+// 256 CUs, one of the widest tile or two of the others at a time, which run at
+// 0.8 of its rate, times the rounds.
+enum Cut { WIDE, SQUARE, NARROW };
+Cut cut_of(int64_t m, int64_t n) {
+  auto rounds = [&](int64_t bm, int64_t bn, int64_t at_once) {
+    const int64_t tiles = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
+    return (tiles + 256 * at_once - 1) / (256 * at_once) * at_once;
+  };
+  const double wide = (double)rounds(256, 256, 1) * 256 * 256 * 0.8, square = (double)rounds(128, 128, 2) * 128 * 128,
+               narrow = (double)rounds(256, 64, 2) * 256 * 64;
+  if (n <= 64 && narrow <= square && narrow <= wide) return NARROW;
+  return square < wide ? SQUARE : WIDE;
+}
+
+template <typename F>
+void with_cut(Cut c, F&& f) {
+  if (c == WIDE) f(Wide{});
+  else if (c == SQUARE) f(Square{});
+  else f(Narrow{});
+}
+
+void layout(const void* src, int64_t ld, int dtype, int64_t dim, int64_t rows, uint16_t* dst, int64_t dp,
+            const int32_t* map, const int32_t* count, hipStream_t s) {
+  const unsigned grid = grid_of(up(rows, 64) * (dp / 8));
+  if (dtype == ZS_BF16)
+    hipLaunchKernelGGL((k_layout<uint16_t>), dim3(grid), dim3(kThreads), 0, s, (const uint16_t*)src, ld, (uint32_t)dim,
+                       rows, dst, dp, map, count);
+  else
+    hipLaunchKernelGGL((k_layout<float>), dim3(grid), dim3(kThreads), 0, s, (const float*)src, ld, (uint32_t)dim, rows,
+                       dst, dp, map, count);
+}
+
+void number_tokens(const void* labels, int index_type, int64_t n, int64_t vocab, bool gather, const float* lse,
+                   const float* dloss, float scale, const Tokens& t, float* loss, float* lse_out, hipStream_t s) {
+  if (index_type == ZS_I64)
+    hipLaunchKernelGGL((k_tokens<int64_t>), dim3(1), dim3(kTokBS), 0, s, (const int64_t*)labels, n, vocab, (int)gather,
+                       lse, dloss, scale, t, loss, lse_out);
+  else
+    hipLaunchKernelGGL((k_tokens<int32_t>), dim3(1), dim3(kTokBS), 0, s, (const int32_t*)labels, n, vocab, (int)gather,
+                       lse, dloss, scale, t, loss, lse_out);
+}
+
+void zero_rows(void* p, int dtype, int64_t ld, int64_t rows, int64_t dim, hipStream_t s) {
+  const unsigned grid = grid_of(rows * ((dim + 7) / 8));
+  if (dtype == ZS_BF16)
+    hipLaunchKernelGGL((k_zero_rows<uint16_t>), dim3(grid), dim3(kThreads), 0, s, (uint16_t*)p, ld, rows, (uint32_t)dim);
+  else
+    hipLaunchKernelGGL((k_zero_rows<float>), dim3(grid), dim3(kThreads), 0, s, (float*)p, ld, rows, (uint32_t)dim);
+}
+
+// Rows of the head laid out at a time, and bytes of the logits' gradient of a
+// piece (at least 4096 rows of the head, so that their product stays long).
+constexpr int64_t kLayoutBytes = 1 << 28;
+constexpr int64_t kGradBytes = 1 << 30;
+constexpr int64_t kMostPiece = 1 << 20;
+// Calls of fewer tokens keep every row where it is in the forward pass.
+constexpr int64_t kGatherTokens = 256;
+
+}  // namespace
+
+HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dtype) {
+  HeadPlan p{};
+  const bool grad = grad_dtype >= 0;
+  p.planes = dtype == ZS_F32 ? 3 : 1;
+  p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? 2 : 1;
+  p.np = up(n, 64);
+  p.dp = up(dim, 64);
+  p.dq = up(dim, 4);
+  const int64_t row = grad ? p.np * p.gplanes * 2 : p.dp * p.planes * 2;
+  int64_t most = (grad ? kGradBytes : kLayoutBytes) / (row > 0 ? row : 1);
+  most = most < 4096 ? 4096 : most > kMostPiece ? kMostPiece : most / 256 * 256;
+  p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
+  p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
+  p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
+  p.splits = 1;
+  if (grad && p.pieces) {
+    // the hidden states' gradient: enough tiles for two rounds on 256 CUs, eight stages at least to each part
+    const int64_t tiles = ((dim + 255) / 256) * ((n + 255) / 256);
+    const int64_t stages = p.piece / kBK * (p.planes == 3 ? kSix.count : 1);
+    int64_t splits = tiles > 0 ? 512 / tiles : 1;
+    splits = least(splits, stages / 8);
+    p.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+  }
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t from = at;
+    at = up(at + bytes, 256);
+    return from;
+  };
+  p.label = take(p.np * 4);
+  p.map = take(p.np * 4);
+  p.inverse = take(p.np * 4);
+  p.count = take(4);
+  p.coef = take(grad ? p.np * 4 : 0);
+  p.lse = take(grad ? p.np * 4 : 0);
+  p.own = take(grad ? 0 : p.np * 4);
+  p.parts = take(grad ? 0 : (vocab + 127) / 128 * p.np * (int64_t)sizeof(float2));
+  p.hidden = take(p.np * p.dp * p.planes * 2);
+  p.weight = take(p.piece * p.dp * p.planes * 2);
+  p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
+  p.dhidden = take(grad ? p.splits * p.np * p.dq * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype, const void* weight,
+                               int64_t weight_ld, const void* labels, int index_type, int64_t n, int64_t vocab,
+                               int64_t dim, float* loss, float* lse, void* workspace, hipStream_t s) {
+  const HeadPlan p = head_plan(n, vocab, dim, dtype, -1);
+  char* ws = static_cast<char*>(workspace);
+  const Tokens tok = tokens_at(p, workspace);
+  const Segments segs = p.planes == 3 ? kSix : kOne;
+  const bool h_lies = as_it_lies(hidden, hidden_ld, dim, dtype), w_lies = as_it_lies(weight, weight_ld, dim, dtype);
+  const bool gather = n > kGatherTokens;
+  number_tokens(labels, index_type, n, vocab, gather, nullptr, nullptr, 0.0f, tok, loss, lse, s);
+  GemmSide h{(const uint16_t*)hidden, hidden_ld, 0, n, 0};
+  if (gather || !h_lies) {
+    uint16_t* to = (uint16_t*)(ws + p.hidden);
+    layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
+    h = GemmSide{to, p.dp * p.planes, p.dp, p.np, 0};
+  }
+  const Cut cut = cut_of(vocab, n);
+  const int64_t piece = w_lies ? vocab : p.piece;
+  for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
+    const int64_t vc = least(piece, vocab - v0);
+    GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, 0};
+    if (!w_lies) {
+      uint16_t* to = (uint16_t*)(ws + p.weight);
+      const int64_t size = dtype == ZS_F32 ? 4 : 2;
+      layout((const char*)weight + v0 * weight_ld * size, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
+      w = GemmSide{to, p.dp * p.planes, p.dp, vc, 0};
+    }
+    with_cut(cut, [&](auto shape) {
+      using S = decltype(shape);
+      const uint32_t tm = (uint32_t)((vc + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
+      hipLaunchKernelGGL((k_logits<S, false>), dim3(tm * tn), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), tm,
+                         tn, v0, vocab, tok, (float2*)(ws + p.parts) + v0 / S::BM * p.np, (float*)(ws + p.own), p.np,
+                         (uint16_t*)nullptr, (int64_t)0, 0);
+    });
+  }
+  int64_t tiles = 0;
+  with_cut(cut, [&](auto shape) { tiles = (vocab + decltype(shape)::BM - 1) / decltype(shape)::BM; });
+  hipLaunchKernelGGL(k_join_loss, dim3((unsigned)((n + 15) / 16)), dim3(kThreads), 0, s, (const float2*)(ws + p.parts),
+                     tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype, const void* weight,
+                                int64_t weight_ld, const void* labels, int index_type, const float* lse,
+                                const float* dloss, float scale, int64_t n, int64_t vocab, int64_t dim, void* dhidden,
+                                int64_t dhidden_ld, void* dweight, int grad_dtype, int64_t dweight_ld, bool first,
+                                void* workspace, hipStream_t s) {
+  if (n == 0 || vocab == 0) {
+    if (n == 0 && first) zero_rows(dweight, grad_dtype, dweight_ld, vocab, dim, s);
+    if (vocab == 0) zero_rows(dhidden, dtype, dhidden_ld, n, dim, s);
+    return hipGetLastError();
+  }
+  const HeadPlan p = head_plan(n, vocab, dim, dtype, grad_dtype);
+  char* ws = static_cast<char*>(workspace);
+  const Tokens tok = tokens_at(p, workspace);
+  const Segments segs = p.planes == 3 ? kSix : kOne;
+  const Segments wsegs = p.planes == 3 ? (grad_dtype == ZS_F32 ? kSix : kThree) : p.gplanes == 2 ? kTwo : kOne;
+  const bool w_lies = as_it_lies(weight, weight_ld, dim, dtype);
+  uint16_t *hp = (uint16_t*)(ws + p.hidden), *gp = (uint16_t*)(ws + p.g);
+  float* sums = (float*)(ws + p.dhidden);
+  number_tokens(labels, index_type, n, vocab, true, lse, dloss, scale, tok, nullptr, nullptr, s);
+  layout(hidden, hidden_ld, dtype, dim, n, hp, p.dp, tok.map, tok.count, s);
+  for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
+    const int64_t vc = least(p.piece, vocab - v0), vp = up(vc, kBK), ldg = vp * p.gplanes;
+    GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, dim};
+    if (!w_lies) {
+      uint16_t* to = (uint16_t*)(ws + p.weight);
+      const int64_t size = dtype == ZS_F32 ? 4 : 2;
+      layout((const char*)weight + v0 * weight_ld * size, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
+      w = GemmSide{to, p.dp * p.planes, p.dp, vc, p.dp};
+    }
+    const GemmSide h{hp, p.dp * p.planes, p.dp, p.np, p.dp};
+    const GemmSide g_rows{gp, ldg, vp, p.np, vp};
+    with_cut(cut_of(vc, n), [&](auto shape) {
+      using S = decltype(shape);
+      const uint32_t tm = (uint32_t)((vc + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
+      hipLaunchKernelGGL((k_logits<S, true>), dim3(tm * tn), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), tm,
+                         tn, v0, vocab, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, p.gplanes);
+    });
+    with_cut(n <= 64 ? NARROW : cut_of(dim, n * p.splits), [&](auto shape) {
+      using S = decltype(shape);
+      const uint32_t tm = (uint32_t)((dim + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
+      hipLaunchKernelGGL((k_dhidden<S>), dim3(tm * tn * p.splits), dim3(S::THREADS), 0, s, w, g_rows, segs,
+                         (int)(vp / kBK), tm, tn, p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np);
+    });
+    with_cut(cut_of(dim, vc) == SQUARE ? SQUARE : WIDE, [&](auto shape) {
+      using S = std::conditional_t<std::is_same_v<decltype(shape), Square>, Square, Wide>;
+      const uint32_t tm = (uint32_t)((dim + S::BM - 1) / S::BM), tn = (uint32_t)((vc + S::BN - 1) / S::BN);
+      if (grad_dtype == ZS_BF16)
+        hipLaunchKernelGGL((k_dweight<S, uint16_t>), dim3(tm * tn), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tm, tn,
+                           tok.count, v0, vc, (uint32_t)dim, (uint16_t*)dweight, dweight_ld, (int)first);
+      else
+        hipLaunchKernelGGL((k_dweight<S, float>), dim3(tm * tn), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tm, tn,
+                           tok.count, v0, vc, (uint32_t)dim, (float*)dweight, dweight_ld, (int)first);
+    });
+  }
+  const unsigned grid = grid_of(n * ((dim + 7) / 8));
+  if (dtype == ZS_BF16)
+    hipLaunchKernelGGL((k_join_dhidden<uint16_t>), dim3(grid), dim3(kThreads), 0, s, sums, p.splits, p.np, p.dq,
+                       tok.inverse, n, (uint32_t)dim, (uint16_t*)dhidden, dhidden_ld);
+  else
+    hipLaunchKernelGGL((k_join_dhidden<float>), dim3(grid), dim3(kThreads), 0, s, sums, p.splits, p.np, p.dq,
+                       tok.inverse, n, (uint32_t)dim, (float*)dhidden, dhidden_ld);
+  return hipGetLastError();
+}
+
+}  // namespace zs

@@ -1,0 +1,216 @@
+// bf16 matrix products D[m, n] = sum_k A[m, k] B[n, k] on the matrix units,
+// accumulated in fp32; the epilogue that uses D is the caller's.
+//
+// Either operand lies in memory as rows of consecutive k (K_IN_ROWS: the logits
+// are hidden states times rows of the head) or as one row for each k (K_IS_ROW:
+// the gradient of the head is a sum over tokens, and a token's row holds
+// consecutive columns of the result). Both are copied to LDS as they lie, by
+// loads that go there directly; operands with a row for each k are transposed
+// on the way from LDS to registers.
+//
+// An fp32 operand is a sum of up to three bf16 planes that lie side by side in
+// each row, and a product of two such operands the sum of the products of their
+// planes that matter: Segments lists them, and the loop over k runs through one
+// after another into the same accumulators.
+#pragma once
+
+#include "zs_device.hpp"
+
+namespace zs {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+enum GemmMode { K_IN_ROWS, K_IS_ROW };
+
+// One operand. Rows start on 16-byte boundaries, `ld` elements apart, and hold
+// planes of `plane` elements. K_IN_ROWS: `rows` rows of the result, at least 64 *
+// steps elements to a plane. K_IS_ROW: `rows` values of k, `cols` columns (a
+// multiple of 8).
+struct GemmSide {
+  const uint16_t* p;
+  int64_t ld;
+  int64_t plane;
+  int64_t rows;
+  int64_t cols;
+};
+
+// Products of planes: nibble i of a and b is product i's plane of either side.
+struct Segments {
+  int count;
+  uint32_t a, b;
+};
+
+constexpr int kBK = 64;  // values of k of a stage
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct GemmShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int THREADS = WM * WN * 64;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;  // 16 x 16 tiles of a wave
+  static constexpr int STAGE_BYTES = (BM + BN) * kBK * 2;
+  static constexpr int LDS = 2 * STAGE_BYTES;
+  using Acc = f32x4[TM][TN];
+};
+
+#ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know the buffer types
+// The part of an operand that one workgroup reads: SIDE rows (or columns) from
+// `start` on, 64 values of k at a time.
+//
+// K_IN_ROWS: a row's 64 values are 128 bytes, row after row in LDS. The chunk of
+// 16 bytes c of row r lies at place c ^ (r & 7): 8 lanes that read the same chunk
+// of 8 rows find it in 8 different places. A load to LDS puts lane l's 16 bytes
+// 16 l behind the wave's start, so what is permuted is where they come from.
+//
+// K_IS_ROW: SIDE columns of a row, row after row in LDS. The 16 lanes of a
+// transposing read take 32 bytes of 4 rows, the wave of 16 rows: the chunk of 32
+// bytes c of row r lies at place c ^ swap(r), with another value of swap for each
+// of these rows.
+template <class S, int SIDE, GemmMode MODE>
+struct SideTile {
+  static constexpr int N = SIDE * kBK * 2 / 16 / S::THREADS;  // 16-byte loads of a thread for a stage
+  static constexpr int T = SIDE / 16;
+  static_assert(N * S::THREADS * 16 == SIDE * kBK * 2, "every thread loads as much");
+  const uint16_t* base;
+  int64_t ld, plane, rows;
+  uint32_t off[N];
+  int tid, live;
+
+  static __device__ __forceinline__ int swap(int r) { return ((r & 3) | ((r >> 1) & 12)) & (T - 1); }
+
+  // byte offsets of the thread's loads; values of k from `there` on come as the last one's copies
+  __device__ __forceinline__ void offsets_k_is_row(int64_t cols, int there) {
+    live = there;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * S::THREADS + tid, r = at / (SIDE / 8), c = at % (SIDE / 8);
+      const int col = (((c >> 1) ^ swap(r)) * 2 + (c & 1)) * 8;
+      const int last = (int)(cols < SIDE ? cols : SIDE) - 8;  // columns behind the last are copies; nobody uses them
+      off[i] = (uint32_t)((r < live ? r : live - 1) * ld * 2) + (col < last ? col : last) * 2;
+    }
+  }
+  __device__ __forceinline__ void init(const GemmSide& g, int64_t start) {
+    tid = threadIdx.x;
+    ld = g.ld;
+    plane = g.plane;
+    rows = g.rows;
+    if constexpr (MODE == K_IN_ROWS) {
+      base = g.p + start * g.ld;
+      const int64_t left = g.rows - start;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int at = i * S::THREADS + tid, r = at >> 3, c = (at & 7) ^ (r & 7);
+        off[i] = (uint32_t)((r < left ? r : left - 1) * ld * 2) + c * 16;  // rows behind the last are its copies
+      }
+    } else {
+      base = g.p + start;
+      offsets_k_is_row(g.cols - start, kBK);
+    }
+  }
+  __device__ __forceinline__ void load(char* lds, int p, int64_t k, int64_t cols_left) {
+    const uint16_t* from = base + p * plane + (MODE == K_IN_ROWS ? k : k * ld);
+    if constexpr (MODE == K_IS_ROW) {
+      const int there = k + kBK <= rows ? kBK : (int)(rows - k);
+      if (there != live) offsets_k_is_row(cols_left, there);
+    }
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0xffffffffu, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rsrc, (__attribute__((address_space(3))) void*)(lds + (i * S::THREADS + (tid & ~63)) * 16), 16, off[i], 0, 0,
+          0);
+  }
+};
+
+// Fragments of 16 rows (columns) x 32 values of k as the 16x16x32 product takes
+// them: lane l has row l % 16, values 8 (l / 16) to 8 (l / 16) + 7.
+template <int SIDE, GemmMode MODE>
+struct Fragments {
+  uint32_t at;  // byte address behind the side's stage
+  __device__ __forceinline__ void init(int first) {  // first row of the wave, a multiple of its tiles' 16
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    if constexpr (MODE == K_IN_ROWS) {
+      at = (uint32_t)((first + r) * 128 + ((q ^ (r & 7)) * 16));
+    } else {
+      const int row = 8 * q + (r >> 2);
+      constexpr int T = SIDE / 16;
+      const int sw = ((row & 3) | ((row >> 1) & 12)) & (T - 1);
+      at = (uint32_t)(row * SIDE * 2 + (((first / 16) ^ sw) * 32) + (r & 3) * 8);
+    }
+  }
+  // fragment i of the wave, values 32 kk and on of the stage
+  __device__ __forceinline__ bf16x8 get(const char* stage, int i, int kk) const {
+    if constexpr (MODE == K_IN_ROWS) {
+      return *(const bf16x8*)(stage + (at ^ (kk * 64)) + i * 2048);
+    } else {
+      const char* p = stage + (at ^ (i * 32)) + kk * 32 * SIDE * 2;
+      typedef __attribute__((address_space(3))) bf16x4* ptr;
+      const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ptr)(p));
+      const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((ptr)(p + 4 * SIDE * 2));
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+  }
+};
+
+// All loads to LDS that this wave has sent off are done.
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+#endif
+
+// acc += the product over stages [s0, s1) of the `segs.count * steps` that there
+// are, `steps` to a segment. Lane l of the wave at (wm, wn) gets in acc[i][j][r]
+// row wm BM / WM + 16 i + 4 (l / 16) + r and column wn BN / WN + 16 j + l % 16 of
+// the tile. Two stages in LDS: the loads of the next are on their way while the
+// products of this one are made, with one barrier between.
+template <class S, GemmMode MA, GemmMode MB>
+__device__ __forceinline__ void gemm_tile(const GemmSide& a, const GemmSide& b, int64_t start_a, int64_t start_b,
+                                          const Segments& segs, int steps, int s0, int s1, char* lds,
+                                          typename S::Acc& acc) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  SideTile<S, S::BM, MA> la;
+  SideTile<S, S::BN, MB> lb;
+  la.init(a, start_a);
+  lb.init(b, start_b);
+  Fragments<S::BM, MA> ga;
+  Fragments<S::BN, MB> gb;
+  ga.init(wm * (S::BM / S::WM));
+  gb.init(wn * (S::BN / S::WN));
+  constexpr int A_BYTES = S::BM * kBK * 2;
+  int seg = s0 / steps, step = s0 % steps;
+  auto load = [&](char* stage) {
+    const int64_t k = (int64_t)step * kBK;
+    la.load(stage, (segs.a >> (4 * seg)) & 15, k, a.cols - start_a);
+    lb.load(stage + A_BYTES, (segs.b >> (4 * seg)) & 15, k, b.cols - start_b);
+    if (++step == steps) step = 0, ++seg;
+  };
+  if (s0 < s1) load(lds);
+  for (int s = s0; s < s1; ++s) {
+    char* now = lds + ((s - s0) & 1) * S::STAGE_BYTES;
+    wait_loads();
+    barrier();  // everybody's loads of this stage are done, and nobody reads the other any more
+    if (s + 1 < s1) load(lds + ((s - s0 + 1) & 1) * S::STAGE_BYTES);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      bf16x8 fa[S::TM], fb[S::TN];
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) fb[j] = gb.get(now + A_BYTES, j, kk);
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i) fa[i] = ga.get(now, i, kk);
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  }
+#endif
+}
+
+}  // namespace zs

@@ -20,6 +20,8 @@
  * And around the update, for the parameters that no matrix product stands for:
  *   embedding   zs_embed_forward, zs_embed_backward
  *   layer norm  zs_layer_norm_forward, zs_layer_norm_backward
+ * And for the head, which may be the embedding's table:
+ *   loss        zs_linear_cross_entropy_forward, zs_linear_cross_entropy_backward
  *
  * Pages (title, address) cited below:
  *   [L5]  "Lesson 5: ZeRO and FSDP", hpc.payai.win/train/lesson05.html
@@ -591,6 +593,77 @@ zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, i
                                  const float* rstd, int64_t rows, int64_t dim, void* dx, int64_t dx_ld,
                                  void* dweight, void* dbias, int32_t grad_dtype, int32_t first,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that the two calls below need for n tokens over [vocab, dim],
+ * with hidden states and weight of `dtype`: zs_linear_cross_entropy_backward with
+ * a dweight of `grad_dtype`, or, with grad_dtype -1, zs_linear_cross_entropy_forward
+ * (0 for sizes and types that they refuse). The contents need no initialisation. */
+size_t zs_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, int32_t dtype,
+                                               int32_t grad_dtype);
+
+/*
+ * zs_linear_cross_entropy_forward -- softmax cross entropy of the logits
+ * z = hidden weight^T over the vocabulary, without keeping the logits.
+ *   hidden[n, dim]     DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride hidden_ld
+ *   weight[vocab, dim] DEVICE, `dtype`, row stride weight_ld: the head, or the
+ *                      embedding's table where they are tied
+ *   labels[n]          DEVICE ids, `index_type` ZS_I32 or ZS_I64; a token whose
+ *                      label is outside of [0, vocab) does not count
+ *   loss[n]            DEVICE fp32: log(sum_v exp(z_v)) - z_label, 0 where a
+ *                      token does not count
+ *   lse[n]             optional DEVICE fp32 (NULL = skip; the backward pass needs
+ *                      it): log(sum_v exp(z_v)), 0 where a token does not count
+ *   workspace          DEVICE scratch of at least
+ *                      zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype, -1)
+ *                      bytes on a 16-byte boundary; calls and graph replays that
+ *                      may run at the same time need one each
+ * Products of bf16 values are exact and added in fp32; fp32 values enter as sums
+ * of three bf16, with an error of the size of fp32 products' roundings. Infinite
+ * or NaN logits make their token's loss infinite or NaN, and no other's. dim at
+ * most 2^20, and at most 2^31 - 1 tiles of 128 rows of the head by 128 tokens.
+ * Weights that lie on 16-byte boundaries with a multiple of 64 columns are read
+ * as they lie; others are laid out in the workspace first. No output or workspace
+ * may share bytes with another argument. Errors: ZS_ERR_NULL, ZS_ERR_SIZE (dim < 1
+ * with n > 0 among them), ZS_ERR_DTYPE, ZS_ERR_WORKSPACE, ZS_ERR_ALIGN,
+ * ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld, int32_t dtype,
+                                          const void* weight, int64_t weight_ld, const void* labels,
+                                          int32_t index_type, int64_t n, int64_t vocab, int64_t dim,
+                                          float* loss, float* lse, void* workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * zs_linear_cross_entropy_backward -- gradients of that loss. With
+ * g_iv = scale * dloss_i * (exp(z_iv - lse_i) - [v == label_i]), 0 for tokens
+ * that do not count:
+ *   hidden, weight, labels
+ *                      as above; lse[n] as the forward pass gives it
+ *   dloss[n]           optional DEVICE fp32 gradient of each token's loss (NULL =
+ *                      ones); scale must be finite (1 / tokens for a mean)
+ *   dhidden[n, dim]    DEVICE, `dtype`, row stride dhidden_ld: sum_v g_iv weight_v,
+ *                      zeros where a token does not count
+ *   dweight[vocab, dim]
+ *                      DEVICE, `grad_dtype`, row stride dweight_ld:
+ *                      (first ? 0 : dweight) + sum_i g_iv hidden_i; hidden states
+ *                      of tokens that do not count reach no sum, whatever they hold
+ *   workspace          DEVICE scratch of at least
+ *                      zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype,
+ *                      grad_dtype) bytes on a 16-byte boundary; calls and graph
+ *                      replays that may run at the same time need one each
+ * The logits are made again, a piece of the vocabulary at a time. g is rounded to
+ * bf16 for the gradients that are stored in bf16 from bf16 inputs, to 16 bits or
+ * more for the others; sums are fp32, in an order that depends on the sizes and
+ * on how many tokens count alone. n == 0 with first != 0 sets dweight to zero.
+ * Limits, overlaps and errors as above, and ZS_ERR_HPARAM.
+ */
+zs_status zs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_ld, int32_t dtype,
+                                           const void* weight, int64_t weight_ld, const void* labels,
+                                           int32_t index_type, const float* lse, const float* dloss,
+                                           float scale, int64_t n, int64_t vocab, int64_t dim,
+                                           void* dhidden, int64_t dhidden_ld, void* dweight,
+                                           int32_t grad_dtype, int64_t dweight_ld, int32_t first,
+                                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, NUL-terminated name of a status code ("ZS_OK", "ZS_ERR_NULL", ...). */
 const char* zs_status_string(zs_status status);

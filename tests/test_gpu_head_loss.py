@@ -1,0 +1,178 @@
+"""The loss over a vocabulary and its gradients against the fp64 oracle.
+
+Tolerances, u = 2^-24, half = half a step of a type (fp32 2^-24, bf16 2^-8). The
+matrix units add 32 exact products at a time to an fp32 sum, not necessarily
+rounded to nearest, so a sum of K products in S segments is off by at most
+  sum(K) = 2 (32 + S K / 32) u of the sum of their magnitudes.
+fp32 operands are sums of three bf16 (S = 6); the products left out are below
+2^-21 of the whole. With A_iv = sum_k |h_ik w_vk| and R_i = max_v |z_iv - top_i|:
+  z:    E_iv = (sum(dim) + 2^-21 where fp32) A_iv
+  exp:  x log2(e) is rounded (|x| 2^-23 with the constant's error) and the
+        function good to 2^-22: relative e(x) = (|x| + 4) 2^-23
+  lse:  max_v E + 2 e(R) + (128 + vocab / 1024) u + 4 u (|top| + log vocab): a
+        lane adds up to 32 terms and tiles are joined in 16 groups; loss twice the
+        first term, for the label's own logit
+  g:    with p = exp(z - lse): |c| (p (1.01 E + e(z - lse)) + 3 u (p + 1)) + r |g|, r the rounding
+        to one, two or three bf16: 2^-8, 2^-16, 2^-23
+  dh:   sum_v dg |w| + (sum(vocab) + 64 u + 2^-21 where fp32) sum_v |g w| + half |dh|
+  dw:   sum_i dg |h| + (sum(n) + 64 u + 2^-21 where fp32, 2^-13 where of fp32 inputs for bf16)
+        sum_i |g h| + 2 u |old| + half |dw|
+(1.01 E for exp(E) - 1, E below 0.01.)
+"""
+import numpy as np
+import pytest
+import torch
+
+import fsdp_sharded_optimizer_flatparameter_amd as zs
+from oracle import head_loss as oh
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+# (n, vocab, dim): one of each, the edges of the tiles (64, 128, 256) on both sides, widths off the stages of 64
+SIZES = [(1, 1, 1), (1, 2, 3), (2, 1, 64), (3, 300, 7), (1, 1000, 64), (16, 257, 128), (63, 255, 72), (64, 256, 64),
+         (65, 129, 65), (100, 64, 200), (127, 513, 128), (129, 1030, 192), (256, 300, 64), (257, 700, 264), (300, 77, 512),
+         (520, 601, 130), (33, 4500, 64)]
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def matrix(g, rows, dim, dtype, gap=0, sigma=1.0, shift=0):
+    """[rows, dim] with NaN in the gaps, `shift` elements behind a 16-byte boundary."""
+    flat = torch.full((rows * (dim + gap) + shift + 8,), float("nan"), device="cuda", dtype=DT[dtype])
+    m = flat[shift:shift + rows * (dim + gap)].view(rows, dim + gap)
+    m[:, :dim] = torch.randn(rows, dim, generator=g, device="cuda") * sigma
+    return flat, m[:, :dim]
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def bits(t):
+    return t.contiguous().view(torch.int32 if t.element_size() == 4 else torch.int16)
+
+
+def labels_of(g, n, vocab, itype, ignored):
+    t = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    if ignored:
+        off = torch.rand(n, generator=g, device="cuda") < ignored
+        t[off] = torch.tensor([-100, vocab, -1, vocab + 5], device="cuda")[torch.arange(n, device="cuda") % 4][off]
+    return t.to(itype)
+
+
+def scratch(n, vocab, dim, dtype, grad=None):
+    """A workspace full of NaN, and a guard behind it."""
+    size = zs.zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, DT[dtype], None if grad is None else DT[grad])
+    big = torch.full((size + 4096,), 0xFF, device="cuda", dtype=torch.uint8)
+    return big, big[:size]
+
+
+def sums(k, segments):
+    return 2 * (32 + segments * k / 32) * U
+
+
+def bounds(h, w, f32):
+    """(z, E) of the tokens that count."""
+    a = np.abs(h) @ np.abs(w).T
+    return h @ w.T, (sums(h.shape[1], 6 if f32 else 1) + (2.0 ** -21 if f32 else 0.0)) * a
+
+
+def e_of(x):
+    return (np.abs(x) + 4) * 2.0 ** -23
+
+
+def within(name, got, want, tol):
+    err = np.abs(got - want)
+    assert np.all(err <= tol), f"{name}: {(~(err <= tol)).sum()} off, worst {np.nanmax(err / np.maximum(tol, 1e-300))} of the tolerance"
+
+
+def check_forward(hidden, weight, labels, loss, lse):
+    h, w, t = f64(hidden), f64(weight), labels.cpu().numpy()
+    want_loss, want_lse = oh.loss_forward(h, w, t)
+    live = oh.counted(t, len(w))
+    got_loss, got_lse = f64(loss), f64(lse)
+    assert np.all(got_loss[~live] == 0) and np.all(got_lse[~live] == 0)
+    if not live.any():
+        return
+    z, e = bounds(h[live], w, hidden.dtype == torch.float32)
+    top = z.max(1)
+    r = (top[:, None] - z).max(1)
+    rest = 2 * e_of(r) + (128 + len(w) / 1024) * U + 4 * U * (np.abs(top) + np.log(len(w)))
+    within("lse", got_lse[live], want_lse[live], e.max(1) + rest)
+    within("loss", got_loss[live], want_loss[live], 2 * e.max(1) + rest)
+
+
+def check_backward(hidden, weight, labels, lse, c, dh, dw, old, first):
+    f32, grad32 = hidden.dtype == torch.float32, dw.dtype == torch.float32
+    h, w, t, ls = f64(hidden), f64(weight), labels.cpu().numpy(), f64(lse)
+    want_h, want_w, g = oh.loss_backward(h, w, t, ls, c)
+    live = oh.counted(t, len(w))
+    assert np.all(f64(dh)[~live] == 0)
+    h, g, c = h[live], g[live], np.abs(c[live])
+    z, e = bounds(h, w, f32)
+    x = z - ls[live][:, None]
+    p = np.exp(x)
+    dg = c[:, None] * (p * (1.01 * e + e_of(x)) + 3 * U * (p + 1))
+    extra = 2.0 ** -21 if f32 else 0.0
+    r_h = 2.0 ** -23 if f32 else 2.0 ** -8
+    r_w = 2.0 ** -23 if f32 else 2.0 ** -16 if grad32 else 2.0 ** -8
+    tol = (dg + r_h * np.abs(g)) @ np.abs(w) + (sums(len(w), 6 if f32 else 1) + 64 * U + extra) * (np.abs(g) @ np.abs(w))
+    within("dh", f64(dh)[live], want_h[live], tol + HALF[dh.dtype] * (np.abs(want_h[live]) + tol))
+    before = np.zeros_like(want_w) if first else f64(old)
+    extra = extra if grad32 else 2.0 ** -13 if f32 else 0.0
+    tol = (dg + r_w * np.abs(g)).T @ np.abs(h) + (sums(len(t), 6 if f32 else 2) + 64 * U + extra) * (np.abs(g).T @ np.abs(h))
+    tol += 2 * U * np.abs(before)
+    within("dw", f64(dw), want_w + before, tol + HALF[dw.dtype] * (np.abs(want_w + before) + tol))
+
+
+def run_forward(hidden, weight, labels, dtype):
+    n, dim = hidden.shape
+    big, ws = scratch(n, len(weight), dim, dtype)
+    loss, lse = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    zs.zs_linear_cross_entropy_forward(hidden, weight, labels, loss, lse=lse, workspace=ws)
+    assert (big[ws.numel():] == 0xFF).all()
+    return loss, lse
+
+
+@pytest.mark.parametrize("n,vocab,dim", SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_forward(n, vocab, dim, dtype):
+    g = gen(n * 7919 + vocab)
+    for gap, shift, ignored, itype in ((0, 0, 0.0, torch.int64), (3, 1, 0.4, torch.int32)):
+        _, w = matrix(g, vocab, dim, dtype, gap, 0.3, shift)
+        _, h = matrix(g, n, dim, dtype, gap, 1.0, shift)
+        t = labels_of(g, n, vocab, itype, ignored)
+        h[~((t >= 0) & (t < vocab))] = float("nan")  # what does not count reaches nothing
+        check_forward(h, w, t, *run_forward(h, w, t, dtype))
+
+
+@pytest.mark.parametrize("n,vocab,dim", SIZES)
+@pytest.mark.parametrize("dtype,grad", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+def test_backward(n, vocab, dim, dtype, grad):
+    g = gen(n * 7919 + vocab + 1)
+    for gap, shift, ignored, itype, first, weighted in ((0, 0, 0.0, torch.int64, True, False),
+                                                        (5, 1, 0.4, torch.int32, False, True)):
+        _, w = matrix(g, vocab, dim, dtype, gap, 0.3, shift)
+        _, h = matrix(g, n, dim, dtype, gap, 1.0, shift)
+        t = labels_of(g, n, vocab, itype, ignored)
+        live = (t >= 0) & (t < vocab)
+        h[~live] = float("nan")
+        lse = torch.where(live, torch.logsumexp(torch.nan_to_num(h).double() @ w.double().t(), 1), 0.0).float()
+        dloss = torch.randn(n, generator=g, device="cuda") if weighted else None
+        big_h, dh = matrix(g, n, dim, dtype, gap, 1.0, shift)
+        big_w, dw = matrix(g, vocab, dim, grad, gap, 0.1, shift)
+        old, before = dw.clone(), (big_h.clone(), big_w.clone())
+        big, ws = scratch(n, vocab, dim, dtype, grad)
+        zs.zs_linear_cross_entropy_backward(h, w, t, lse, dh, dw, dloss=dloss, scale=0.37, first=first, workspace=ws)
+        c = np.full(n, np.float32(0.37), np.float64) * (1.0 if dloss is None else f64(dloss))
+        check_backward(h, w, t, lse, c, dh, dw, old, first)
+        assert (big[ws.numel():] == 0xFF).all()
+        for now, was, view in ((big_h, before[0], dh), (big_w, before[1], dw)):  # gaps and what lies around
+            view.zero_()
+            at = torch.isnan(was)
+            assert torch.isnan(now[at]).all()
