@@ -13,6 +13,8 @@ from .api import (  # noqa: F401
     ZsError,
     zs_accumulate_grads,
     zs_accumulate_local,
+    zs_activation_pack,
+    zs_activation_unpack,
     zs_adamw_step,
     zs_cast_for_gather,
     zs_clip_coefficient,
@@ -33,6 +35,9 @@ from .api import (  # noqa: F401
     zs_pack_shard_dim0,
     zs_reduce_grads,
     zs_reduce_grads_noalloc,
+    zs_rms_norm_backward,
+    zs_rms_norm_forward,
+    zs_rms_norm_workspace_bytes,
     zs_sharded_step,
     zs_version,
     zs_workspace_bytes,

@@ -15,6 +15,7 @@ ZS_F32 = 0
 ZS_BF16 = 1
 ZS_I32 = 2
 ZS_I64 = 3
+ZS_E4M3 = 4
 ZS_MAX_WORLD = 256
 ZS_NOALLOC_MAX_N = 1 << 28
 STATUS = {
@@ -88,6 +89,19 @@ SIGNATURES = {
                                            C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
                                            C.c_int64, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p,
                                            C.c_size_t, C.c_void_p]),
+    "zs_activation_pack": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                       C.c_int64, C.c_void_p, C.c_int64, C.c_void_p]),
+    "zs_activation_unpack": (C.c_int32, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                                         C.c_void_p, C.c_int32, C.c_int64, C.c_void_p]),
+    "zs_rms_norm_forward": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                        C.c_int64, C.c_int32, C.c_void_p, C.c_int32, C.c_int64, C.c_int64,
+                                        C.c_double, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p,
+                                        C.c_int64, C.c_void_p, C.c_void_p]),
+    "zs_rms_norm_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64]),
+    "zs_rms_norm_backward": (C.c_int32, [C.c_void_p, C.c_int32, C.c_int64, C.c_void_p, C.c_int32, C.c_int64,
+                                         C.c_void_p, C.c_int64, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                         C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64, C.c_int32,
+                                         C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p]),
     "zs_linear_cross_entropy_workspace_bytes": (C.c_size_t, [C.c_int64, C.c_int64, C.c_int64, C.c_int32, C.c_int32]),
     "zs_linear_cross_entropy_forward": (C.c_int32, [C.c_void_p, C.c_int64, C.c_int32, C.c_void_p, C.c_int64,
                                                     C.c_void_p, C.c_int32, C.c_int64, C.c_int64, C.c_int64,

@@ -414,6 +414,20 @@ def _rows2d(t, name, dev):
     raise ValueError(f"unsupported dtype {t.dtype} of {name}")
 
 
+def _shape2d(t, name):
+    """_rows2d's sizes for a tensor of another type."""
+    if t.dim() == 2:
+        rows, dim = t.shape
+        ld, unit = t.stride()
+        if (unit == 1 or dim <= 1) and (ld >= dim or rows <= 1):
+            return rows, dim, max(ld, dim)
+        raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
+    if not t.dim() or not t.is_contiguous():
+        raise ValueError(f"{name} must have two dimensions or be contiguous")
+    dim = t.shape[-1]
+    return (t.numel() // dim if dim else 0), dim, dim
+
+
 def _on_device(t, name, dev):
     if not isinstance(t, _Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
@@ -595,6 +609,137 @@ def zs_layer_norm_backward(dy, x, weight, mean, rstd, dx, *, dweight=None, dbias
           _DTYPES[wdtype], _vector(mean, "mean", rows, dev, torch.float32),
           _vector(rstd, "rstd", rows, dev, torch.float32), rows, dim, dx.data_ptr(), dx_ld, dw, db,
           _DTYPES[gdtype], 1 if first else 0, ws, ws_bytes)
+
+
+# ---------------------------------------------------------------- RMS norm, activations in 8 bits
+
+_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+SCALE_BLOCK = 128
+
+
+def _codes(codes, scales, rows, dim, dev):
+    """(pointer, row stride) of codes and of their scales."""
+    if codes is None or scales is None:
+        raise ValueError("codes and scales come together")
+    if not (isinstance(codes, _Tensor) and codes.get_device() == dev):
+        _on_device(codes, "codes", dev)
+    if codes.dtype not in _CODE_TYPES:
+        raise ValueError(f"codes must be uint8 or float8_e4m3fn, got {codes.dtype}")
+    c_rows, c_dim, c_ld = _shape2d(codes, "codes")
+    if not (isinstance(scales, _Tensor) and scales.get_device() == dev):
+        _on_device(scales, "scales", dev)
+    if scales.dtype is not torch.float32:
+        raise ValueError(f"scales must be torch.float32, got {scales.dtype}")
+    s_rows, s_dim, s_ld = _shape2d(scales, "scales")
+    if (c_rows, c_dim) != (rows, dim):
+        raise ValueError(f"codes are {c_rows} x {c_dim}, the rows {rows} x {dim}")
+    if dim and (s_rows, s_dim) != (rows, -(-dim // SCALE_BLOCK)):
+        raise ValueError(f"scales are {s_rows} x {s_dim}, expected {rows} x {-(-dim // SCALE_BLOCK)}")
+    return codes.data_ptr(), c_ld, scales.data_ptr(), s_ld
+
+
+def zs_activation_pack(x, codes, scales, *, stream=None):
+    """x's rows as e4m3 codes (uint8 or float8_e4m3fn) and an fp32 scale, a power of two, for each
+    block of 128 elements of a row: scales is [rows, ceil(dim / 128)]."""
+    dev = _device_index(x, "x")
+    rows, dim, x_ld = _rows2d(x, "x", dev)
+    c, c_ld, sc, sc_ld = _codes(codes, scales, rows, dim, dev)
+    _call("zs_activation_pack", dev, stream, x.data_ptr(), _DTYPES[x.dtype], x_ld, rows, dim, c, c_ld, sc, sc_ld)
+
+
+def zs_activation_unpack(codes, scales, out, *, stream=None):
+    """out = code * scale."""
+    dev = _device_index(out, "out")
+    rows, dim, out_ld = _rows2d(out, "out", dev)
+    c, c_ld, sc, sc_ld = _codes(codes, scales, rows, dim, dev)
+    _call("zs_activation_unpack", dev, stream, c, c_ld, sc, sc_ld, rows, dim, out.data_ptr(), _DTYPES[out.dtype], out_ld)
+
+
+def zs_rms_norm_forward(x, weight, y=None, *, eps=1e-5, residual=None, residual_out=None, codes=None, scales=None,
+                        rstd=None, stream=None):
+    """y = h * rstd * weight for h = x + residual (residual None: x) and rstd = 1 / sqrt(mean(h^2) + eps).
+    residual_out takes h (it may be residual, or x where the types are the same), codes and scales take
+    y in 8 bits, rstd (fp32, one per row) the statistics, each where given; y may be None with codes.
+    residual and residual_out have x's dtype or fp32."""
+    dev = _device_index(x, "x")
+    rows, dim, x_ld = _rows2d(x, "x", dev)
+    xcode = sum_code = _DTYPES[x.dtype]
+    y_ptr = r_ptr = s_ptr = c_ptr = sc_ptr = None
+    y_ld = r_ld = s_ld = c_ld = sc_ld = 0
+    if y is not None:
+        y_rows, y_dim, y_ld = _rows2d(y, "y", dev)
+        if y_rows != rows or y_dim != dim or y.dtype != x.dtype:
+            raise ValueError("y must have x's rows, width and dtype")
+        y_ptr = y.data_ptr()
+    elif codes is None:
+        raise ValueError("y may be None only with codes")
+    if residual is not None:
+        r_rows, r_dim, r_ld = _rows2d(residual, "residual", dev)
+        if r_rows != rows or r_dim != dim:
+            raise ValueError("residual must have x's rows and width")
+        r_ptr, sum_code = residual.data_ptr(), _DTYPES[residual.dtype]
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out comes with a residual")
+        s_rows, s_dim, s_ld = _rows2d(residual_out, "residual_out", dev)
+        if s_rows != rows or s_dim != dim or residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out must have residual's rows, width and dtype")
+        s_ptr = residual_out.data_ptr()
+    if codes is not None or scales is not None:
+        c_ptr, c_ld, sc_ptr, sc_ld = _codes(codes, scales, rows, dim, dev)
+    w = _vector(weight, "weight", dim, dev)
+    wdtype = x.dtype if weight is None else weight.dtype
+    if wdtype not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {wdtype}")
+    _call("zs_rms_norm_forward", dev, stream, x.data_ptr(), xcode, x_ld, r_ptr, r_ld, s_ptr, s_ld, sum_code, w,
+          _DTYPES[wdtype], rows, dim, float(eps), y_ptr, y_ld, c_ptr, c_ld, sc_ptr, sc_ld,
+          _vector(rstd, "rstd", rows, dev, torch.float32))
+
+
+def zs_rms_norm_workspace_bytes(rows: int, dim: int) -> int:
+    return int(_lib().zs_rms_norm_workspace_bytes(_int64(rows), _int64(dim)))
+
+
+def zs_rms_norm_backward(dy, h, weight, rstd, dh, *, scales=None, dresidual=None, dweight=None, first=False,
+                         workspace=None, stream=None):
+    """dh = rstd * (dy * weight - xh * mean(dy * weight * xh)) (+ dresidual) for xh = h * rstd, and (0 if
+    first else the old value) + the sum of dy * xh over rows in dweight where given, which then needs a
+    workspace. h is what was normed, in dh's dtype, or its codes with their scales; dh has dy's
+    dtype or fp32 and may be dresidual."""
+    dev = _device_index(dy, "dy")
+    rows, dim, dy_ld = _rows2d(dy, "dy", dev)
+    dh_rows, dh_dim, dh_ld = _rows2d(dh, "dh", dev)
+    if dh_rows != rows or dh_dim != dim:
+        raise ValueError("dh must have dy's rows and width")
+    sc_ptr, sc_ld = None, 0
+    if scales is not None or (isinstance(h, _Tensor) and h.dtype in _CODE_TYPES):
+        h_ptr, h_ld, sc_ptr, sc_ld = _codes(h, scales, rows, dim, dev)
+        h_code = L.ZS_E4M3
+    else:
+        h_rows, h_dim, h_ld = _rows2d(h, "h", dev)
+        if h_rows != rows or h_dim != dim or h.dtype != dh.dtype:
+            raise ValueError("h must have dy's rows and width and dh's dtype, or be codes")
+        h_ptr, h_code = h.data_ptr(), _DTYPES[h.dtype]
+    r_ptr, r_ld = None, 0
+    if dresidual is not None:
+        r_rows, r_dim, r_ld = _rows2d(dresidual, "dresidual", dev)
+        if r_rows != rows or r_dim != dim or dresidual.dtype != dh.dtype:
+            raise ValueError("dresidual must have dy's rows and width and dh's dtype")
+        r_ptr = dresidual.data_ptr()
+    if rstd is None:
+        raise ValueError("rstd is that of the forward pass")
+    w = _vector(weight, "weight", dim, dev)
+    wdtype = dy.dtype if weight is None else weight.dtype
+    if wdtype not in _DTYPES:
+        raise ValueError(f"unsupported weight dtype {wdtype}")
+    gdtype = dy.dtype if dweight is None else dweight.dtype
+    dw = _vector(dweight, "dweight", dim, dev)
+    if gdtype not in _DTYPES:
+        raise ValueError(f"unsupported gradient dtype {gdtype}")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("zs_rms_norm_backward", dev, stream, dy.data_ptr(), _DTYPES[dy.dtype], dy_ld, h_ptr, h_code, h_ld, sc_ptr,
+          sc_ld, w, _DTYPES[wdtype], _vector(rstd, "rstd", rows, dev, torch.float32), r_ptr, r_ld, rows, dim,
+          dh.data_ptr(), dh_ld, _DTYPES[dh.dtype], dw, _DTYPES[gdtype], 1 if first else 0, ws, ws_bytes)
 
 
 # ---------------------------------------------------------------- loss over a vocabulary

@@ -34,7 +34,8 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
           "-ffp-contract=off"]
 
 SOURCES = ["abi.cpp", "tuning.cpp", "reduce.hip", "adamw.hip", "fused.hip", "accumulate.hip",
-           "segments.hip", "embed.hip", "layernorm.hip", "head_loss.hip"]
+           "segments.hip", "embed.hip", "layernorm.hip", "rmsnorm_forward.hip", "rmsnorm_backward.hip",
+           "activation.hip", "head_loss.hip"]
 
 
 def hipcc() -> str:

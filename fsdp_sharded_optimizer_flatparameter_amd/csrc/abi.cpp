@@ -107,6 +107,20 @@ bool any_overlap(const Span& a, const Span* b, int n) {
   return false;
 }
 
+// Activations in 8 bits: a byte and a share of a scale for each element.
+inline int64_t scale_blocks(int64_t dim) { return (dim + 127) / 128; }
+Span codes_span(const void* p, int64_t rows, int64_t dim, int64_t ld) {
+  return Span{p, p && rows > 0 && dim > 0 ? (rows - 1) * ld + dim : 0};
+}
+Span scales_span(const void* p, int64_t rows, int64_t dim, int64_t ld) {
+  return rows_span(p, rows, scale_blocks(dim), ld, ZS_F32);
+}
+inline bool codes_size_ok(int64_t rows, int64_t dim, int64_t codes_ld, int64_t scales_ld) {
+  return stride_ok(rows, dim, codes_ld) && stride_ok(rows, scale_blocks(dim), scales_ld);
+}
+// The residual stream has the type of what is added to it, or fp32.
+inline bool stream_type_ok(int32_t dtype, int32_t stream) { return stream == ZS_F32 || (stream == ZS_BF16 && dtype == ZS_BF16); }
+
 // Sizes of the loss over a vocabulary: 256 rows of three planes within 32 bits of
 // offset, a grid of tiles within 31 bits.
 inline bool head_size_ok(int64_t n, int64_t vocab, int64_t dim) {
@@ -604,6 +618,126 @@ zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, i
   return launch([&] {
     return zs::launch_layer_norm_backward(dy, dy_ld, x, x_ld, dtype, weight, wdtype, mean, rstd, rows, dim, dx, dx_ld,
                                           dweight, dbias, grad_dtype, first != 0, workspace, stream);
+  });
+}
+
+zs_status zs_activation_pack(const void* x, int32_t dtype, int64_t x_ld, int64_t rows, int64_t dim,
+                             uint8_t* codes, int64_t codes_ld, float* scales, int64_t scales_ld,
+                             hipStream_t stream) {
+  if (!float_type(dtype)) return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, x_ld) || !codes_size_ok(rows, dim, codes_ld, scales_ld)) return ZS_ERR_SIZE;
+  if (rows == 0 || dim == 0) return ZS_OK;
+  if (!x || !codes || !scales) return ZS_ERR_NULL;
+  if (!aligned(x, (uintptr_t)elem_size(dtype)) || !aligned(scales, 4)) return ZS_ERR_ALIGN;
+  const Span in = rows_span(x, rows, dim, x_ld, dtype), c = codes_span(codes, rows, dim, codes_ld),
+             sc = scales_span(scales, rows, dim, scales_ld);
+  if (any_overlap(c, &in, 1) || any_overlap(sc, &in, 1) || any_overlap(sc, &c, 1)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_activation_pack(x, dtype, x_ld, rows, dim, codes, codes_ld, scales, scales_ld, stream);
+  });
+}
+
+zs_status zs_activation_unpack(const uint8_t* codes, int64_t codes_ld, const float* scales,
+                               int64_t scales_ld, int64_t rows, int64_t dim, void* out, int32_t dtype,
+                               int64_t out_ld, hipStream_t stream) {
+  if (!float_type(dtype)) return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, out_ld) || !codes_size_ok(rows, dim, codes_ld, scales_ld)) return ZS_ERR_SIZE;
+  if (rows == 0 || dim == 0) return ZS_OK;
+  if (!codes || !scales || !out) return ZS_ERR_NULL;
+  if (!aligned(out, (uintptr_t)elem_size(dtype)) || !aligned(scales, 4)) return ZS_ERR_ALIGN;
+  const Span in[2] = {codes_span(codes, rows, dim, codes_ld), scales_span(scales, rows, dim, scales_ld)};
+  if (any_overlap(rows_span(out, rows, dim, out_ld, dtype), in, 2)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_activation_unpack(codes, codes_ld, scales, scales_ld, rows, dim, out, dtype, out_ld, stream);
+  });
+}
+
+zs_status zs_rms_norm_forward(const void* x, int32_t dtype, int64_t x_ld, const void* residual,
+                              int64_t residual_ld, void* sum, int64_t sum_ld, int32_t sum_dtype,
+                              const void* weight, int32_t wdtype, int64_t rows, int64_t dim, double eps,
+                              void* y, int64_t y_ld, uint8_t* codes, int64_t codes_ld, float* scales,
+                              int64_t scales_ld, float* rstd, hipStream_t stream) {
+  if (!float_type(dtype) || !float_type(wdtype) || (residual && !stream_type_ok(dtype, sum_dtype))) return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim) || (rows > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, x_ld) || (residual && !stride_ok(rows, dim, residual_ld)) ||
+      (sum && !stride_ok(rows, dim, sum_ld)) || (y && !stride_ok(rows, dim, y_ld)) ||
+      (codes && !codes_size_ok(rows, dim, codes_ld, scales_ld)))
+    return ZS_ERR_SIZE;
+  if (!std::isfinite((float)eps) || eps < 0) return ZS_ERR_HPARAM;
+  if (rows == 0) return ZS_OK;
+  if (!x || (!y && !codes) || (sum && !residual) || (codes == nullptr) != (scales == nullptr)) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), rs = (uintptr_t)elem_size(sum_dtype);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, (uintptr_t)elem_size(wdtype)) || !aligned(scales, 4) ||
+      !aligned(rstd, 4) || (residual && (!aligned(residual, rs) || !aligned(sum, rs))))
+    return ZS_ERR_ALIGN;
+  const Span in[3] = {rows_span(x, rows, dim, x_ld, dtype), rows_span(residual, rows, dim, residual_ld, sum_dtype),
+                      rows_span(weight, 1, dim, dim, wdtype)};
+  const Span out[5] = {rows_span(sum, rows, dim, sum_ld, sum_dtype), rows_span(y, rows, dim, y_ld, dtype),
+                       codes_span(codes, rows, dim, codes_ld), scales_span(scales, rows, dim, scales_ld),
+                       {rstd, rstd ? rows * 4 : 0}};
+  // the sum may take the place of what it is made from: each element is read by the lane that writes it
+  const bool on_x = sum == x && sum_ld == x_ld && sum_dtype == dtype, on_residual = sum == residual && sum_ld == residual_ld;
+  if ((!on_x && any_overlap(out[0], &in[0], 1)) || (!on_residual && any_overlap(out[0], &in[1], 1)) ||
+      any_overlap(out[0], &in[2], 1))
+    return ZS_ERR_OVERLAP;
+  for (int i = 1; i < 5; ++i)
+    if (any_overlap(out[i], in, 3) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  return launch([&] {
+    return zs::launch_rms_norm_forward(x, dtype, x_ld, residual, residual_ld, sum, sum_ld, residual ? sum_dtype : dtype,
+                                       weight, wdtype, rows, dim, (float)eps, y, y_ld, codes, codes_ld, scales,
+                                       scales_ld, rstd, stream);
+  });
+}
+
+size_t zs_rms_norm_workspace_bytes(int64_t rows, int64_t dim) {
+  if (!count_ok(rows) || !dim_ok(dim)) return 0;
+  const zs::RmsPlan p = zs::rms_plan(rows, dim);
+  return (size_t)(p.parts * p.pitch) * sizeof(float);
+}
+
+zs_status zs_rms_norm_backward(const void* dy, int32_t dtype, int64_t dy_ld, const void* h,
+                               int32_t h_dtype, int64_t h_ld, const float* scales, int64_t scales_ld,
+                               const void* weight, int32_t wdtype, const float* rstd, const void* dres,
+                               int64_t dres_ld, int64_t rows, int64_t dim, void* dh, int64_t dh_ld,
+                               int32_t dh_dtype, void* dweight, int32_t grad_dtype, int32_t first,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const bool kept8 = h_dtype == ZS_E4M3;
+  if (!float_type(dtype) || !float_type(wdtype) || !float_type(grad_dtype) || !stream_type_ok(dtype, dh_dtype) ||
+      (!kept8 && h_dtype != dh_dtype))
+    return ZS_ERR_DTYPE;
+  if (!count_ok(rows) || !dim_ok(dim) || (rows > 0 && dim < 1)) return ZS_ERR_SIZE;
+  if (!stride_ok(rows, dim, dy_ld) || !stride_ok(rows, dim, h_ld) || !stride_ok(rows, dim, dh_ld) ||
+      (kept8 && !stride_ok(rows, scale_blocks(dim), scales_ld)) || (dres && !stride_ok(rows, dim, dres_ld)))
+    return ZS_ERR_SIZE;
+  if (dim == 0 || (rows == 0 && (!dweight || !first))) return ZS_OK;
+  if (rows > 0 && (!dy || !h || !rstd || !dh || (kept8 && !scales))) return ZS_ERR_NULL;
+  const uintptr_t es = (uintptr_t)elem_size(dtype), rs = (uintptr_t)elem_size(dh_dtype);
+  if (rows > 0 && (!aligned(dy, es) || !aligned(h, kept8 ? 1 : rs) || !aligned(dh, rs) || !aligned(dres, rs) ||
+                   !aligned(rstd, 4) || (kept8 && !aligned(scales, 4)) ||
+                   !aligned(weight, (uintptr_t)elem_size(wdtype))))
+    return ZS_ERR_ALIGN;
+  if (!aligned(dweight, (uintptr_t)elem_size(grad_dtype))) return ZS_ERR_ALIGN;
+  const size_t need = dweight ? zs_rms_norm_workspace_bytes(rows, dim) : 0;
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return ZS_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return ZS_ERR_ALIGN;
+  }
+  const Span in[6] = {rows_span(dres, rows, dim, dres_ld, dh_dtype), rows_span(dy, rows, dim, dy_ld, dtype),
+                      kept8 ? codes_span(h, rows, dim, h_ld) : rows_span(h, rows, dim, h_ld, dh_dtype),
+                      scales_span(kept8 ? scales : nullptr, rows, dim, scales_ld),
+                      rows_span(weight, rows > 0, dim, dim, wdtype), {rstd, rows * 4}};
+  const Span out[3] = {rows_span(dh, rows, dim, dh_ld, dh_dtype), rows_span(dweight, 1, dim, dim, grad_dtype),
+                       {workspace, (int64_t)need}};
+  for (int i = 0; i < 3; ++i) {
+    const int skip = i == 0 && dh == dres && dh_ld == dres_ld ? 1 : 0;  // in place: read by the lane that writes
+    if (any_overlap(out[i], in + skip, 6 - skip) || any_overlap(out[i], out, i)) return ZS_ERR_OVERLAP;
+  }
+  return launch([&] {
+    return zs::launch_rms_norm_backward(dy, dtype, dy_ld, h, h_dtype, h_ld, scales, scales_ld, weight, wdtype, rstd, dres,
+                                        dres_ld, rows, dim, dh, dh_ld, dh_dtype, dweight, grad_dtype, first != 0,
+                                        workspace, stream);
   });
 }
 

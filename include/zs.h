@@ -20,6 +20,10 @@
  * And around the update, for the parameters that no matrix product stands for:
  *   embedding   zs_embed_forward, zs_embed_backward
  *   layer norm  zs_layer_norm_forward, zs_layer_norm_backward
+ *   RMS norm    zs_rms_norm_forward, zs_rms_norm_backward (with the residual's
+ *               addition; outputs and kept inputs in 8 bits)
+ * For what the passes between keep:
+ *   activations zs_activation_pack, zs_activation_unpack (8 bits)
  * And for the head, which may be the embedding's table:
  *   loss        zs_linear_cross_entropy_forward, zs_linear_cross_entropy_backward
  *
@@ -95,6 +99,9 @@ typedef int32_t zs_status;
 /* Element types of gradient contributions and parameters. */
 #define ZS_F32 0
 #define ZS_BF16 1
+
+/* Type of activations kept in 8 bits (zs_activation_pack). */
+#define ZS_E4M3 4
 
 /* Types of token and position ids. */
 #define ZS_I32 2
@@ -593,6 +600,109 @@ zs_status zs_layer_norm_backward(const void* dy, int64_t dy_ld, const void* x, i
                                  const float* rstd, int64_t rows, int64_t dim, void* dx, int64_t dx_ld,
                                  void* dweight, void* dbias, int32_t grad_dtype, int32_t first,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Activations in 8 bits: codes[rows, dim] are e4m3 (sign, 4 bits of exponent, 3 of
+ * mantissa, largest finite value 448, no infinity), scales[rows, ceil(dim / 128)]
+ * fp32, one for each block of 128 consecutive elements of a row (the last may be
+ * short); a value is code * scale. A block's scale is the smallest power of two,
+ * at least 2^-117, with which its largest finite magnitude stays within 448 (1
+ * where all are zero): values are rounded once, to nearest even, and what they
+ * stand for is exact in bf16 and fp32. Infinities and NaN become NaN, and are no
+ * measure of the scale; magnitudes above 1.875 * 2^127 become that.
+ */
+
+/*
+ * zs_activation_pack -- rows in 8 bits.
+ *   x[rows, dim]       DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride x_ld
+ *   codes[rows, dim]   DEVICE, row stride codes_ld
+ *   scales[rows, ceil(dim / 128)]
+ *                      DEVICE fp32, row stride scales_ld
+ * No output may share bytes with another argument. Errors: ZS_ERR_NULL,
+ * ZS_ERR_SIZE, ZS_ERR_DTYPE, ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_activation_pack(const void* x, int32_t dtype, int64_t x_ld, int64_t rows, int64_t dim,
+                             uint8_t* codes, int64_t codes_ld, float* scales, int64_t scales_ld,
+                             hipStream_t stream);
+
+/*
+ * zs_activation_unpack -- out[rows, dim] = code * scale, in `dtype` (ZS_F32 or
+ * ZS_BF16) with row stride out_ld. Other scales than those of the calls here are
+ * taken as they are, and products rounded. Otherwise as above.
+ */
+zs_status zs_activation_unpack(const uint8_t* codes, int64_t codes_ld, const float* scales,
+                               int64_t scales_ld, int64_t rows, int64_t dim, void* out, int32_t dtype,
+                               int64_t out_ld, hipStream_t stream);
+
+/*
+ * zs_rms_norm_forward -- root-mean-square norm over the last dimension, with the
+ * residual's addition before it and an output in 8 bits.
+ *   x[rows, dim]       DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride x_ld
+ *   residual[rows, dim]
+ *                      optional DEVICE (NULL = none), `sum_dtype`, row stride residual_ld
+ *   sum[rows, dim]     optional DEVICE output, `sum_dtype`, row stride sum_ld: h = x +
+ *                      residual, the residual stream behind this place; only with a
+ *                      residual. It may be residual itself, or x where the types are
+ *                      the same (same address and stride)
+ *   sum_dtype          `dtype`, or ZS_F32 with bf16 x; read only with a residual
+ *   weight[dim]        DEVICE, `wdtype` (ZS_F32 or ZS_BF16), or NULL (ones)
+ *   eps                finite in fp32, >= 0
+ *   y[rows, dim]       DEVICE, `dtype`, row stride y_ld: y = h * rstd * weight with
+ *                      rstd = 1 / sqrt(sum(h^2) / dim + eps), of h before it is
+ *                      rounded; NULL (skip) only with codes
+ *   codes[rows, dim], scales[rows, ceil(dim / 128)]
+ *                      optional DEVICE (both or none): y in 8 bits, as
+ *                      zs_activation_pack gives it for y before its rounding
+ *   rstd[rows]         optional DEVICE fp32 (the backward pass needs it)
+ * Apart from sum in place no output may share bytes with another argument.
+ * Squares are added in fp32: magnitudes above 2^63 overflow to rstd = 0. Errors:
+ * ZS_ERR_NULL (sum without residual, neither y nor codes, codes or scales alone
+ * among them), ZS_ERR_SIZE (dim < 1 with rows > 0 among them), ZS_ERR_DTYPE,
+ * ZS_ERR_HPARAM, ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_rms_norm_forward(const void* x, int32_t dtype, int64_t x_ld, const void* residual,
+                              int64_t residual_ld, void* sum, int64_t sum_ld, int32_t sum_dtype,
+                              const void* weight, int32_t wdtype, int64_t rows, int64_t dim, double eps,
+                              void* y, int64_t y_ld, uint8_t* codes, int64_t codes_ld, float* scales,
+                              int64_t scales_ld, float* rstd, hipStream_t stream);
+
+/* Bytes of workspace zs_rms_norm_backward needs for the weight's gradient (0 for
+ * sizes it refuses). The contents need no initialisation. */
+size_t zs_rms_norm_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * zs_rms_norm_backward -- gradients of the RMS norm.
+ *   dy[rows, dim]      DEVICE, `dtype` (ZS_F32 or ZS_BF16), row stride dy_ld
+ *   h[rows, dim]       DEVICE, what was normed (sum, or x without a residual), row
+ *                      stride h_ld: `dh_dtype`, or ZS_E4M3 codes with
+ *   scales[rows, ceil(dim / 128)]
+ *                      DEVICE fp32, row stride scales_ld, read only with codes
+ *   weight[dim]        DEVICE, `wdtype`, or NULL (ones)
+ *   rstd[rows]         DEVICE fp32, as zs_rms_norm_forward gives it
+ *   dres[rows, dim]    optional DEVICE (NULL = none), `dh_dtype`, row stride dres_ld:
+ *                      the gradient that reaches h along the residual stream
+ *   dh[rows, dim]      DEVICE, `dh_dtype` (`dtype`, or ZS_F32 with bf16 dy), row
+ *                      stride dh_ld: with xh = h * rstd,
+ *                      dh = rstd * (dy * weight - xh * mean(dy * weight * xh)) + dres,
+ *                      the gradient of x and of the residual alike; it may be dres
+ *                      itself (same address and stride)
+ *   dweight[dim]       optional DEVICE, `grad_dtype`:
+ *                      (first ? 0 : dweight) + sum over rows of dy * xh
+ *   workspace          DEVICE scratch of at least zs_rms_norm_workspace_bytes(rows,
+ *                      dim) bytes on a 16-byte boundary, required unless dweight is
+ *                      NULL or there are no rows; calls and graph replays that may run
+ *                      at the same time need one each
+ * rows == 0 with first != 0 sets dweight to zero. Apart from dh in place no output
+ * may share bytes with an input, the workspace or another output. Errors:
+ * ZS_ERR_NULL, ZS_ERR_SIZE, ZS_ERR_DTYPE, ZS_ERR_WORKSPACE, ZS_ERR_ALIGN,
+ * ZS_ERR_OVERLAP, ZS_ERR_HIP.
+ */
+zs_status zs_rms_norm_backward(const void* dy, int32_t dtype, int64_t dy_ld, const void* h,
+                               int32_t h_dtype, int64_t h_ld, const float* scales, int64_t scales_ld,
+                               const void* weight, int32_t wdtype, const float* rstd, const void* dres,
+                               int64_t dres_ld, int64_t rows, int64_t dim, void* dh, int64_t dh_ld,
+                               int32_t dh_dtype, void* dweight, int32_t grad_dtype, int32_t first,
+                               void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of workspace that the two calls below need for n tokens over [vocab, dim],
  * with hidden states and weight of `dtype`: zs_linear_cross_entropy_backward with
