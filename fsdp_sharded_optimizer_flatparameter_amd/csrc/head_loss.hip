@@ -158,7 +158,7 @@ struct Tile {
   int64_t m, n;
 };
 __device__ __forceinline__ Tile tile_of(uint32_t id, uint32_t total, uint32_t tm, uint32_t tn) {
-  constexpr uint32_t DEEP = 4;
+  constexpr uint32_t DEEP = 8;
   const uint32_t xcd = id & 7, per = total >> 3, rest = total & 7;
   const uint32_t at = xcd * per + (xcd < rest ? xcd : rest) + (id >> 3);
   const uint32_t g = at / (DEEP * tn), in = at % (DEEP * tn);

@@ -54,6 +54,18 @@ struct GemmShape {
 };
 
 #ifdef __HIP_DEVICE_COMPILE__  // the host's pass does not know the buffer types
+// 16 bytes from byte `off` of each lane behind the buffer's start to LDS, lane l's
+// to 16 l behind `lds`. Written out, as behind the builtin the compiler waits for
+// all loads before the next transposing read (ds_read_b64_tr_b16), which it
+// takes to read what they write; the waits are gemm_tile's own. M0 holds the LDS
+// address, and needs a wait state before it is used.
+__device__ __forceinline__ void load_to_lds(u32x4 buffer, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(off), "s"(buffer)
+               : "memory");
+}
+
 // The part of an operand that one workgroup reads: SIDE rows (or columns) from
 // `start` on, 64 values of k at a time.
 //
@@ -107,19 +119,20 @@ struct SideTile {
       offsets_k_is_row(g.cols - start, kBK);
     }
   }
-  __device__ __forceinline__ void load(char* lds, int p, int64_t k, int64_t cols_left) {
+  // where the values of plane p from k on come from
+  __device__ __forceinline__ u32x4 source(int p, int64_t k, int64_t cols_left) {
     const uint16_t* from = base + p * plane + (MODE == K_IN_ROWS ? k : k * ld);
     if constexpr (MODE == K_IS_ROW) {
       const int there = k + kBK <= rows ? kBK : (int)(rows - k);
       if (there != live) offsets_k_is_row(cols_left, there);
     }
-    const __amdgpu_buffer_rsrc_t rsrc =
-        __builtin_amdgcn_make_buffer_rsrc((void*)from, 0, 0xffffffffu, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rsrc, (__attribute__((address_space(3))) void*)(lds + (i * S::THREADS + (tid & ~63)) * 16), 16, off[i], 0, 0,
-          0);
+    const uint64_t at = (uint64_t)from;
+    return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, 0xffffffffu, 0x00020000u};
+  }
+  // the thread's load i of N
+  __device__ __forceinline__ void load(int i, u32x4 from, char* lds) const {
+    load_to_lds(from, (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds +
+                          (uint32_t)__builtin_amdgcn_readfirstlane((i * S::THREADS + (tid & ~63)) * 16), off[i]);
   }
 };
 
@@ -153,8 +166,11 @@ struct Fragments {
   }
 };
 
-// All loads to LDS that this wave has sent off are done.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// This wave's reads of LDS are done, and all its loads but the last N.
+template <int N>
+__device__ __forceinline__ void wait_reads_and_loads_but() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -165,8 +181,17 @@ __device__ __forceinline__ void barrier() {
 // acc += the product over stages [s0, s1) of the `segs.count * steps` that there
 // are, `steps` to a segment. Lane l of the wave at (wm, wn) gets in acc[i][j][r]
 // row wm BM / WM + 16 i + 4 (l / 16) + r and column wn BN / WN + 16 j + l % 16 of
-// the tile. Two stages in LDS: the loads of the next are on their way while the
-// products of this one are made, with one barrier between.
+// the tile.
+//
+// Two stages lie in LDS. The fragments of a step are read during the products of
+// the step before, so the one barrier of a stage stands before its last step:
+// behind it everybody has read this stage, and the next stage but one can come
+// into its place while the last step's and the next stage's products are made.
+// A 256 x 256 tile on 8 waves: 1250 TFLOP/s for 16384 x 8192 x 4096 in each of
+// the three layouts (1030, 890 and 920 with reads, products and a barrier in
+// turn), of the 1490 that the same loop reaches without loads. Stages of 32
+// values, four or five in LDS: 1130; loads sent off a few with each step: 1210 to
+// 1260; 32 x 32 x 16 products: 1190; of zeros, at the full clock: 1370.
 template <class S, GemmMode MA, GemmMode MB>
 __device__ __forceinline__ void gemm_tile(const GemmSide& a, const GemmSide& b, int64_t start_a, int64_t start_b,
                                           const Segments& segs, int steps, int s0, int s1, char* lds,
@@ -183,32 +208,66 @@ __device__ __forceinline__ void gemm_tile(const GemmSide& a, const GemmSide& b, 
   ga.init(wm * (S::BM / S::WM));
   gb.init(wn * (S::BN / S::WN));
   constexpr int A_BYTES = S::BM * kBK * 2;
+  const int n = s1 - s0;
+  if (n <= 0) return;
+  constexpr int NA = SideTile<S, S::BM, MA>::N, NB = SideTile<S, S::BN, MB>::N;  // a thread's loads for a stage
   int seg = s0 / steps, step = s0 % steps;
-  auto load = [&](char* stage) {
+  auto load = [&](char* stage) {  // all of the next stage
     const int64_t k = (int64_t)step * kBK;
-    la.load(stage, (segs.a >> (4 * seg)) & 15, k, a.cols - start_a);
-    lb.load(stage + A_BYTES, (segs.b >> (4 * seg)) & 15, k, b.cols - start_b);
+    const u32x4 from_a = la.source((segs.a >> (4 * seg)) & 15, k, a.cols - start_a);
+    const u32x4 from_b = lb.source((segs.b >> (4 * seg)) & 15, k, b.cols - start_b);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) la.load(i, from_a, stage);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) lb.load(i, from_b, stage + A_BYTES);
     if (++step == steps) step = 0, ++seg;
   };
-  if (s0 < s1) load(lds);
-  for (int s = s0; s < s1; ++s) {
-    char* now = lds + ((s - s0) & 1) * S::STAGE_BYTES;
-    wait_loads();
-    barrier();  // everybody's loads of this stage are done, and nobody reads the other any more
-    if (s + 1 < s1) load(lds + ((s - s0 + 1) & 1) * S::STAGE_BYTES);
+  // A stage's products in steps of two rows of tiles, STEPS for each half of its
+  // values of k. The fragments of a step are read during the step before.
+  constexpr int STEPS = S::TM / 2, LAST = 2 * STEPS - 1;
+  bf16x8 fa[2][2], fb[2][S::TN];
+  auto read = [&](int u, const char* stage) {  // u is a constant after unrolling
+    const int kk = u / STEPS, i = u % STEPS * 2;
+    if (i == 0)
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 fa[S::TM], fb[S::TN];
+      for (int j = 0; j < S::TN; ++j) fb[kk][j] = gb.get(stage + A_BYTES, j, kk);
+    fa[u & 1][0] = ga.get(stage, i, kk);
+    fa[u & 1][1] = ga.get(stage, i + 1, kk);
+  };
+  auto multiply = [&](int u) {
+    const int kk = u / STEPS, i = u % STEPS * 2;
 #pragma unroll
-      for (int j = 0; j < S::TN; ++j) fb[j] = gb.get(now + A_BYTES, j, kk);
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int i = 0; i < S::TM; ++i) fa[i] = ga.get(now, i, kk);
+      for (int j = 0; j < S::TN; ++j)
+        acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u & 1][x], fb[kk][j], acc[i + x][j], 0, 0, 0);
+  };
+  load(lds);
+  if (n > 1) {
+    load(lds + S::STAGE_BYTES);
+    wait_reads_and_loads_but<NA + NB>();
+  } else {
+    wait_reads_and_loads_but<0>();
+  }
+  barrier();
+  read(0, lds);
+  for (int s = 0; s < n; ++s) {
+    char* now = lds + (s & 1) * S::STAGE_BYTES;
+    const char* next = lds + (~s & 1) * S::STAGE_BYTES;
 #pragma unroll
-      for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    for (int u = 0; u < LAST; ++u) {
+      read(u + 1, now);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(u);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    wait_reads_and_loads_but<0>();
+    barrier();  // everybody has read this stage, and everybody's loads of the next are done
+    if (s + 1 < n) read(0, next);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(LAST);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + 2 < n) load(now);
   }
 #endif
 }
