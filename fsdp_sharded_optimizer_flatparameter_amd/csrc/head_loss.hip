@@ -186,82 +186,110 @@ __device__ __forceinline__ float join4(float x, bool take_max) {  // over the la
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// The tiles of one workgroup, one after another: make(at) aims the loop at a tile,
+// finish(at) uses its products and says whether all lanes have sent off at least
+// kStored stores.
+template <class S, GemmMode MA, GemmMode MB, typename Make, typename Finish>
+__device__ __forceinline__ void tiles_of(char* lds, uint32_t total, uint32_t tm, uint32_t tn, Make&& make, Finish&& finish) {
+  TileLoop<S, MA, MB> loop;
+  uint32_t id = blockIdx.x;
+  if (id >= total) return;  // uniform
+  Tile at = tile_of(id, total, tm, tn);
+  make(loop, at);
+  loop.preload(lds);
+  bool stored = false;
+  while (true) {
+    typename S::Acc acc;
+    clear<S>(acc);
+    loop.run(lds, acc, stored);
+    const Tile done = at;
+    id += gridDim.x;
+    if (id < total) {
+      at = tile_of(id, total, tm, tn);
+      make(loop, at);
+      loop.preload(lds);
+    }
+    stored = finish(done, acc);
+    if (id >= total) return;
+  }
+}
+
 // Rows of the tile are rows of the head, columns tokens: a lane holds 4 TM
-// logits of each of its TN tokens.
-template <class S, bool GRAD>
-__global__ __launch_bounds__(S::THREADS)
-void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, uint32_t tm, uint32_t tn, int64_t v0, int64_t vocab,
-              Tokens tok, float2* __restrict__ parts, float* __restrict__ own, int64_t np, uint16_t* __restrict__ g,
-              int64_t gp, int gplanes) {
+// logits of each of its TN tokens. PLANES: 0 for the loss, else those of g.
+template <class S, int PLANES>
+__global__ __launch_bounds__(S::THREADS, 2)
+void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Tokens tok, float2* __restrict__ parts,
+              float* __restrict__ own, int64_t np, uint16_t* __restrict__ g, int64_t gp) {
   __shared__ __align__(1024) char lds[S::LDS];
-  const Tile at = tile_of(blockIdx.x, gridDim.x, tm, tn);
-  const int64_t count = *tok.count;
-  if (at.n * S::BN >= (GRAD ? (count + 63) / 64 * 64 : count)) return;  // uniform
-  typename S::Acc acc;
-  clear<S>(acc);
-  gemm_tile<S, K_IN_ROWS, K_IN_ROWS>(w, h, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps, lds, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
-  const int q4 = (lane >> 4) * 4;
-  const int row0 = wm * (S::BM / S::WM);                    // of the wave in the tile
-  const int64_t in_piece = at.m * S::BM + row0 + q4;        // of acc[0][.][0], from v0 on
-  const int left = (int)(w.rows - in_piece);                // rows of the head there are from it on
+  __shared__ float2 joined[PLANES ? 1 : S::WM * S::BN];
+  const int64_t count = *tok.count, written = PLANES ? (count + 63) / 64 * 64 : count;
+  const uint32_t tm = (uint32_t)((w.rows + S::BM - 1) / S::BM), tn = (uint32_t)((written + S::BN - 1) / S::BN);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN, q4 = (lane >> 4) * 4;
+  constexpr int ROWS = S::BM / S::WM;  // of a wave
+  auto make = [&](auto& loop, const Tile& at) {
+    loop.aim(w, h, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps);
+  };
+  auto finish = [&](const Tile& at, typename S::Acc& acc) {
+    const int64_t first = at.m * S::BM + wm * ROWS;  // the wave's first row, from v0 on
+    const int left = (int)(w.rows - first) - q4;     // rows of the head from acc[0][.][0] on
+    // a wave whose rows and tokens are all there needs no comparison for each logit
+    const bool whole = w.rows - first >= ROWS && at.n * S::BN + S::BN <= count;
+    const bool whole_tile = w.rows - at.m * S::BM >= S::BM && at.n * S::BN + S::BN <= count;  // the same in all waves
 #pragma unroll
-  for (int j = 0; j < S::TN; ++j) {
-    const int col = wn * (S::BN / S::WN) + j * 16 + (lane & 15);
-    const int64_t token = at.n * S::BN + col;
-    const bool live = token < count;
-    const int label = live ? tok.label[token] : -1;
-    const int mine = label >= 0 ? (int)(label - v0 - in_piece) : -1;  // the label's place among the lane's rows
-    if constexpr (!GRAD) {
-      float top = -INFINITY;
+    for (int j = 0; j < S::TN; ++j) {
+      const int col = wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+      const int64_t token = at.n * S::BN + col;
+      const bool live = token < count;
+      const int label = live ? tok.label[token] : -1;
+      const int mine = label >= 0 ? (int)(label - v0 - first) - q4 : -1;  // the label's place among the lane's rows
+      const bool hit = __any(mine >= 0 && mine < 16 * S::TM && (mine & 15) < 4);
+      auto each = [&](auto f) {
 #pragma unroll
-      for (int i = 0; i < S::TM; ++i)
+        for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * i + r < left) top = fmaxf(top, acc[i][j][r]);
-      top = join4(top, true);
-      const float from = top == -INFINITY ? 0.0f : top;  // no row, or none above it: exp(-inf) = 0, not of -inf + inf
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float z = acc[i][j][r];
-          if (16 * i + r < left) sum += exp_of(z - from);
-          if (mine == 16 * i + r) own[token] = z;
-        }
-      sum = join4(sum, false);
-      if (S::WM == 1) {
-        if (q4 == 0 && live) parts[at.m * np + token] = float2{top, sum};
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = f(acc[i][j][r], 16 * i + r);
+      };
+      if constexpr (PLANES == 0) {
+        if (!whole) each([&](float z, int row) { return row < left ? z : -INFINITY; });
+        if (hit)
+          each([&](float z, int row) {
+            if (row == mine) own[token] = z;
+            return z;
+          });
+        float top = -INFINITY;
+        each([&](float z, int) {
+          top = fmaxf(top, z);
+          return z;
+        });
+        top = join4(top, true);
+        const float from = top == -INFINITY ? 0.0f : top;  // exp(-inf) = 0 where all are that, not of -inf + inf
+        float sum = 0.0f;
+        each([&](float z, int) {
+          sum += exp_of(z - from);
+          return z;
+        });
+        sum = join4(sum, false);
+        if (j == 0) __syncthreads();  // nobody reads the last tile's any more
+        if (q4 == 0) joined[wm * S::BN + col] = float2{top, sum};
       } else {
-        float2* mine_of = reinterpret_cast<float2*>(lds) + wm * S::BN;  // behind the barrier below
-        if (j == 0) __syncthreads();  // nobody reads the last stage any more
-        if (q4 == 0) mine_of[col] = float2{top, sum};
-      }
-    } else {
-      const float lse = live ? tok.lse[token] : 0.0f, coef = live ? tok.coef[token] : 0.0f;
+        const float lse = live ? tok.lse[token] : 0.0f, coef = live ? tok.coef[token] : 0.0f;
+        each([&](float z, int) { return exp_of(z - lse); });
+        if (hit) each([&](float p, int row) { return row == mine ? p - 1.0f : p; });
+        if (whole) each([&](float p, int) { return coef * p; });
+        else each([&](float p, int row) { return live && row < left ? coef * p : 0.0f; });
+        uint16_t* row = g + token * gp * PLANES + first + q4;
 #pragma unroll
-      for (int i = 0; i < S::TM; ++i) {
-        const int64_t v = in_piece + 16 * i;
-        float d[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float p = exp_of(acc[i][j][r] - lse);
-          const float e = mine == 16 * i + r ? p - 1.0f : p;
-          d[r] = live && label >= 0 && 16 * i + r < left ? coef * e : 0.0f;
-        }
-        if (token < np && v < gp) {
-          uint16_t* to = g + token * gp * gplanes + v;
-          uint32_t lo[2], hi[2];
-          if (gplanes < 3) {
-            hi[0] = pack_bf16(d[0], d[1]);
-            hi[1] = pack_bf16(d[2], d[3]);
+        for (int i = 0; i < S::TM; ++i) {
+          if (!whole_tile && (token >= written || first + 16 * i >= gp)) continue;
+          const f32x4 d = acc[i][j];
+          uint16_t* to = row + 16 * i;
+          if constexpr (PLANES < 3) {
+            const uint32_t hi[2] = {pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
             *(uint2*)to = uint2{hi[0], hi[1]};
-            if (gplanes == 2) {
-              lo[0] = pack_bf16(d[0] - bf16_lo(hi[0]), d[1] - bf16_hi(hi[0]));
-              lo[1] = pack_bf16(d[2] - bf16_lo(hi[1]), d[3] - bf16_hi(hi[1]));
-              *(uint2*)(to + gp) = uint2{lo[0], lo[1]};
-            }
+            if constexpr (PLANES == 2)
+              *(uint2*)(to + gp) = uint2{pack_bf16(d.x - bf16_lo(hi[0]), d.y - bf16_hi(hi[0])),
+                                         pack_bf16(d.z - bf16_lo(hi[1]), d.w - bf16_hi(hi[1]))};
           } else {
             uint32_t p[4][3];
 #pragma unroll
@@ -273,23 +301,25 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, uint32_t tm, uin
         }
       }
     }
-  }
-  if constexpr (!GRAD && S::WM > 1) {
-    __syncthreads();
-    const float2* all = reinterpret_cast<const float2*>(lds);
-    for (int c = threadIdx.x; c < S::BN; c += S::THREADS) {
-      const int64_t token = at.n * S::BN + c;
-      if (token >= count) continue;
-      float top = all[c].x;
+    if constexpr (PLANES == 0) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < S::BN; c += S::THREADS) {
+        const int64_t token = at.n * S::BN + c;
+        if (token >= count) continue;
+        float top = joined[c].x;
 #pragma unroll
-      for (int i = 1; i < S::WM; ++i) top = fmaxf(top, all[i * S::BN + c].x);
-      const float from = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f;
+        for (int i = 1; i < S::WM; ++i) top = fmaxf(top, joined[i * S::BN + c].x);
+        const float from = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < S::WM; ++i) sum += all[i * S::BN + c].y * exp_of(all[i * S::BN + c].x - from);
-      parts[at.m * np + token] = float2{top, sum};
+        for (int i = 0; i < S::WM; ++i) sum += joined[i * S::BN + c].y * exp_of(joined[i * S::BN + c].x - from);
+        parts[at.m * np + token] = float2{top, sum};
+      }
+      return false;
     }
-  }
+    return whole_tile && S::TM * S::TN >= 16;
+  };
+  tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
 }
 
 // Joins the tiles' maxima and sums: 16 tokens and 16 groups of tiles to a workgroup.
@@ -330,85 +360,95 @@ void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, co
 // The hidden states' gradient over one piece: rows of the tile are columns of the
 // hidden states, columns tokens. Split i of the sum goes to fp32 rows of its own.
 template <class S>
-__global__ __launch_bounds__(S::THREADS)
-void k_dhidden(GemmSide w, GemmSide g, Segments segs, int steps, uint32_t tm, uint32_t tn, int splits, int add,
-               const int32_t* __restrict__ count_of, float* __restrict__ out, int64_t dq, int64_t np) {
+__global__ __launch_bounds__(S::THREADS, 2)
+void k_dhidden(GemmSide w, GemmSide g, Segments segs, int steps, int splits, int add, const int32_t* __restrict__ count_of,
+               float* __restrict__ out, int64_t dq, int64_t np) {
   __shared__ __align__(1024) char lds[S::LDS];
-  const uint32_t tiles = tm * tn, split = blockIdx.x / tiles;
-  const Tile at = tile_of(blockIdx.x % tiles, tiles, tm, tn);
   const int64_t count = *count_of;
-  if (at.n * S::BN >= count) return;  // uniform
+  const uint32_t tm = (uint32_t)((w.cols + S::BM - 1) / S::BM), tn = (uint32_t)((count + S::BN - 1) / S::BN);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
   const int total = segs.count * steps;
-  const int s0 = (int)((int64_t)total * split / splits), s1 = (int)((int64_t)total * (split + 1) / splits);
-  typename S::Acc acc;
-  clear<S>(acc);
-  gemm_tile<S, K_IS_ROW, K_IN_ROWS>(w, g, at.m * S::BM, at.n * S::BN, segs, steps, s0, s1, lds, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
-  float* mine = out + (int64_t)split * np * dq;
+  // the splits of a tile lie behind one another in the tiles' order: tile.n = split * tn + n
+  auto make = [&](auto& loop, const Tile& at) {
+    const int64_t split = at.n / tn;
+    loop.aim(w, g, at.m * S::BM, at.n % tn * S::BN, segs, steps, (int)(total * split / splits),
+             (int)(total * (split + 1) / splits));
+  };
+  auto finish = [&](const Tile& at, typename S::Acc& acc) {
+    float* mine = out + (int64_t)(at.n / tn) * np * dq;
 #pragma unroll
-  for (int j = 0; j < S::TN; ++j) {
-    const int64_t token = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+    for (int j = 0; j < S::TN; ++j) {
+      const int64_t token = at.n % tn * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i) {
-      const int64_t c = at.m * S::BM + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
-      if (token < count && c < dq) {
-        f32x4* to = (f32x4*)(mine + token * dq + c);
-        *to = add ? *to + acc[i][j] : acc[i][j];
+      for (int i = 0; i < S::TM; ++i) {
+        const int64_t c = at.m * S::BM + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
+        if (token < count && c < dq) {
+          f32x4* to = (f32x4*)(mine + token * dq + c);
+          *to = add ? *to + acc[i][j] : acc[i][j];
+        }
       }
     }
-  }
+    return false;
+  };
+  tiles_of<S, K_IS_ROW, K_IN_ROWS>(lds, tm * tn * splits, tm, tn * splits, make, finish);
 }
 
 // The head's gradient for one piece: rows of the tile are columns of the hidden
 // states, columns rows of the head.
 template <class S, typename Gt>
-__global__ __launch_bounds__(S::THREADS)
-void k_dweight(GemmSide h, GemmSide g, Segments segs, uint32_t tm, uint32_t tn, const int32_t* __restrict__ count_of,
-               int64_t v0, int64_t vc, uint32_t dim, Gt* __restrict__ dw, int64_t dw_ld, int first) {
+__global__ __launch_bounds__(S::THREADS, 2)
+void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict__ count_of, int64_t v0, int64_t vc,
+               uint32_t dim, Gt* __restrict__ dw, int64_t dw_ld, int first) {
   __shared__ __align__(1024) char lds[S::LDS];
-  const Tile at = tile_of(blockIdx.x, gridDim.x, tm, tn);
-  const int steps = (int)((*count_of + 63) / 64);
-  typename S::Acc acc;
-  clear<S>(acc);
-  if (steps > 0)
-    gemm_tile<S, K_IS_ROW, K_IS_ROW>(h, g, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps, lds, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / S::WN, wn = wave % S::WN;
+  const uint32_t tm = (dim + S::BM - 1) / S::BM, tn = (uint32_t)((vc + S::BN - 1) / S::BN);
+  const int steps = (int)((*count_of + 63) / 64);  // none: the sums are zero
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  auto make = [&](auto& loop, const Tile& at) {
+    loop.aim(h, g, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps);
+  };
+  auto finish = [&](const Tile& at, typename S::Acc& acc) {
+    const bool whole = dim - at.m * S::BM >= S::BM && vc - at.n * S::BN >= S::BN;
 #pragma unroll
-  for (int j = 0; j < S::TN; ++j) {
-    const int64_t v = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
-    Gt* row = dw + (v0 + v) * dw_ld;
+    for (int j = 0; j < S::TN; ++j) {
+      const int64_t v = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+      Gt* row = dw + (v0 + v) * dw_ld;
 #pragma unroll
-    for (int i = 0; i < S::TM; ++i) {
-      const uint32_t c = (uint32_t)(at.m * S::BM) + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
-      if (v >= vc || c >= dim) continue;
-      f32x4 x = acc[i][j];
-      if (c + 4 <= dim) {
-        if constexpr (sizeof(Gt) == 4) {
-          if (!first) {
-            const u32x4 old = ld16(row + c);
-            x += f32x4{__uint_as_float(old.x), __uint_as_float(old.y), __uint_as_float(old.z), __uint_as_float(old.w)};
+      for (int i = 0; i < S::TM; ++i) {
+        const uint32_t c = (uint32_t)(at.m * S::BM) + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
+        if (!whole && (v >= vc || c >= dim)) continue;
+        f32x4 x = acc[i][j];
+        if (whole || c + 4 <= dim) {
+          if constexpr (sizeof(Gt) == 4) {
+            if (!first) {
+              const u32x4 old = ld16(row + c);
+              x += f32x4{__uint_as_float(old.x), __uint_as_float(old.y), __uint_as_float(old.z), __uint_as_float(old.w)};
+            }
+            st16(u32x4{__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)}, row + c);
+          } else {
+            const auto p = (__attribute__((address_space(1))) u32x2_any*)(row + c);
+            if (!first) {
+              const u32x2 old = *p;
+              x += f32x4{bf16_lo(old.x), bf16_hi(old.x), bf16_lo(old.y), bf16_hi(old.y)};
+            }
+            *p = u32x2{pack_bf16(x.x, x.y), pack_bf16(x.z, x.w)};
           }
-          st16(u32x4{__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)}, row + c);
         } else {
-          const auto p = (__attribute__((address_space(1))) u32x2_any*)(row + c);
-          if (!first) {
-            const u32x2 old = *p;
-            x += f32x4{bf16_lo(old.x), bf16_hi(old.x), bf16_lo(old.y), bf16_hi(old.y)};
+          for (uint32_t e = 0; c + e < dim; ++e) {
+            float y = e == 0 ? x.x : e == 1 ? x.y : x.z;
+            if (!first) {
+              if constexpr (sizeof(Gt) == 4) y += row[c + e];
+              else y += bf16_to_f32(row[c + e]);
+            }
+            st_g(round_to<Gt>(y), row + c + e);
           }
-          *p = u32x2{pack_bf16(x.x, x.y), pack_bf16(x.z, x.w)};
-        }
-      } else {
-        for (uint32_t e = 0; c + e < dim; ++e) {
-          float y = e == 0 ? x.x : e == 1 ? x.y : x.z;
-          if (!first) {
-            if constexpr (sizeof(Gt) == 4) y += row[c + e];
-            else y += bf16_to_f32(row[c + e]);
-          }
-          st_g(round_to<Gt>(y), row + c + e);
         }
       }
     }
-  }
+    return whole && S::TM * S::TN >= 16;
+  };
+  tiles_of<S, K_IS_ROW, K_IS_ROW>(lds, tm * tn, tm, tn, make, finish);
 }
 
 // The splits' sums, rounded once, back in the tokens' places; zeros where a token does not count.
@@ -467,19 +507,38 @@ Tokens tokens_at(const HeadPlan& p, void* workspace) {
                 (float*)(w + p.coef), (float*)(w + p.lse)};
 }
 
-// The tiles of a product of `m` by `n`: the time of a round of workgroups on
-// 256 CUs, one of the widest tile or two of the others at a time, which run at
-// 0.8 of its rate, times the rounds.
+// The tiles of a product, and how long it takes: rounds of tiles on 256 CUs, in
+// the time of one round of the widest. Two of the others run on a CU at once and
+// reach 0.72 of its rate (128 x 128: 890 TFLOP/s against 1250), one alone takes
+// 0.6 of the time of two.
 enum Cut { WIDE, SQUARE, NARROW };
-Cut cut_of(int64_t m, int64_t n) {
-  auto rounds = [&](int64_t bm, int64_t bn, int64_t at_once) {
-    const int64_t tiles = ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
-    return (tiles + 256 * at_once - 1) / (256 * at_once) * at_once;
-  };
-  const double wide = (double)rounds(256, 256, 1) * 256 * 256 * 0.8, square = (double)rounds(128, 128, 2) * 128 * 128,
-               narrow = (double)rounds(256, 64, 2) * 256 * 64;
-  if (n <= 64 && narrow <= square && narrow <= wide) return NARROW;
-  return square < wide ? SQUARE : WIDE;
+struct CutOf {
+  Cut cut;
+  double rounds;
+};
+CutOf cut_of(int64_t m, int64_t n) {
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+  auto pairs = [&](int64_t t) { return (double)(t / 512) + (t % 512 == 0 ? 0.0 : t % 512 <= 256 ? 0.6 : 1.0); };
+  const double wide = (double)((tiles(256, 256) + 255) / 256), square = pairs(tiles(128, 128)) * 0.5 / 0.72,
+               narrow = pairs(tiles(256, 64)) * 0.5 / 0.72;
+  if (n <= 64 && narrow <= square && narrow <= wide) return {NARROW, narrow};
+  return square < wide ? CutOf{SQUARE, square} : CutOf{WIDE, wide};
+}
+// What a round costs beside its stages (first loads, what is done with the products), in stages.
+constexpr double kRoundStages = 10;
+
+// Parts of the sum for the hidden states' gradient, so that its tiles fill the CUs: eight stages at least to each.
+int splits_of(int64_t dim, int64_t n, int64_t stages) {
+  const int64_t tiles = ((dim + 255) / 256) * ((n + 255) / 256);
+  const int64_t splits = least(512 / tiles, stages / 8);
+  return (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+}
+
+// As many workgroups as 256 CUs hold at once, or tiles, which they then take in turn.
+template <class S>
+unsigned workgroups(int64_t m, int64_t n, int64_t splits = 1) {
+  const int64_t tiles = ((m + S::BM - 1) / S::BM) * ((n + S::BN - 1) / S::BN) * splits;
+  return (unsigned)least(tiles, S::LDS <= 80 * 1024 ? 512 : 256);
 }
 
 template <typename F>
@@ -541,16 +600,35 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   most = most < 4096 ? 4096 : most > kMostPiece ? kMostPiece : most / 256 * 256;
   p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
-  p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
   p.splits = 1;
   if (grad && p.pieces) {
-    // the hidden states' gradient: enough tiles for two rounds on 256 CUs, eight stages at least to each part
-    const int64_t tiles = ((dim + 255) / 256) * ((n + 255) / 256);
-    const int64_t stages = p.piece / kBK * (p.planes == 3 ? kSix.count : 1);
-    int64_t splits = tiles > 0 ? 512 / tiles : 1;
-    splits = least(splits, stages / 8);
-    p.splits = (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+    // Of pieces of equal size and those whose head's gradient fills rounds of the widest tiles, what takes least.
+    const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1,
+                  wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;
+    auto one = [&](int64_t vc) {
+      const int64_t stages = up(vc, kBK) / kBK * parts;
+      const int splits = splits_of(dim, n, stages);
+      return cut_of(vc, n).rounds * (double)(p.dp / kBK * parts + kRoundStages) +
+             cut_of(dim, n * splits).rounds * ((double)stages / splits + kRoundStages) +
+             cut_of(dim, vc).rounds * (double)(p.np / kBK * wparts + kRoundStages);
+    };
+    auto all = [&](int64_t piece) {
+      const int64_t rest = vocab % piece;
+      return (double)(vocab / piece) * one(piece) + (rest ? one(rest) : 0.0);
+    };
+    double best = all(p.piece);
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+      const int64_t piece = rounds * 256 / tm * 256;
+      if (piece < 4096 || piece > most || piece >= vocab) continue;
+      const double cost = all(piece);
+      if (cost < best) {
+        best = cost;
+        p.piece = piece;
+      }
+    }
+    p.splits = splits_of(dim, n, p.piece / kBK * parts);
   }
+  p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -589,7 +667,7 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
     h = GemmSide{to, p.dp * p.planes, p.dp, p.np, 0};
   }
-  const Cut cut = cut_of(vocab, n);
+  const Cut cut = cut_of(vocab, n).cut;
   const int64_t piece = w_lies ? vocab : p.piece;
   for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
     const int64_t vc = least(piece, vocab - v0);
@@ -602,10 +680,9 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     }
     with_cut(cut, [&](auto shape) {
       using S = decltype(shape);
-      const uint32_t tm = (uint32_t)((vc + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
-      hipLaunchKernelGGL((k_logits<S, false>), dim3(tm * tn), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), tm,
-                         tn, v0, vocab, tok, (float2*)(ws + p.parts) + v0 / S::BM * p.np, (float*)(ws + p.own), p.np,
-                         (uint16_t*)nullptr, (int64_t)0, 0);
+      hipLaunchKernelGGL((k_logits<S, 0>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs,
+                         (int)(p.dp / kBK), v0, tok, (float2*)(ws + p.parts) + v0 / S::BM * p.np, (float*)(ws + p.own),
+                         p.np, (uint16_t*)nullptr, (int64_t)0);
     });
   }
   int64_t tiles = 0;
@@ -646,27 +723,28 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     }
     const GemmSide h{hp, p.dp * p.planes, p.dp, p.np, p.dp};
     const GemmSide g_rows{gp, ldg, vp, p.np, vp};
-    with_cut(cut_of(vc, n), [&](auto shape) {
+    with_cut(cut_of(vc, n).cut, [&](auto shape) {
       using S = decltype(shape);
-      const uint32_t tm = (uint32_t)((vc + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
-      hipLaunchKernelGGL((k_logits<S, true>), dim3(tm * tn), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), tm,
-                         tn, v0, vocab, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, p.gplanes);
+      auto go = [&](auto planes) {
+        hipLaunchKernelGGL((k_logits<S, decltype(planes)::value>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w,
+                           h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp);
+      };
+      if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
+      else if (p.gplanes == 2) go(std::integral_constant<int, 2>{});
+      else go(std::integral_constant<int, 3>{});
     });
-    with_cut(n <= 64 ? NARROW : cut_of(dim, n * p.splits), [&](auto shape) {
+    with_cut(n <= 64 ? NARROW : cut_of(dim, n * p.splits).cut, [&](auto shape) {
       using S = decltype(shape);
-      const uint32_t tm = (uint32_t)((dim + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
-      hipLaunchKernelGGL((k_dhidden<S>), dim3(tm * tn * p.splits), dim3(S::THREADS), 0, s, w, g_rows, segs,
-                         (int)(vp / kBK), tm, tn, p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np);
+      hipLaunchKernelGGL((k_dhidden<S>), dim3(workgroups<S>(dim, n, p.splits)), dim3(S::THREADS), 0, s, w, g_rows, segs,
+                         (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np);
     });
-    with_cut(cut_of(dim, vc) == SQUARE ? SQUARE : WIDE, [&](auto shape) {
+    with_cut(cut_of(dim, vc).cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {
       using S = std::conditional_t<std::is_same_v<decltype(shape), Square>, Square, Wide>;
-      const uint32_t tm = (uint32_t)((dim + S::BM - 1) / S::BM), tn = (uint32_t)((vc + S::BN - 1) / S::BN);
+      const unsigned grid = workgroups<S>(dim, vc);
       if (grad_dtype == ZS_BF16)
-        hipLaunchKernelGGL((k_dweight<S, uint16_t>), dim3(tm * tn), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tm, tn,
-                           tok.count, v0, vc, (uint32_t)dim, (uint16_t*)dweight, dweight_ld, (int)first);
+        hipLaunchKernelGGL((k_dweight<S, uint16_t>), dim3(grid), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tok.count, v0, vc, (uint32_t)dim, (uint16_t*)dweight, dweight_ld, (int)first);
       else
-        hipLaunchKernelGGL((k_dweight<S, float>), dim3(tm * tn), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tm, tn,
-                           tok.count, v0, vc, (uint32_t)dim, (float*)dweight, dweight_ld, (int)first);
+        hipLaunchKernelGGL((k_dweight<S, float>), dim3(grid), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tok.count, v0, vc, (uint32_t)dim, (float*)dweight, dweight_ld, (int)first);
     });
   }
   const unsigned grid = grid_of(n * ((dim + 7) / 8));

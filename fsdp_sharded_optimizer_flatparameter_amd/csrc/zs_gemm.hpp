@@ -178,10 +178,14 @@ __device__ __forceinline__ void barrier() {
 }
 #endif
 
-// acc += the product over stages [s0, s1) of the `segs.count * steps` that there
-// are, `steps` to a segment. Lane l of the wave at (wm, wn) gets in acc[i][j][r]
-// row wm BM / WM + 16 i + 4 (l / 16) + r and column wn BN / WN + 16 j + l % 16 of
-// the tile.
+// The product of one tile: aim(), preload(), run(). Lane l of the wave at (wm, wn)
+// gets in acc[i][j][r] row wm BM / WM + 16 i + 4 (l / 16) + r and column
+// wn BN / WN + 16 j + l % 16 of the tile.
+//
+// A workgroup that makes several tiles sends the first loads of the next off
+// before it does what it does with the products of this one: a tile of 12
+// stages waits as long for its first loads as it takes for some of its stages.
+// `run` leaves LDS to the next tile's loads.
 //
 // Two stages lie in LDS. The fragments of a step are read during the products of
 // the step before, so the one barrier of a stage stands before its last step:
@@ -193,83 +197,102 @@ __device__ __forceinline__ void barrier() {
 // values, four or five in LDS: 1130; loads sent off a few with each step: 1210 to
 // 1260; 32 x 32 x 16 products: 1190; of zeros, at the full clock: 1370.
 template <class S, GemmMode MA, GemmMode MB>
-__device__ __forceinline__ void gemm_tile(const GemmSide& a, const GemmSide& b, int64_t start_a, int64_t start_b,
-                                          const Segments& segs, int steps, int s0, int s1, char* lds,
-                                          typename S::Acc& acc) {
+struct TileLoop {
 #ifdef __HIP_DEVICE_COMPILE__
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
+  static constexpr int A_BYTES = S::BM * kBK * 2;
+  static constexpr int NA = SideTile<S, S::BM, MA>::N, NB = SideTile<S, S::BN, MB>::N;  // a thread's loads for a stage
   SideTile<S, S::BM, MA> la;
   SideTile<S, S::BN, MB> lb;
-  la.init(a, start_a);
-  lb.init(b, start_b);
-  Fragments<S::BM, MA> ga;
-  Fragments<S::BN, MB> gb;
-  ga.init(wm * (S::BM / S::WM));
-  gb.init(wn * (S::BN / S::WN));
-  constexpr int A_BYTES = S::BM * kBK * 2;
-  const int n = s1 - s0;
-  if (n <= 0) return;
-  constexpr int NA = SideTile<S, S::BM, MA>::N, NB = SideTile<S, S::BN, MB>::N;  // a thread's loads for a stage
-  int seg = s0 / steps, step = s0 % steps;
-  auto load = [&](char* stage) {  // all of the next stage
+  int64_t cols_a, cols_b;
+  Segments segs;
+  int steps, seg, step, n;  // stages of a segment, the next stage to load, stages of the tile
+
+  // At stages [s0, s1) of the `segs.count * steps` that there are, `steps` to a segment.
+  __device__ __forceinline__ void aim(const GemmSide& a, const GemmSide& b, int64_t start_a, int64_t start_b,
+                                      const Segments& sg, int per_segment, int s0, int s1) {
+    la.init(a, start_a);
+    lb.init(b, start_b);
+    cols_a = a.cols - start_a;
+    cols_b = b.cols - start_b;
+    segs = sg;
+    steps = per_segment;
+    n = s1 - s0;
+    seg = n > 0 ? s0 / steps : 0;
+    step = n > 0 ? s0 % steps : 0;
+  }
+  __device__ __forceinline__ void load(char* stage) {  // all of the next stage
     const int64_t k = (int64_t)step * kBK;
-    const u32x4 from_a = la.source((segs.a >> (4 * seg)) & 15, k, a.cols - start_a);
-    const u32x4 from_b = lb.source((segs.b >> (4 * seg)) & 15, k, b.cols - start_b);
+    const u32x4 from_a = la.source((segs.a >> (4 * seg)) & 15, k, cols_a);
+    const u32x4 from_b = lb.source((segs.b >> (4 * seg)) & 15, k, cols_b);
 #pragma unroll
     for (int i = 0; i < NA; ++i) la.load(i, from_a, stage);
 #pragma unroll
     for (int i = 0; i < NB; ++i) lb.load(i, from_b, stage + A_BYTES);
     if (++step == steps) step = 0, ++seg;
-  };
-  // A stage's products in steps of two rows of tiles, STEPS for each half of its
-  // values of k. The fragments of a step are read during the step before.
-  constexpr int STEPS = S::TM / 2, LAST = 2 * STEPS - 1;
-  bf16x8 fa[2][2], fb[2][S::TN];
-  auto read = [&](int u, const char* stage) {  // u is a constant after unrolling
-    const int kk = u / STEPS, i = u % STEPS * 2;
-    if (i == 0)
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j) fb[kk][j] = gb.get(stage + A_BYTES, j, kk);
-    fa[u & 1][0] = ga.get(stage, i, kk);
-    fa[u & 1][1] = ga.get(stage, i + 1, kk);
-  };
-  auto multiply = [&](int u) {
-    const int kk = u / STEPS, i = u % STEPS * 2;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j)
-        acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u & 1][x], fb[kk][j], acc[i + x][j], 0, 0, 0);
-  };
-  load(lds);
-  if (n > 1) {
-    load(lds + S::STAGE_BYTES);
-    wait_reads_and_loads_but<NA + NB>();
-  } else {
-    wait_reads_and_loads_but<0>();
   }
-  barrier();
-  read(0, lds);
-  for (int s = 0; s < n; ++s) {
-    char* now = lds + (s & 1) * S::STAGE_BYTES;
-    const char* next = lds + (~s & 1) * S::STAGE_BYTES;
+  __device__ __forceinline__ void preload(char* lds) {
+    if (n > 0) load(lds);
+    if (n > 1) load(lds + S::STAGE_BYTES);
+  }
+  // acc += the product. `stored`: at least kStored stores were sent off behind
+  // preload(); they need not be done.
+  static constexpr int kStored = 16;
+  __device__ __forceinline__ void run(char* lds, typename S::Acc& acc, bool stored) {
+    if (n <= 0) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Fragments<S::BM, MA> ga;
+    Fragments<S::BN, MB> gb;
+    ga.init(wave / S::WN * (S::BM / S::WM));
+    gb.init(wave % S::WN * (S::BN / S::WN));
+    // A stage's products in steps of two rows of tiles, STEPS for each half of its
+    // values of k. The fragments of a step are read during the step before.
+    constexpr int STEPS = S::TM / 2, LAST = 2 * STEPS - 1;
+    bf16x8 fa[2][2], fb[2][S::TN];
+    auto read = [&](int u, const char* stage) {  // u is a constant after unrolling
+      const int kk = u / STEPS, i = u % STEPS * 2;
+      if (i == 0)
 #pragma unroll
-    for (int u = 0; u < LAST; ++u) {
-      read(u + 1, now);
+        for (int j = 0; j < S::TN; ++j) fb[kk][j] = gb.get(stage + A_BYTES, j, kk);
+      fa[u & 1][0] = ga.get(stage, i, kk);
+      fa[u & 1][1] = ga.get(stage, i + 1, kk);
+    };
+    auto multiply = [&](int u) {
+      const int kk = u / STEPS, i = u % STEPS * 2;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+          acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u & 1][x], fb[kk][j], acc[i + x][j], 0, 0, 0);
+    };
+    if (n == 1) wait_reads_and_loads_but<0>();
+    else if (stored) wait_reads_and_loads_but<NA + NB + kStored>();
+    else wait_reads_and_loads_but<NA + NB>();
+    barrier();
+    read(0, lds);
+    for (int s = 0; s < n; ++s) {
+      char* now = lds + (s & 1) * S::STAGE_BYTES;
+      const char* next = lds + (~s & 1) * S::STAGE_BYTES;
+#pragma unroll
+      for (int u = 0; u < LAST; ++u) {
+        read(u + 1, now);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(u);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_reads_and_loads_but<0>();
+      barrier();  // everybody has read this stage, and everybody's loads of the next are done
+      if (s + 1 < n) read(0, next);
       __builtin_amdgcn_sched_barrier(0);
-      multiply(u);
+      multiply(LAST);
       __builtin_amdgcn_sched_barrier(0);
+      if (s + 2 < n) load(now);
     }
-    wait_reads_and_loads_but<0>();
-    barrier();  // everybody has read this stage, and everybody's loads of the next are done
-    if (s + 1 < n) read(0, next);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(LAST);
-    __builtin_amdgcn_sched_barrier(0);
-    if (s + 2 < n) load(now);
   }
+#else
+  __device__ void aim(const GemmSide&, const GemmSide&, int64_t, int64_t, const Segments&, int, int, int) {}
+  __device__ void preload(char*) {}
+  __device__ void run(char*, typename S::Acc&, bool) {}
 #endif
-}
+};
 
 }  // namespace zs
