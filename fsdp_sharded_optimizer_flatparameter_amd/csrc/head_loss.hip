@@ -54,11 +54,11 @@ struct Tokens {
 // ---------------------------------------------------------------- tokens
 
 constexpr int kTokBS = 1024;
+constexpr int kTokEach = 4;
 
-// One workgroup walks over the labels and numbers those that count (or, with
-// `gather` 0, keeps every row where it is). Rows that do not count get zeros in
-// loss and lse_out where given. Places behind the last one, up to a multiple of
-// 64, get a gradient of zero.
+// One workgroup walks over the labels, four to a thread, and numbers those that
+// count (or, with `gather` 0, keeps every row where it is). Rows that do not
+// count get zeros in loss and lse_out where given.
 template <typename I>
 __global__ __launch_bounds__(kTokBS)
 void k_tokens(const I* __restrict__ labels, int64_t n, int64_t vocab, int gather, const float* __restrict__ lse_in,
@@ -67,33 +67,54 @@ void k_tokens(const I* __restrict__ labels, int64_t n, int64_t vocab, int gather
   __shared__ int waves[2][kTokBS / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int base = 0, turn = 0;
-  for (int64_t at = 0; at < n; at += kTokBS, turn ^= 1) {
-    const int64_t i = at + threadIdx.x;
-    const int64_t id = i < n ? (int64_t)labels[i] : -1;
-    const bool counts = id >= 0 && id < vocab, takes = gather ? counts : i < n;
-    const uint64_t mask = __ballot(takes);
-    if (lane == 0) waves[turn][wave] = __popcll(mask);
+  for (int64_t at = 0; at < n; at += kTokBS * kTokEach, turn ^= 1) {
+    // of the wave's 256 rows lane l has l, l + 64, ...: whole lines, and their order by masks
+    const int64_t first = at + (int64_t)wave * 64 * kTokEach + lane;
+    int64_t id[kTokEach];
+    float ls[kTokEach], dl[kTokEach];
+    uint64_t mask[kTokEach];
+    int all_mine = 0;
+#pragma unroll
+    for (int k = 0; k < kTokEach; ++k) {
+      const int64_t i = first + 64 * k;
+      id[k] = i < n ? (int64_t)labels[i] : -1;
+      ls[k] = lse_in && i < n ? lse_in[i] : 0.0f;
+      dl[k] = dloss && i < n ? dloss[i] : 1.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < kTokEach; ++k) {
+      const bool counts = id[k] >= 0 && id[k] < vocab;
+      mask[k] = __ballot(gather ? counts : first + 64 * k < n);
+      all_mine += __popcll(mask[k]);
+    }
+    if (lane == 0) waves[turn][wave] = all_mine;
     __syncthreads();  // the other turn's entries are read by nobody any more
-    int before = 0, all = 0;
+    int before = base, all = 0;
 #pragma unroll
     for (int w = 0; w < kTokBS / 64; ++w) {
       const int c = waves[turn][w];
       before += w < wave ? c : 0;
       all += c;
     }
-    const int place = base + before + __popcll(mask & ((1ull << lane) - 1));
-    if (takes) {
-      t.label[place] = counts ? (int32_t)id : -1;
-      t.map[place] = (int32_t)i;
-      if (lse_in) {
-        t.lse[place] = lse_in[i];
-        t.coef[place] = counts ? (dloss ? scale * dloss[i] : scale) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kTokEach; ++k) {
+      const int64_t i = first + 64 * k;
+      const bool counts = id[k] >= 0 && id[k] < vocab;
+      const int place = before + __popcll(mask[k] & ((1ull << lane) - 1));
+      before += __popcll(mask[k]);
+      if (mask[k] >> lane & 1) {
+        t.label[place] = counts ? (int32_t)id[k] : -1;
+        t.map[place] = (int32_t)i;
+        if (lse_in) {
+          t.lse[place] = ls[k];
+          t.coef[place] = counts ? scale * dl[k] : 0.0f;
+        }
       }
-    }
-    if (i < n) {
-      t.inverse[i] = counts ? place : -1;
-      if (!counts && loss) loss[i] = 0.0f;
-      if (!counts && lse_out) lse_out[i] = 0.0f;
+      if (i < n) {
+        t.inverse[i] = counts ? place : -1;
+        if (!counts && loss) loss[i] = 0.0f;
+        if (!counts && lse_out) lse_out[i] = 0.0f;
+      }
     }
     base += all;
   }
@@ -322,34 +343,43 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
   tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
 }
 
-// Joins the tiles' maxima and sums: 16 tokens and 16 groups of tiles to a workgroup.
+// Joins the tiles' maxima and sums: TOKENS tokens and as many groups of tiles as
+// fit beside them to a workgroup. Sixteen tokens read whole lines; for few tokens,
+// one to a workgroup has all its tiles on their way at once.
+template <int TOKENS>
 __global__ __launch_bounds__(kThreads)
 void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, const float* __restrict__ own, Tokens tok,
                  float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float2 lds[16][17];
-  const int c = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int64_t token = (int64_t)blockIdx.x * 16 + c, count = *tok.count;
-  if ((int64_t)blockIdx.x * 16 >= count) return;  // uniform
+  constexpr int GROUPS = kThreads / TOKENS, U = 8;
+  __shared__ float2 lds[GROUPS][TOKENS + 1];
+  const int c = threadIdx.x % TOKENS, group = threadIdx.x / TOKENS;
+  const int64_t token = (int64_t)blockIdx.x * TOKENS + c, count = *tok.count;
+  if ((int64_t)blockIdx.x * TOKENS >= count) return;  // uniform
   float top = -INFINITY, sum = 0.0f;
-  auto add = [&](float2 p) {
-    const float t = fmaxf(top, p.x), from = t == -INFINITY ? 0.0f : t;
-    sum = sum * exp_of(top - from) + p.y * exp_of(p.x - from);
+  auto add = [&](const float2* p, int n) {  // n is a constant
+    float t = top;
+    for (int u = 0; u < n; ++u) t = fmaxf(t, p[u].x);
+    const float from = t == -INFINITY ? 0.0f : t;
+    sum *= exp_of(top - from);
+    for (int u = 0; u < n; ++u) sum = fmaf(p[u].y, exp_of(p[u].x - from), sum);
     top = t;
   };
   if (token < count)
-    for (int64_t t = group; t < tiles; t += 16 * 8) {
-      float2 p[8];  // on their way together
+    for (int64_t t = group; t < tiles; t += GROUPS * U) {
+      float2 p[U];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        p[u] = t + 16 * u < tiles ? parts[(t + 16 * u) * np + token] : float2{-INFINITY, 0.0f};
-#pragma unroll
-      for (int u = 0; u < 8; ++u) add(p[u]);
+      for (int u = 0; u < U; ++u)
+        p[u] = t + GROUPS * u < tiles ? parts[(t + GROUPS * u) * np + token] : float2{-INFINITY, 0.0f};
+      add(p, U);
     }
-  lds[group][c] = float2{top, sum};
-  __syncthreads();
-  if (group != 0 || token >= count) return;
+  // a tree over the groups
 #pragma unroll
-  for (int i = 1; i < 16; ++i) add(lds[i][c]);
+  for (int half = GROUPS / 2; half > 0; half /= 2) {
+    if (group >= half && group < 2 * half) lds[group][c] = float2{top, sum};
+    __syncthreads();
+    if (group < half) add(&lds[group + half][c], 1);
+  }
+  if (group != 0 || token >= count) return;
   const int64_t i = tok.map[token];
   const bool counts = tok.label[token] >= 0;
   const float log_sum = logf(sum);
@@ -687,8 +717,13 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   }
   int64_t tiles = 0;
   with_cut(cut, [&](auto shape) { tiles = (vocab + decltype(shape)::BM - 1) / decltype(shape)::BM; });
-  hipLaunchKernelGGL(k_join_loss, dim3((unsigned)((n + 15) / 16)), dim3(kThreads), 0, s, (const float2*)(ws + p.parts),
-                     tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
+  auto join = [&](auto tokens) {
+    constexpr int T = decltype(tokens)::value;
+    hipLaunchKernelGGL((k_join_loss<T>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
+                       (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
+  };
+  if (n <= 64) join(std::integral_constant<int, 1>{});
+  else join(std::integral_constant<int, 16>{});
   return hipGetLastError();
 }
 
