@@ -343,6 +343,101 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
   tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
 }
 
+// The loss of up to 16 tokens: the head's rows stream through registers once,
+// as they lie, whatever their type and alignment. A wave takes 16 rows at a time
+// as one operand of a 16 x 16 product and the tokens (the last one's copies
+// behind them) as the other; lane l loads 16 bytes of row l % 16, at piece l / 16
+// of each 64 bytes, so a wave's instruction takes 64 bytes of each row and its
+// eight a chunk of 512. bf16 products take 32 values of k, fp32 ones 4: which k
+// a lane holds does not matter as long as both operands agree. The tokens' pieces
+// come from the caches. Running maxima and sums stay with the lanes over all rows
+// of a wave.
+constexpr int kFewTokens = 16;
+constexpr int kFewWaves = 4096;  // 4 workgroups of 4 waves on each CU
+
+template <typename T>
+__global__ __launch_bounds__(kThreads, 4)
+void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h, int64_t h_ld, int n, int64_t vocab,
+                  uint32_t dim, int64_t groups, const int32_t* __restrict__ labels, float2* __restrict__ parts,
+                  float* __restrict__ own, int64_t np) {
+  constexpr int VEC = 16 / (int)sizeof(T), U = 8;  // values of a piece, pieces on their way
+  constexpr uint32_t STEP = 4 * VEC;               // values of k that a wave's instruction takes of a row
+  __shared__ float2 joined[4][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
+  const T* hr = h + (int64_t)(col < n ? col : n - 1) * h_ld;
+  const int label = col < n ? labels[col] : -1;
+  const int64_t g0 = ((int64_t)blockIdx.x * 4 + wave) * groups;
+  float top = -INFINITY, sum = 0.0f;
+  for (int64_t g = g0; g < g0 + groups && g * 16 < vocab; ++g) {
+    const int64_t row = g * 16 + col;
+    const T* wr = w + (row < vocab ? row : vocab - 1) * w_ld;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Piece<T, VEC>& a, const Piece<T, VEC>& b) {
+      if constexpr (sizeof(T) == 2) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0,
+                                                      0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.get(e), b.get(e), acc, 0, 0, 0);
+      }
+    };
+    uint32_t k = 0;
+    const uint32_t whole = dim / (U * STEP) * (U * STEP);
+    const T *wk = wr + q * VEC, *hk = hr + q * VEC;
+    Piece<T, VEC> pw[2][U], ph[U];
+    auto fetch = [&](Piece<T, VEC> (&to)[U], const T* from) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) to[u].template load<false>(from + u * STEP);
+    };
+    auto chunk = [&](int which) {
+      fetch(ph, hk + k);
+      if (k + U * STEP < whole) fetch(pw[which ^ 1], wk + k + U * STEP);
+#pragma unroll
+      for (int u = 0; u < U; ++u) multiply(pw[which][u], ph[u]);
+      k += U * STEP;
+    };
+    if (whole) fetch(pw[0], wk);
+    while (k < whole) {
+      chunk(0);
+      if (k < whole) chunk(1);
+    }
+    for (; k < dim; k += STEP) {
+      Piece<T, VEC> a, b;
+      take_cols<T, VEC>(a, wr, k + q * VEC, dim);
+      take_cols<T, VEC>(b, hr, k + q * VEC, dim);
+      multiply(a, b);
+    }
+    // lane l has rows 4 (l / 16) to 4 (l / 16) + 3 of token l % 16
+    const int64_t v = g * 16 + 4 * q;
+    float t = top;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (v + r >= vocab) acc[r] = -INFINITY;
+      else if (v + r == label) own[col] = acc[r];
+      t = fmaxf(t, acc[r]);
+    }
+    const float from = t == -INFINITY ? 0.0f : t;
+    sum *= exp_of(top - from);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum += exp_of(acc[r] - from);
+    top = t;
+  }
+  auto join = [&](float other_top, float other_sum) {
+    const float t = fmaxf(top, other_top), from = t == -INFINITY ? 0.0f : t;
+    sum = sum * exp_of(top - from) + other_sum * exp_of(other_top - from);
+    top = t;
+  };
+  const float all = join4(top, true), from = all == -INFINITY ? 0.0f : all;
+  sum = join4(sum * exp_of(top - from), false);
+  top = all;
+  if (q == 0) joined[wave][col] = float2{top, sum};
+  __syncthreads();
+  if (threadIdx.x >= (unsigned)n) return;  // of the first wave, as n is at most 16
+#pragma unroll
+  for (int i = 1; i < 4; ++i) join(joined[i][col].x, joined[i][col].y);
+  parts[(int64_t)blockIdx.x * np + col] = float2{top, sum};
+}
+
 // Joins the tiles' maxima and sums: TOKENS tokens and as many groups of tiles as
 // fit beside them to a workgroup. Sixteen tokens read whole lines; for few tokens,
 // one to a workgroup has all its tiles on their way at once.
@@ -631,7 +726,7 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
   p.splits = 1;
-  if (grad && p.pieces) {
+  if (grad && p.pieces && n > 0 && dim > 0) {
     // Of pieces of equal size and those whose head's gradient fills rounds of the widest tiles, what takes least.
     const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1,
                   wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;
@@ -672,7 +767,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.coef = take(grad ? p.np * 4 : 0);
   p.lse = take(grad ? p.np * 4 : 0);
   p.own = take(grad ? 0 : p.np * 4);
-  p.parts = take(grad ? 0 : (vocab + 127) / 128 * p.np * (int64_t)sizeof(float2));
+  const int64_t rows_of_part = n <= kFewTokens ? 64 : 128;  // of the head, at least
+  p.parts = take(grad ? 0 : (vocab + rows_of_part - 1) / rows_of_part * p.np * (int64_t)sizeof(float2));
   p.hidden = take(p.np * p.dp * p.planes * 2);
   p.weight = take(p.piece * p.dp * p.planes * 2);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
@@ -691,6 +787,27 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   const bool h_lies = as_it_lies(hidden, hidden_ld, dim, dtype), w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   const bool gather = n > kGatherTokens;
   number_tokens(labels, index_type, n, vocab, gather, nullptr, nullptr, 0.0f, tok, loss, lse, s);
+  auto join = [&](auto tokens, int64_t tiles) {
+    constexpr int T = decltype(tokens)::value;
+    hipLaunchKernelGGL((k_join_loss<T>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
+                       (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
+  };
+  if (n <= kFewTokens) {
+    const int64_t all = (vocab + 15) / 16, groups = (all + kFewWaves - 1) / kFewWaves;
+    const int64_t grid = groups ? (all + 4 * groups - 1) / (4 * groups) : 0;
+    auto go = [&](auto type) {
+      using T = decltype(type);
+      hipLaunchKernelGGL((k_logits_few<T>), dim3((unsigned)grid), dim3(kThreads), 0, s, (const T*)weight, weight_ld,
+                         (const T*)hidden, hidden_ld, (int)n, vocab, (uint32_t)dim, groups, tok.label,
+                         (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
+    };
+    if (grid > 0) {
+      if (dtype == ZS_BF16) go(uint16_t{});
+      else go(float{});
+    }
+    join(std::integral_constant<int, 1>{}, grid);
+    return hipGetLastError();
+  }
   GemmSide h{(const uint16_t*)hidden, hidden_ld, 0, n, 0};
   if (gather || !h_lies) {
     uint16_t* to = (uint16_t*)(ws + p.hidden);
@@ -717,13 +834,8 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   }
   int64_t tiles = 0;
   with_cut(cut, [&](auto shape) { tiles = (vocab + decltype(shape)::BM - 1) / decltype(shape)::BM; });
-  auto join = [&](auto tokens) {
-    constexpr int T = decltype(tokens)::value;
-    hipLaunchKernelGGL((k_join_loss<T>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
-                       (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
-  };
-  if (n <= 64) join(std::integral_constant<int, 1>{});
-  else join(std::integral_constant<int, 16>{});
+  if (n <= 64) join(std::integral_constant<int, 1>{}, tiles);
+  else join(std::integral_constant<int, 16>{}, tiles);
   return hipGetLastError();
 }
 
