@@ -4,7 +4,7 @@
 
 Each source is compiled by hipcc in parallel; the objects are linked into
 fsdp_sharded_optimizer_flatparameter_amd/libzs.so, replaced atomically. The
-standalone C-ABI test drivers (tests/c/zs_driver, zs_rows_driver) are linked
+standalone C-ABI test drivers (tests/c/zs_driver and others) are linked
 against it.
 """
 from __future__ import annotations
@@ -78,7 +78,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     return LIB
 
 
-DRIVERS = ("zs_driver", "zs_rows_driver")
+DRIVERS = ("zs_driver", "zs_rows_driver", "zs_head_driver")
 
 
 def build_driver(name: str) -> str:
