@@ -343,57 +343,95 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
   tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
 }
 
-// The loss of up to 16 tokens: the head's rows stream through registers once,
-// as they lie, whatever their type and alignment. A wave takes 16 rows at a time
-// as one operand of a 16 x 16 product and the tokens (the last one's copies
-// behind them) as the other; lane l loads 16 bytes of row l % 16, at piece l / 16
-// of each 64 bytes, so a wave's instruction takes 64 bytes of each row and its
-// eight a chunk of 512. bf16 products take 32 values of k, fp32 ones 4: which k
-// a lane holds does not matter as long as both operands agree. The tokens' pieces
-// come from the caches. Running maxima and sums stay with the lanes over all rows
-// of a wave.
-constexpr int kFewTokens = 16;
-constexpr int kFewWaves = 4096;  // 4 workgroups of 4 waves on each CU
+// The loss of few tokens: the head's rows stream through registers once, as they
+// lie, whatever their type and alignment. A wave takes 16 rows at a time as one
+// operand of 16 x 16 products and NT times 16 tokens (the last one's copies behind
+// them) as the other; lane l loads 16 bytes of row l % 16, at piece l / 16 of each
+// 64 bytes, so a wave's instruction takes 64 bytes of each row. bf16 products take
+// 32 values of k, fp32 ones 4: which k a lane holds does not matter as long as both
+// operands agree. The tokens' pieces come from the caches. Running maxima and sums
+// stay with the lanes over all rows of a wave.
+//
+// 16-byte loads at odd multiples of 2 bytes take three times as long here (4
+// tokens, 41246 rows of 1856: 30 us, and 101 with a row stride of 1857). So a
+// wave takes rows of the same parity, every second one where strides are odd,
+// leaves the first element of rows that start off the 4-byte grid to a product of
+// its own, and takes the tokens from a copy that starts one element later.
+constexpr int kFewTokens = 64;
+constexpr int kFewWaves = 4096;    // 4 workgroups of 4 waves on each CU
+// Rows that the narrow tiles take as they lie are read as fast by them (1 token, 128256 rows of 4096 bf16: 181 us,
+// 179 here; 16 tokens of 1856: 111, 125 here); what they would have to lay out first is not (4 tokens, 41246 rows of
+// 1855: 100 in all, 35 here; 64: 92, 101 here; fp32, 20 tokens of 1856: over 260, 104 here).
+constexpr int kFewAligned = 8;
 
-template <typename T>
-__global__ __launch_bounds__(kThreads, 4)
-void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h, int64_t h_ld, int n, int64_t vocab,
-                  uint32_t dim, int64_t groups, const int32_t* __restrict__ labels, float2* __restrict__ parts,
-                  float* __restrict__ own, int64_t np) {
-  constexpr int VEC = 16 / (int)sizeof(T), U = 8;  // values of a piece, pieces on their way
-  constexpr uint32_t STEP = 4 * VEC;               // values of k that a wave's instruction takes of a row
-  __shared__ float2 joined[4][16];
+template <typename T, int NT>
+__global__ __launch_bounds__(kThreads, 3)
+void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h0, const T* __restrict__ h1, int64_t h_ld,
+                  int n, int64_t vocab, uint32_t dim, int64_t groups, const int32_t* __restrict__ labels,
+                  float2* __restrict__ parts, float* __restrict__ own, int64_t np) {
+  constexpr int VEC = 16 / (int)sizeof(T), U = NT == 1 ? 8 : 4;  // values of a piece, pieces of the head on their way
+  constexpr uint32_t STEP = 4 * VEC;                             // values of k that a wave's instruction takes of a row
+  __shared__ float2 joined[4][16 * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const T* hr = h + (int64_t)(col < n ? col : n - 1) * h_ld;
-  const int label = col < n ? labels[col] : -1;
+  int label[NT];
+  int64_t token_at[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int i = t * 16 + col;
+    label[t] = i < n ? labels[i] : -1;
+    token_at[t] = (int64_t)(i < n ? i : n - 1) * h_ld;
+  }
+  const bool paired = sizeof(T) == 2 && (w_ld & 1);
   const int64_t g0 = ((int64_t)blockIdx.x * 4 + wave) * groups;
-  float top = -INFINITY, sum = 0.0f;
-  for (int64_t g = g0; g < g0 + groups && g * 16 < vocab; ++g) {
-    const int64_t row = g * 16 + col;
-    const T* wr = w + (row < vocab ? row : vocab - 1) * w_ld;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto multiply = [&](const Piece<T, VEC>& a, const Piece<T, VEC>& b) {
+  float top[NT], sum[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) top[t] = -INFINITY, sum[t] = 0.0f;
+  for (int64_t g = g0; g < g0 + groups; ++g) {
+    const int64_t first = paired ? (g >> 1) * 32 + (g & 1) : g * 16, step = paired ? 2 : 1;
+    if (first >= vocab) break;  // uniform
+    const int64_t mine = first + col * step, row = mine < vocab ? mine : first;  // rows behind the last: the first's copies
+    const bool shift = sizeof(T) == 2 && (((uint32_t)(uintptr_t)w >> 1) + (uint32_t)(first * w_ld)) & 1;  // uniform
+    const T *wr = w + row * w_ld, *h = shift ? h1 : h0;
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](int t, const Piece<T, VEC>& a, const Piece<T, VEC>& b) {
       if constexpr (sizeof(T) == 2) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0,
-                                                      0, 0);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
+                                                         acc[t], 0, 0, 0);
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.get(e), b.get(e), acc, 0, 0, 0);
+        for (int e = 0; e < VEC; ++e) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(a.get(e), b.get(e), acc[t], 0, 0, 0);
       }
     };
+    if (shift) {
+      Piece<T, VEC> a, b;
+      a.clear();
+      if (q == 0) a.put(0, ld_g(wr));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        b.clear();
+        if (q == 0) b.put(0, ld_g(h0 + token_at[t]));
+        multiply(t, a, b);
+      }
+      ++wr;
+    }
+    const uint32_t left = dim - (shift ? 1 : 0), whole = left / (U * STEP) * (U * STEP);
     uint32_t k = 0;
-    const uint32_t whole = dim / (U * STEP) * (U * STEP);
-    const T *wk = wr + q * VEC, *hk = hr + q * VEC;
-    Piece<T, VEC> pw[2][U], ph[U];
+    const T* wk = wr + q * VEC;
+    Piece<T, VEC> pw[2][U], ph[NT][U];
     auto fetch = [&](Piece<T, VEC> (&to)[U], const T* from) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) to[u].template load<false>(from + u * STEP);
+      for (int u = 0; u < U; ++u) to[u].load(from + u * STEP);
     };
     auto chunk = [&](int which) {
-      fetch(ph, hk + k);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) fetch(ph[t], h + token_at[t] + q * VEC + k);
       if (k + U * STEP < whole) fetch(pw[which ^ 1], wk + k + U * STEP);
 #pragma unroll
-      for (int u = 0; u < U; ++u) multiply(pw[which][u], ph[u]);
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(t, pw[which][u], ph[t][u]);
       k += U * STEP;
     };
     if (whole) fetch(pw[0], wk);
@@ -401,41 +439,49 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
       chunk(0);
       if (k < whole) chunk(1);
     }
-    for (; k < dim; k += STEP) {
+    for (; k < left; k += STEP) {
       Piece<T, VEC> a, b;
-      take_cols<T, VEC>(a, wr, k + q * VEC, dim);
-      take_cols<T, VEC>(b, hr, k + q * VEC, dim);
-      multiply(a, b);
-    }
-    // lane l has rows 4 (l / 16) to 4 (l / 16) + 3 of token l % 16
-    const int64_t v = g * 16 + 4 * q;
-    float t = top;
+      take_cols<T, VEC>(a, wr, k + q * VEC, left);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      if (v + r >= vocab) acc[r] = -INFINITY;
-      else if (v + r == label) own[col] = acc[r];
-      t = fmaxf(t, acc[r]);
+      for (int t = 0; t < NT; ++t) {
+        take_cols<T, VEC>(b, h + token_at[t], k + q * VEC, left);
+        multiply(t, a, b);
+      }
     }
-    const float from = t == -INFINITY ? 0.0f : t;
-    sum *= exp_of(top - from);
+    // lane l has the wave's rows 4 (l / 16) to 4 (l / 16) + 3 for token l % 16 of each tile
 #pragma unroll
-    for (int r = 0; r < 4; ++r) sum += exp_of(acc[r] - from);
-    top = t;
+    for (int t = 0; t < NT; ++t) {
+      float m = top[t];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t v = first + (4 * q + r) * step;
+        if (v >= vocab) acc[t][r] = -INFINITY;
+        else if (v == label[t]) own[t * 16 + col] = acc[t][r];
+        m = fmaxf(m, acc[t][r]);
+      }
+      const float from = m == -INFINITY ? 0.0f : m;
+      sum[t] *= exp_of(top[t] - from);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum[t] += exp_of(acc[t][r] - from);
+      top[t] = m;
+    }
   }
-  auto join = [&](float other_top, float other_sum) {
-    const float t = fmaxf(top, other_top), from = t == -INFINITY ? 0.0f : t;
-    sum = sum * exp_of(top - from) + other_sum * exp_of(other_top - from);
-    top = t;
-  };
-  const float all = join4(top, true), from = all == -INFINITY ? 0.0f : all;
-  sum = join4(sum * exp_of(top - from), false);
-  top = all;
-  if (q == 0) joined[wave][col] = float2{top, sum};
-  __syncthreads();
-  if (threadIdx.x >= (unsigned)n) return;  // of the first wave, as n is at most 16
 #pragma unroll
-  for (int i = 1; i < 4; ++i) join(joined[i][col].x, joined[i][col].y);
-  parts[(int64_t)blockIdx.x * np + col] = float2{top, sum};
+  for (int t = 0; t < NT; ++t) {
+    const float all = join4(top[t], true), from = all == -INFINITY ? 0.0f : all;
+    const float s = join4(sum[t] * exp_of(top[t] - from), false);
+    if (q == 0) joined[wave][t * 16 + col] = float2{all, s};
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    float m = joined[0][i].x, s = 0.0f;
+#pragma unroll
+    for (int x = 1; x < 4; ++x) m = fmaxf(m, joined[x][i].x);
+    const float from = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s += joined[x][i].y * exp_of(joined[x][i].x - from);
+    parts[(int64_t)blockIdx.x * np + i] = float2{m, s};
+  }
 }
 
 // Joins the tiles' maxima and sums: TOKENS tokens and as many groups of tiles as
@@ -576,29 +622,48 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
   tiles_of<S, K_IS_ROW, K_IS_ROW>(lds, tm * tn, tm, tn, make, finish);
 }
 
-// The splits' sums, rounded once, back in the tokens' places; zeros where a token does not count.
-template <typename T>
+// The splits' sums, rounded once, back in the tokens' places; zeros where a token
+// does not count. GROUPS threads share a piece of 8 columns: with few tokens there
+// are few pieces and many splits.
+template <typename T, int GROUPS>
 __global__ __launch_bounds__(kThreads)
 void k_join_dhidden(const float* __restrict__ sums, int splits, int64_t np, int64_t dq, const int32_t* __restrict__ inverse,
                     int64_t n, uint32_t dim, T* __restrict__ out, int64_t ld) {
-  const int64_t per = (dim + 7) / 8;
-  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < n * per; at += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = at / per;
+  constexpr int PIECES = kThreads / GROUPS;
+  __shared__ float lds[GROUPS > 1 ? GROUPS : 1][PIECES][9];
+  const int64_t per = (dim + 7) / 8, all = n * per;
+  const int piece = threadIdx.x % PIECES, group = threadIdx.x / PIECES;
+  for (int64_t base = (int64_t)blockIdx.x * PIECES; base < all; base += (int64_t)gridDim.x * PIECES) {
+    const int64_t at = base + piece, i = at / per;
     const uint32_t c = (uint32_t)(at % per) * 8;
-    const int32_t place = inverse[i];
+    const int32_t place = at < all ? inverse[i] : -1;
     float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (place >= 0)
-      for (int k = 0; k < splits; ++k) {
-        const float* from = sums + ((int64_t)k * np + place) * dq + c;
-        const f32x4 a = *(const f32x4*)from;
-        const f32x4 b = c + 4 < dq ? *(const f32x4*)(from + 4) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (place >= 0) {
+      const float* from = sums + (int64_t)place * dq + c;
+      const bool both = c + 4 < dq;
+#pragma unroll 4
+      for (int k = group; k < splits; k += GROUPS) {
+        const f32x4 a = *(const f32x4*)(from + (int64_t)k * np * dq);
+        const f32x4 b = both ? *(const f32x4*)(from + (int64_t)k * np * dq + 4) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] += a[e];
           v[4 + e] += b[e];
         }
       }
-    store_cols<T, 8>(out + i * ld, v, c, dim);
+    }
+    if constexpr (GROUPS > 1) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[group][piece][e] = v[e];
+      __syncthreads();
+      if (group == 0)
+        for (int x = 1; x < GROUPS; ++x)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += lds[x][piece][e];
+      __syncthreads();
+      if (group != 0) continue;
+    }
+    if (at < all) store_cols<T, 8>(out + i * ld, v, c, dim);
   }
 }
 
@@ -652,11 +717,12 @@ CutOf cut_of(int64_t m, int64_t n) {
 // What a round costs beside its stages (first loads, what is done with the products), in stages.
 constexpr double kRoundStages = 10;
 
-// Parts of the sum for the hidden states' gradient, so that its tiles fill the CUs: eight stages at least to each.
+// Parts of the sum for the hidden states' gradient, so that its tiles fill the CUs (two of the narrow ones on
+// each): eight stages at least to each.
 int splits_of(int64_t dim, int64_t n, int64_t stages) {
   const int64_t tiles = ((dim + 255) / 256) * ((n + 255) / 256);
-  const int64_t splits = least(512 / tiles, stages / 8);
-  return (int)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+  const int64_t splits = least(least(512 / tiles, n <= 64 ? 256 : 16), stages / 8);
+  return (int)(splits < 1 ? 1 : splits);
 }
 
 // As many workgroups as 256 CUs hold at once, or tiles, which they then take in turn.
@@ -767,9 +833,10 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.coef = take(grad ? p.np * 4 : 0);
   p.lse = take(grad ? p.np * 4 : 0);
   p.own = take(grad ? 0 : p.np * 4);
-  const int64_t rows_of_part = n <= kFewTokens ? 64 : 128;  // of the head, at least
-  p.parts = take(grad ? 0 : (vocab + rows_of_part - 1) / rows_of_part * p.np * (int64_t)sizeof(float2));
-  p.hidden = take(p.np * p.dp * p.planes * 2);
+  // a workgroup's rows of the head, at least; where strides are odd few tokens' may be one more
+  const int64_t parts_of = n <= kFewTokens ? vocab / 64 + 2 : (vocab + 127) / 128;
+  p.parts = take(grad ? 0 : parts_of * p.np * (int64_t)sizeof(float2));
+  p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
   p.weight = take(p.piece * p.dp * p.planes * 2);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
   p.dhidden = take(grad ? p.splits * p.np * p.dq * 4 : 0);
@@ -792,18 +859,36 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     hipLaunchKernelGGL((k_join_loss<T>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
                        (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
   };
-  if (n <= kFewTokens) {
-    const int64_t all = (vocab + 15) / 16, groups = (all + kFewWaves - 1) / kFewWaves;
+  if (n <= (w_lies ? kFewAligned : kFewTokens)) {
+    const bool bf16 = dtype == ZS_BF16, w_even = !bf16 || (weight_ld % 2 == 0 && reinterpret_cast<uintptr_t>(weight) % 4 == 0);
+    const bool h_even = !bf16 || (hidden_ld % 2 == 0 && reinterpret_cast<uintptr_t>(hidden) % 4 == 0);
+    const void *h0 = hidden, *h1 = hidden;
+    int64_t h_ld = hidden_ld;
+    if (!w_even || !h_even) {  // copies of the tokens on the grid, and from their second element on
+      uint16_t* to = (uint16_t*)(ws + p.hidden);
+      h0 = to;
+      h1 = to + p.np * p.dp;
+      h_ld = p.dp;
+      layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, nullptr, nullptr, s);
+      if (dim > 1)
+        layout((const uint16_t*)hidden + 1, hidden_ld, dtype, dim - 1, n, to + p.np * p.dp, p.dp, nullptr, nullptr, s);
+    }
+    const int64_t all = (vocab + 31) / 32 * 2, groups = (all + kFewWaves - 1) / kFewWaves;
     const int64_t grid = groups ? (all + 4 * groups - 1) / (4 * groups) : 0;
-    auto go = [&](auto type) {
+    auto go = [&](auto type, auto tiles) {
       using T = decltype(type);
-      hipLaunchKernelGGL((k_logits_few<T>), dim3((unsigned)grid), dim3(kThreads), 0, s, (const T*)weight, weight_ld,
-                         (const T*)hidden, hidden_ld, (int)n, vocab, (uint32_t)dim, groups, tok.label,
-                         (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
+      hipLaunchKernelGGL((k_logits_few<T, decltype(tiles)::value>), dim3((unsigned)grid), dim3(kThreads), 0, s,
+                         (const T*)weight, weight_ld, (const T*)h0, (const T*)h1, h_ld, (int)n, vocab, (uint32_t)dim,
+                         groups, tok.label, (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
+    };
+    auto by_tokens = [&](auto type) {
+      if (n <= 16) go(type, std::integral_constant<int, 1>{});
+      else if (n <= 32) go(type, std::integral_constant<int, 2>{});
+      else go(type, std::integral_constant<int, 4>{});
     };
     if (grid > 0) {
-      if (dtype == ZS_BF16) go(uint16_t{});
-      else go(float{});
+      if (bf16) by_tokens(uint16_t{});
+      else by_tokens(float{});
     }
     join(std::integral_constant<int, 1>{}, grid);
     return hipGetLastError();
@@ -894,13 +979,19 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
         hipLaunchKernelGGL((k_dweight<S, float>), dim3(grid), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tok.count, v0, vc, (uint32_t)dim, (float*)dweight, dweight_ld, (int)first);
     });
   }
-  const unsigned grid = grid_of(n * ((dim + 7) / 8));
-  if (dtype == ZS_BF16)
-    hipLaunchKernelGGL((k_join_dhidden<uint16_t>), dim3(grid), dim3(kThreads), 0, s, sums, p.splits, p.np, p.dq,
-                       tok.inverse, n, (uint32_t)dim, (uint16_t*)dhidden, dhidden_ld);
-  else
-    hipLaunchKernelGGL((k_join_dhidden<float>), dim3(grid), dim3(kThreads), 0, s, sums, p.splits, p.np, p.dq,
-                       tok.inverse, n, (uint32_t)dim, (float*)dhidden, dhidden_ld);
+  auto join = [&](auto type, auto groups) {
+    using T = decltype(type);
+    constexpr int GROUPS = decltype(groups)::value;
+    const unsigned grid = (unsigned)least((n * ((dim + 7) / 8) * GROUPS + kThreads - 1) / kThreads, 1 << 16);
+    hipLaunchKernelGGL((k_join_dhidden<T, GROUPS>), dim3(grid), dim3(kThreads), 0, s, sums, p.splits, p.np, p.dq,
+                       tok.inverse, n, (uint32_t)dim, (T*)dhidden, dhidden_ld);
+  };
+  auto by_splits = [&](auto type) {
+    if (p.splits > 4) join(type, std::integral_constant<int, 8>{});
+    else join(type, std::integral_constant<int, 1>{});
+  };
+  if (dtype == ZS_BF16) by_splits(uint16_t{});
+  else by_splits(float{});
   return hipGetLastError();
 }
 
