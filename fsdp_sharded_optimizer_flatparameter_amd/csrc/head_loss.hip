@@ -235,6 +235,11 @@ __device__ __forceinline__ void tiles_of(char* lds, uint32_t total, uint32_t tm,
   }
 }
 
+template <class S>
+constexpr int parts_of_tile() {  // partial maxima and sums that a tile leaves for each token
+  return S::LDS % (80 * 1024) == 0 ? S::WM : 1;
+}
+
 // Rows of the tile are rows of the head, columns tokens: a lane holds 4 TM
 // logits of each of its TN tokens. PLANES: 0 for the loss, else those of g.
 template <class S, int PLANES>
@@ -242,12 +247,22 @@ __global__ __launch_bounds__(S::THREADS, 2)
 void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Tokens tok, float2* __restrict__ parts,
               float* __restrict__ own, int64_t np, uint16_t* __restrict__ g, int64_t gp) {
   __shared__ __align__(1024) char lds[S::LDS];
-  __shared__ float2 joined[PLANES ? 1 : S::WM * S::BN];
+  constexpr int ROWS = S::BM / S::WM;  // of a wave
+  // The waves of a tile join their maxima and sums in LDS, or leave them apart where two
+  // workgroups' stages fill it.
+  constexpr int APART = parts_of_tile<S>();
+  __shared__ float2 joined[PLANES == 0 && APART == 1 ? S::WM * S::BN : 1];
+  // The lanes of a store hold 32 bytes each of 16 tokens' rows of g. By way of LDS, where
+  // there is room, they are whole lines: 335 instead of 439 us for 8192 tokens, 21760
+  // rows of 768, two planes (287 without stores). The chunk of 16 bytes c of token t lies at
+  // place c ^ t.
+  constexpr bool LINES = PLANES > 0 && APART == 1;
+  constexpr int CHUNKS = ROWS / 8;
+  __shared__ __align__(16) u32x4 lines[LINES ? S::WM * S::WN : 1][LINES ? 16 * CHUNKS : 1];
   const int64_t count = *tok.count, written = PLANES ? (count + 63) / 64 * 64 : count;
   const uint32_t tm = (uint32_t)((w.rows + S::BM - 1) / S::BM), tn = (uint32_t)((written + S::BN - 1) / S::BN);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN, q4 = (lane >> 4) * 4;
-  constexpr int ROWS = S::BM / S::WM;  // of a wave
   auto make = [&](auto& loop, const Tile& at) {
     loop.aim(w, h, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps);
   };
@@ -291,14 +306,49 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
           return z;
         });
         sum = join4(sum, false);
-        if (j == 0) __syncthreads();  // nobody reads the last tile's any more
-        if (q4 == 0) joined[wm * S::BN + col] = float2{top, sum};
+        if constexpr (APART > 1) {
+          if (q4 == 0 && live) parts[(at.m * APART + wm) * np + token] = float2{top, sum};
+        } else {
+          if (j == 0) __syncthreads();  // nobody reads the last tile's any more
+          if (q4 == 0) joined[wm * S::BN + col] = float2{top, sum};
+        }
       } else {
         const float lse = live ? tok.lse[token] : 0.0f, coef = live ? tok.coef[token] : 0.0f;
         each([&](float z, int) { return exp_of(z - lse); });
         if (hit) each([&](float p, int row) { return row == mine ? p - 1.0f : p; });
         if (whole) each([&](float p, int) { return coef * p; });
         else each([&](float p, int row) { return live && row < left ? coef * p : 0.0f; });
+        if (LINES && whole_tile) {
+          u32x4* mine_of = lines[wave];
+          const int t = lane & 15;
+#pragma unroll
+          for (int k = 0; k < PLANES; ++k) {
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i) {
+              f32x4& d = acc[i][j];
+              uint2 v;
+              if constexpr (PLANES < 3) {
+                v = uint2{pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
+                if (k + 1 < PLANES)  // what is left for the next plane
+                  d = f32x4{d.x - bf16_lo(v.x), d.y - bf16_hi(v.x), d.z - bf16_lo(v.y), d.w - bf16_hi(v.y)};
+              } else {
+                uint32_t p[4][3];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) three_planes(d[r], p[r]);
+                v = uint2{bits_hi(p[0][k], p[1][k]), bits_hi(p[2][k], p[3][k])};
+              }
+              const int place = (2 * i + (lane >> 5)) ^ (t & (CHUNKS - 1));
+              reinterpret_cast<uint2*>(mine_of + t * CHUNKS + place)[lane >> 4 & 1] = v;
+            }
+#pragma unroll
+            for (int x = 0; x < 16 * CHUNKS / 64; ++x) {
+              const int at16 = x * 64 + lane, t2 = at16 / CHUNKS, c = at16 % CHUNKS;
+              const u32x4 v = mine_of[t2 * CHUNKS + (c ^ (t2 & (CHUNKS - 1)))];
+              *(u32x4*)(g + (token - t + t2) * gp * PLANES + k * gp + first + c * 8) = v;
+            }
+          }
+          continue;
+        }
         uint16_t* row = g + token * gp * PLANES + first + q4;
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
@@ -322,7 +372,8 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
         }
       }
     }
-    if constexpr (PLANES == 0) {
+    if constexpr (PLANES == 0 && APART > 1) return false;
+    if constexpr (PLANES == 0 && APART == 1) {
       __syncthreads();
       for (int c = threadIdx.x; c < S::BN; c += S::THREADS) {
         const int64_t token = at.n * S::BN + c;
@@ -338,7 +389,7 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
       }
       return false;
     }
-    return whole_tile && S::TM * S::TN >= 16;
+    return whole_tile && (LINES ? S::TN * 16 * CHUNKS / 64 * PLANES : S::TM * S::TN) >= 16;
   };
   tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
 }
@@ -833,9 +884,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.coef = take(grad ? p.np * 4 : 0);
   p.lse = take(grad ? p.np * 4 : 0);
   p.own = take(grad ? 0 : p.np * 4);
-  // a workgroup's rows of the head, at least; where strides are odd few tokens' may be one more
-  const int64_t parts_of = n <= kFewTokens ? vocab / 64 + 2 : (vocab + 127) / 128;
-  p.parts = take(grad ? 0 : parts_of * p.np * (int64_t)sizeof(float2));
+  const int64_t parts = n <= kFewTokens ? vocab / 64 + 4 : (vocab + 127) / 128;  // 64 or 128 rows of the head each
+  p.parts = take(grad ? 0 : parts * p.np * (int64_t)sizeof(float2));
   p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
   p.weight = take(p.piece * p.dp * p.planes * 2);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
@@ -913,12 +963,15 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     with_cut(cut, [&](auto shape) {
       using S = decltype(shape);
       hipLaunchKernelGGL((k_logits<S, 0>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs,
-                         (int)(p.dp / kBK), v0, tok, (float2*)(ws + p.parts) + v0 / S::BM * p.np, (float*)(ws + p.own),
+                         (int)(p.dp / kBK), v0, tok, (float2*)(ws + p.parts) + v0 / S::BM * parts_of_tile<S>() * p.np, (float*)(ws + p.own),
                          p.np, (uint16_t*)nullptr, (int64_t)0);
     });
   }
   int64_t tiles = 0;
-  with_cut(cut, [&](auto shape) { tiles = (vocab + decltype(shape)::BM - 1) / decltype(shape)::BM; });
+  with_cut(cut, [&](auto shape) {
+    using S = decltype(shape);
+    tiles = (vocab + S::BM - 1) / S::BM * parts_of_tile<S>();
+  });
   if (n <= 64) join(std::integral_constant<int, 1>{}, tiles);
   else join(std::integral_constant<int, 16>{}, tiles);
   return hipGetLastError();
