@@ -32,7 +32,20 @@ struct RmsBackward {
   int64_t dy_ld, h_ld, scales_ld, dres_ld, dh_ld, rows;
   uint32_t dim, pitch;
   int wdtype;
+  // with one workgroup alone its sums are the gradient, and no launch joins them
+  void* alone;
+  int grad_dtype, first;
 };
+
+__device__ __forceinline__ void store_alone(const RmsBackward& a, uint32_t c, float sum) {
+  if (a.grad_dtype == ZS_BF16) {
+    uint16_t* to = (uint16_t*)a.alone + c;
+    *to = round_to<uint16_t>(a.first ? sum : sum + bf16_to_f32(*to));
+  } else {
+    float* to = (float*)a.alone + c;
+    *to = a.first ? sum : sum + *to;
+  }
+}
 
 // One lane's piece of the kept h: of type R, or codes with their block's scale.
 template <typename H, int VEC>
@@ -197,13 +210,20 @@ void k_rms_bwd(RmsBackward a) {
       float t = joined[c];
 #pragma unroll
       for (int g = 1; g < RPB; ++g) t += joined[g * COLS + c];
-      pw[c] = t;
+      if (a.alone) store_alone(a, c, t);
+      else pw[c] = t;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t c = col_of<LPR, VEC>(j, l);
-      if (c < a.pitch) store_piece<float, VEC>(pw + c, dw[j]);  // pitch is a multiple of VEC
+      if (a.alone) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (c + e < dim) store_alone(a, c + e, dw[j][e]);
+      } else if (c < a.pitch) {
+        store_piece<float, VEC>(pw + c, dw[j]);  // pitch is a multiple of VEC
+      }
     }
   }
 }
@@ -327,9 +347,9 @@ void k_rms_dw(const float* __restrict__ partials, int64_t pitch, int parts, int6
 
 constexpr int64_t kStreamBytes = 100000000;  // calls of more bytes bypass the caches, as for the layer norm
 
-// Returns the number of rows of partial sums.
+// Returns the number of rows of partial sums, or 0 where they are the gradient already.
 template <typename T, typename R, typename H, int VEC>
-int run(const RmsBackward& a, int64_t bytes, hipStream_t s) {
+int run(RmsBackward a, int64_t bytes, hipStream_t s) {
   const int64_t nvec = ((int64_t)a.dim + VEC - 1) / VEC;
   const bool nt = bytes > kStreamBytes;
   int parts = (int)(a.rows < kMaxParts ? a.rows : kMaxParts);
@@ -338,8 +358,11 @@ int run(const RmsBackward& a, int64_t bytes, hipStream_t s) {
     const int64_t need = (a.rows + BS / LPR - 1) / (BS / LPR);
     const int64_t want = LPR >= 512 && need >= 64 ? (need + 1) / 2 : need;
     parts = (int)(want < kMaxParts ? want : kMaxParts);
-    if (nt) hipLaunchKernelGGL((k_rms_bwd<T, R, H, LPR, NV, VEC, true>), dim3((unsigned)parts), dim3(BS), 0, s, a);
-    else hipLaunchKernelGGL((k_rms_bwd<T, R, H, LPR, NV, VEC, false>), dim3((unsigned)parts), dim3(BS), 0, s, a);
+    if (parts > 1) a.alone = nullptr;
+    else if (a.alone) parts = 0;
+    const dim3 grid((unsigned)(parts > 0 ? parts : 1));
+    if (nt) hipLaunchKernelGGL((k_rms_bwd<T, R, H, LPR, NV, VEC, true>), grid, dim3(BS), 0, s, a);
+    else hipLaunchKernelGGL((k_rms_bwd<T, R, H, LPR, NV, VEC, false>), grid, dim3(BS), 0, s, a);
   };
   using std::integral_constant;
   if (nvec <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
@@ -380,7 +403,7 @@ hipError_t launch_rms_norm_backward(const void* dy, int dtype, int64_t dy_ld, co
   float* partials = dw ? static_cast<float*>(workspace) : nullptr;
   if (rows > 0) {
     const RmsBackward a{dy, h, w, dres, scales, rstd, dh, partials, dy_ld, h_ld, scales_ld, dres_ld, dh_ld, rows,
-                        (uint32_t)dim, (uint32_t)p.pitch, wdtype};
+                        (uint32_t)dim, (uint32_t)p.pitch, wdtype, dw, grad_dtype, (int)first};
     const int64_t t = dtype == ZS_BF16 ? 2 : 4, r = dh_dtype == ZS_BF16 ? 2 : 4, k = h_dtype == ZS_E4M3 ? 1 : r;
     const int64_t bytes = rows * dim * (t + k + r * (dres ? 2 : 1));
     const bool kept8 = h_dtype == ZS_E4M3;
@@ -390,7 +413,7 @@ hipError_t launch_rms_norm_backward(const void* dy, int dtype, int64_t dy_ld, co
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dw && (rows > 0 || first)) {  // without rows the sum is zero
+  if (dw && (parts > 0 || (rows == 0 && first))) {  // without rows the sum is zero
     const dim3 gd((unsigned)((dim + 63) / 64)), bd(kJoinWaves * 64);
     if (grad_dtype == ZS_BF16) hipLaunchKernelGGL((k_rms_dw<uint16_t>), gd, bd, 0, s, partials, p.pitch, parts, dim, (uint16_t*)dw, (int)first);
     else hipLaunchKernelGGL((k_rms_dw<float>), gd, bd, 0, s, partials, p.pitch, parts, dim, (float*)dw, (int)first);
