@@ -20,9 +20,9 @@
 //
 // Rounding: bf16 products are exact and added in fp32. g is rounded to bf16 for
 // gradients in bf16, which are rounded as much themselves; for an fp32
-// gradient of a bf16 head it is a sum of two bf16 (17 bits), and all three
-// operands of an fp32 head are sums of three (24 bits), whose products below
-// 2^-24 of the largest are left out.
+// gradient of a bf16 head it is a sum of three bf16 (24 bits) or, for many
+// tokens, of two (17 bits), and all three operands of an fp32 head are sums of
+// three, whose products below 2^-21 of the largest are left out.
 #include <type_traits>
 
 #include "zs_gemm.hpp"
@@ -39,6 +39,7 @@ using Narrow = GemmShape<256, 64, 4, 1>;  // at most 64 tokens: the head's rows 
 
 constexpr Segments kOne{1, 0, 0};
 constexpr Segments kTwo{2, 0x00, 0x10};             // one plane times two
+constexpr Segments kOneThree{3, 0x000, 0x210};      // one plane times three
 constexpr Segments kThree{3, 0x100, 0x010};         // 2 x 2 planes without the last
 constexpr Segments kSix{6, 0x201100, 0x021010};     // 3 x 3 planes, those above 2^-24
 
@@ -52,6 +53,17 @@ struct Tokens {
 };
 
 // ---------------------------------------------------------------- tokens
+
+// Labels as the caller gives them: -1 for those outside of the vocabulary.
+struct Labels {
+  const void* p;
+  int wide;  // int64, else int32
+  int64_t vocab;
+  __device__ __forceinline__ int at(int64_t i) const {
+    const int64_t id = wide ? ((const int64_t*)p)[i] : (int64_t)((const int32_t*)p)[i];
+    return id >= 0 && id < vocab ? (int)id : -1;
+  }
+};
 
 constexpr int kTokBS = 1024;
 constexpr int kTokEach = 4;
@@ -326,17 +338,9 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
 #pragma unroll
             for (int i = 0; i < S::TM; ++i) {
               f32x4& d = acc[i][j];
-              uint2 v;
-              if constexpr (PLANES < 3) {
-                v = uint2{pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
-                if (k + 1 < PLANES)  // what is left for the next plane
-                  d = f32x4{d.x - bf16_lo(v.x), d.y - bf16_hi(v.x), d.z - bf16_lo(v.y), d.w - bf16_hi(v.y)};
-              } else {
-                uint32_t p[4][3];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) three_planes(d[r], p[r]);
-                v = uint2{bits_hi(p[0][k], p[1][k]), bits_hi(p[2][k], p[3][k])};
-              }
+              const uint2 v = uint2{pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
+              if (k + 1 < PLANES)  // what is left for the next plane
+                d = f32x4{d.x - bf16_lo(v.x), d.y - bf16_hi(v.x), d.z - bf16_lo(v.y), d.w - bf16_hi(v.y)};
               const int place = (2 * i + (lane >> 5)) ^ (t & (CHUNKS - 1));
               reinterpret_cast<uint2*>(mine_of + t * CHUNKS + place)[lane >> 4 & 1] = v;
             }
@@ -353,21 +357,12 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) {
           if (!whole_tile && (token >= written || first + 16 * i >= gp)) continue;
-          const f32x4 d = acc[i][j];
-          uint16_t* to = row + 16 * i;
-          if constexpr (PLANES < 3) {
-            const uint32_t hi[2] = {pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
-            *(uint2*)to = uint2{hi[0], hi[1]};
-            if constexpr (PLANES == 2)
-              *(uint2*)(to + gp) = uint2{pack_bf16(d.x - bf16_lo(hi[0]), d.y - bf16_hi(hi[0])),
-                                         pack_bf16(d.z - bf16_lo(hi[1]), d.w - bf16_hi(hi[1]))};
-          } else {
-            uint32_t p[4][3];
+          f32x4 d = acc[i][j];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) three_planes(d[r], p[r]);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              *(uint2*)(to + k * gp) = uint2{bits_hi(p[0][k], p[1][k]), bits_hi(p[2][k], p[3][k])};
+          for (int k = 0; k < PLANES; ++k) {
+            const uint2 v = uint2{pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
+            *(uint2*)(row + 16 * i + k * gp) = v;
+            d = f32x4{d.x - bf16_lo(v.x), d.y - bf16_hi(v.x), d.z - bf16_lo(v.y), d.w - bf16_hi(v.y)};
           }
         }
       }
@@ -418,8 +413,7 @@ constexpr int kFewAligned = 8;
 template <typename T, int NT>
 __global__ __launch_bounds__(kThreads, 3)
 void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h0, const T* __restrict__ h1, int64_t h_ld,
-                  int n, int64_t vocab, uint32_t dim, int64_t groups, const int32_t* __restrict__ labels,
-                  float2* __restrict__ parts, float* __restrict__ own, int64_t np) {
+                  int n, int64_t vocab, uint32_t dim, int64_t groups, Labels labels, float2* __restrict__ parts, float* __restrict__ own, int64_t np) {
   constexpr int VEC = 16 / (int)sizeof(T), U = NT == 1 ? 8 : 4;  // values of a piece, pieces of the head on their way
   constexpr uint32_t STEP = 4 * VEC;                             // values of k that a wave's instruction takes of a row
   __shared__ float2 joined[4][16 * NT];
@@ -429,7 +423,7 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int i = t * 16 + col;
-    label[t] = i < n ? labels[i] : -1;
+    label[t] = i < n ? labels.at(i) : -1;
     token_at[t] = (int64_t)(i < n ? i : n - 1) * h_ld;
   }
   const bool paired = sizeof(T) == 2 && (w_ld & 1);
@@ -538,14 +532,16 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
 // Joins the tiles' maxima and sums: TOKENS tokens and as many groups of tiles as
 // fit beside them to a workgroup. Sixteen tokens read whole lines; for few tokens,
 // one to a workgroup has all its tiles on their way at once.
-template <int TOKENS>
+//
+// PLACED: tokens are where k_tokens put them; otherwise each is in its row.
+template <int TOKENS, bool PLACED>
 __global__ __launch_bounds__(kThreads)
 void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, const float* __restrict__ own, Tokens tok,
-                 float* __restrict__ loss, float* __restrict__ lse) {
+                 Labels labels, int64_t n, float* __restrict__ loss, float* __restrict__ lse) {
   constexpr int GROUPS = kThreads / TOKENS, U = 8;
   __shared__ float2 lds[GROUPS][TOKENS + 1];
   const int c = threadIdx.x % TOKENS, group = threadIdx.x / TOKENS;
-  const int64_t token = (int64_t)blockIdx.x * TOKENS + c, count = *tok.count;
+  const int64_t token = (int64_t)blockIdx.x * TOKENS + c, count = PLACED ? *tok.count : n;
   if ((int64_t)blockIdx.x * TOKENS >= count) return;  // uniform
   float top = -INFINITY, sum = 0.0f;
   auto add = [&](const float2* p, int n) {  // n is a constant
@@ -572,8 +568,8 @@ void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, co
     if (group < half) add(&lds[group + half][c], 1);
   }
   if (group != 0 || token >= count) return;
-  const int64_t i = tok.map[token];
-  const bool counts = tok.label[token] >= 0;
+  const int64_t i = PLACED ? tok.map[token] : token;
+  const bool counts = (PLACED ? tok.label[token] : labels.at(token)) >= 0;
   const float log_sum = logf(sum);
   loss[i] = counts ? log_sum + (top - own[token]) : 0.0f;  // exact where the label's logit is the largest
   if (lse) lse[i] = counts ? top + log_sum : 0.0f;
@@ -824,6 +820,10 @@ void zero_rows(void* p, int dtype, int64_t ld, int64_t rows, int64_t dim, hipStr
 constexpr int64_t kLayoutBytes = 1 << 28;
 constexpr int64_t kGradBytes = 1 << 30;
 constexpr int64_t kMostPiece = 1 << 20;
+// For an fp32 gradient of a bf16 head g has 24 bits, or 17 where this many tokens are added: rounding g to 17 bits is
+// off by 2^-19 of it on average, about what the fp32 sum of 4096 products is by itself, and a third of the products
+// for dw and of g's bytes are saved (8192 tokens, 50257 x 768: 2.9 ms, 3.6 with 24 bits).
+constexpr int64_t kLongSum = 4096;
 // Calls of fewer tokens keep every row where it is in the forward pass.
 constexpr int64_t kGatherTokens = 256;
 
@@ -833,7 +833,7 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   HeadPlan p{};
   const bool grad = grad_dtype >= 0;
   p.planes = dtype == ZS_F32 ? 3 : 1;
-  p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? 2 : 1;
+  p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? (n < kLongSum ? 3 : 2) : 1;
   p.np = up(n, 64);
   p.dp = up(dim, 64);
   p.dq = up(dim, 4);
@@ -902,12 +902,11 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   const Tokens tok = tokens_at(p, workspace);
   const Segments segs = p.planes == 3 ? kSix : kOne;
   const bool h_lies = as_it_lies(hidden, hidden_ld, dim, dtype), w_lies = as_it_lies(weight, weight_ld, dim, dtype);
-  const bool gather = n > kGatherTokens;
-  number_tokens(labels, index_type, n, vocab, gather, nullptr, nullptr, 0.0f, tok, loss, lse, s);
-  auto join = [&](auto tokens, int64_t tiles) {
+  const Labels given{labels, index_type == ZS_I64, vocab};
+  auto join = [&](auto tokens, auto placed, int64_t tiles) {
     constexpr int T = decltype(tokens)::value;
-    hipLaunchKernelGGL((k_join_loss<T>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
-                       (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, loss, lse);
+    hipLaunchKernelGGL((k_join_loss<T, decltype(placed)::value>), dim3((unsigned)((n + T - 1) / T)), dim3(kThreads), 0, s,
+                       (const float2*)(ws + p.parts), tiles, p.np, (const float*)(ws + p.own), tok, given, n, loss, lse);
   };
   if (n <= (w_lies ? kFewAligned : kFewTokens)) {
     const bool bf16 = dtype == ZS_BF16, w_even = !bf16 || (weight_ld % 2 == 0 && reinterpret_cast<uintptr_t>(weight) % 4 == 0);
@@ -929,7 +928,7 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
       using T = decltype(type);
       hipLaunchKernelGGL((k_logits_few<T, decltype(tiles)::value>), dim3((unsigned)grid), dim3(kThreads), 0, s,
                          (const T*)weight, weight_ld, (const T*)h0, (const T*)h1, h_ld, (int)n, vocab, (uint32_t)dim,
-                         groups, tok.label, (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
+                         groups, given, (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
     };
     auto by_tokens = [&](auto type) {
       if (n <= 16) go(type, std::integral_constant<int, 1>{});
@@ -940,9 +939,11 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
       if (bf16) by_tokens(uint16_t{});
       else by_tokens(float{});
     }
-    join(std::integral_constant<int, 1>{}, grid);
+    join(std::integral_constant<int, 1>{}, std::false_type{}, grid);
     return hipGetLastError();
   }
+  const bool gather = n > kGatherTokens;
+  number_tokens(labels, index_type, n, vocab, gather, nullptr, nullptr, 0.0f, tok, loss, lse, s);
   GemmSide h{(const uint16_t*)hidden, hidden_ld, 0, n, 0};
   if (gather || !h_lies) {
     uint16_t* to = (uint16_t*)(ws + p.hidden);
@@ -972,8 +973,8 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     using S = decltype(shape);
     tiles = (vocab + S::BM - 1) / S::BM * parts_of_tile<S>();
   });
-  if (n <= 64) join(std::integral_constant<int, 1>{}, tiles);
-  else join(std::integral_constant<int, 16>{}, tiles);
+  if (n <= 64) join(std::integral_constant<int, 1>{}, std::true_type{}, tiles);
+  else join(std::integral_constant<int, 16>{}, std::true_type{}, tiles);
   return hipGetLastError();
 }
 
@@ -991,7 +992,10 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
   char* ws = static_cast<char*>(workspace);
   const Tokens tok = tokens_at(p, workspace);
   const Segments segs = p.planes == 3 ? kSix : kOne;
-  const Segments wsegs = p.planes == 3 ? (grad_dtype == ZS_F32 ? kSix : kThree) : p.gplanes == 2 ? kTwo : kOne;
+  const Segments wsegs = p.planes == 3      ? (grad_dtype == ZS_F32 ? kSix : kThree)
+                         : p.gplanes == 3 ? kOneThree
+                         : p.gplanes == 2 ? kTwo
+                                          : kOne;
   const bool w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   uint16_t *hp = (uint16_t*)(ws + p.hidden), *gp = (uint16_t*)(ws + p.g);
   float* sums = (float*)(ws + p.dhidden);

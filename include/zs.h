@@ -762,8 +762,9 @@ zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld,
  *                      grad_dtype) bytes on a 16-byte boundary; calls and graph
  *                      replays that may run at the same time need one each
  * The logits are made again, a piece of the vocabulary at a time. g is rounded to
- * bf16 for the gradients that are stored in bf16 from bf16 inputs, to 16 bits or
- * more for the others; sums are fp32, in an order that depends on the sizes and
+ * bf16 for the gradients that are stored in bf16 from bf16 inputs; for the others
+ * it has 24 bits, or 17 for an fp32 dweight of bf16 inputs and 4096 tokens or more,
+ * whose sum is off by as much; sums are fp32, in an order that depends on the sizes and
  * on how many tokens count alone. n == 0 with first != 0 sets dweight to zero.
  * Limits, overlaps and errors as above, and ZS_ERR_HPARAM.
  */
