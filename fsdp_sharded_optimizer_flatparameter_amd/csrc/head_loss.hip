@@ -25,6 +25,7 @@
 // three, whose products below 2^-21 of the largest are left out.
 #include <type_traits>
 
+#include "zs_e4m3.hpp"
 #include "zs_gemm.hpp"
 #include "zs_launch.hpp"
 #include "zs_launch_head.hpp"
@@ -43,6 +44,7 @@ constexpr Segments kTwo{2, 0x00, 0x01};           // one plane times two
 constexpr Segments kOneThree{3, 0x000, 0x012};    // one plane times three
 constexpr Segments kThree{3, 0x010, 0x001};       // 2 x 2 planes without the last
 constexpr Segments kSix{6, 0x010120, 0x001102};   // 3 x 3 planes, those above 2^-21
+constexpr Segments kHalves{3, 0x021, 0x012};      // fp16 planes hi, hi 2^-11, lo 2^11
 
 // What is kept of each token that counts, in the order in which they are moved
 // together: its label (-1: none), the gradient of its loss, its log sum of
@@ -183,6 +185,59 @@ void k_layout(const T* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows,
   }
 }
 
+// fp32 rows for the loss alone, as fp16: with 2^k the power of two that brings the
+// row's largest finite magnitude to [2^14, 2^15), x 2^k = hi + lo, of 11 bits each, lie
+// as planes hi, hi 2^-11 and lo 2^11 (so that lo is rarely subnormal), of `dp` elements.
+// hi hi' + (hi 2^-11)(lo' 2^11) + (lo 2^11)(hi' 2^-11) is the product of two rows
+// within 3 2^-22 |x x'|, where hi 2^-11 is subnormal within 2^-39 of the one's |x| by
+// the other's largest, in three products instead of bf16's six. power takes -k.
+// Infinities lie in hi alone, so that they meet each value once. A wave takes a row,
+// and reads it twice.
+__global__ __launch_bounds__(kThreads)
+void k_layout_half(const float* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows, uint16_t* __restrict__ dst,
+                   int64_t dp, int32_t* __restrict__ power, const int32_t* __restrict__ map, const int32_t* __restrict__ count) {
+  const int lane = threadIdx.x & 63;
+  const int64_t live = count ? *count : rows;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < live; r += (int64_t)gridDim.x * 4) {
+    const float* from = src + (map ? (int64_t)map[r] : r) * ld;
+    float top = 0.0f;
+    for (uint32_t c = lane * 8; c < dim; c += 64 * 8) {
+      Piece<float, 8> p;
+      take_cols<float, 8>(p, from, c, dim);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = fabsf(p.get(e));
+        top = x < INFINITY ? fmaxf(top, x) : top;
+      }
+    }
+    top = lane_max<32>(top);
+    const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+    top = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+    const int k = top == 0.0f ? 0 : 14 - e > 126 ? 126 : 14 - e;
+    const float s = __uint_as_float((uint32_t)(127 + k) << 23);
+    if (lane == 0) power[r] = -k;
+    for (uint32_t c = lane * 8; c < dp; c += 64 * 8) {
+      Piece<float, 8> p;
+      p.clear();
+      take_cols<float, 8>(p, from, c, dim);
+      f16x8 hi, low, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = p.get(i) * s;
+        hi[i] = (_Float16)x;
+        const bool finite = fabsf(x) < INFINITY;
+        low[i] = finite ? (_Float16)((float)hi[i] * 0x1p-11f) : (_Float16)0.0f;
+        lo[i] = finite ? (_Float16)((x - (float)hi[i]) * 0x1p11f) : (_Float16)0.0f;
+      }
+      uint16_t* to = dst + r * dp * 3 + c;
+      *(f16x8*)to = hi;
+      *(f16x8*)(to + dp) = low;
+      *(f16x8*)(to + 2 * dp) = lo;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- products
 
 // Which tile a workgroup takes. Workgroups go round robin over the 8 XCDs, each
@@ -223,9 +278,9 @@ __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f
 // The tiles of one workgroup, one after another: make(at) aims the loop at a tile,
 // finish(at) uses its products and says whether all lanes have sent off at least
 // kStored stores.
-template <class S, GemmMode MA, GemmMode MB, typename Make, typename Finish>
+template <class S, GemmMode MA, GemmMode MB, bool HALF = false, typename Make, typename Finish>
 __device__ __forceinline__ void tiles_of(char* lds, uint32_t total, uint32_t tm, uint32_t tn, Make&& make, Finish&& finish) {
-  TileLoop<S, MA, MB> loop;
+  TileLoop<S, MA, MB, HALF> loop;
   uint32_t id = blockIdx.x;
   if (id >= total) return;  // uniform
   Tile at = tile_of(id, total, tm, tn);
@@ -254,11 +309,13 @@ constexpr int parts_of_tile() {  // partial maxima and sums that a tile leaves f
 }
 
 // Rows of the tile are rows of the head, columns tokens: a lane holds 4 TM
-// logits of each of its TN tokens. PLANES: 0 for the loss, else those of g.
-template <class S, int PLANES>
+// logits of each of its TN tokens. PLANES: 0 for the loss, else those of g. HALF:
+// the operands are k_layout_half's.
+template <class S, int PLANES, bool HALF = false>
 __global__ __launch_bounds__(S::THREADS, 2)
 void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Tokens tok, float2* __restrict__ parts,
-              float* __restrict__ own, int64_t np, uint16_t* __restrict__ g, int64_t gp) {
+              float* __restrict__ own, int64_t np, uint16_t* __restrict__ g, int64_t gp, const int32_t* __restrict__ w_power,
+              const int32_t* __restrict__ h_power) {
   __shared__ __align__(1024) char lds[S::LDS];
   constexpr int ROWS = S::BM / S::WM;  // of a wave
   // The waves of a tile join their maxima and sums in LDS, or leave them apart where two
@@ -299,6 +356,17 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = f(acc[i][j][r], 16 * i + r);
       };
+      if constexpr (HALF) {
+        const int of_token = live ? h_power[token] : 0;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) {
+          const int4 of_row = *(const int4*)(w_power + first + q4 + 16 * i);  // whole tiles have a place
+          acc[i][j][0] = ldexpf(acc[i][j][0], of_row.x + of_token);
+          acc[i][j][1] = ldexpf(acc[i][j][1], of_row.y + of_token);
+          acc[i][j][2] = ldexpf(acc[i][j][2], of_row.z + of_token);
+          acc[i][j][3] = ldexpf(acc[i][j][3], of_row.w + of_token);
+        }
+      }
       if constexpr (PLANES == 0) {
         if (!whole) each([&](float z, int row) { return row < left ? z : -INFINITY; });
         if (hit)
@@ -392,7 +460,7 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
     }
     return whole_tile && (LINES ? S::TN * 16 * CHUNKS / 64 * PLANES : S::TM * S::TN) >= 16;
   };
-  tiles_of<S, K_IN_ROWS, K_IN_ROWS>(lds, tm * tn, tm, tn, make, finish);
+  tiles_of<S, K_IN_ROWS, K_IN_ROWS, HALF>(lds, tm * tn, tm, tn, make, finish);
 }
 
 // The loss of few tokens: the head's rows stream through registers once, as they
@@ -908,6 +976,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.parts = take(grad ? 0 : parts * p.np * (int64_t)sizeof(float2));
   p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
   p.weight = take(p.piece * p.dp * p.planes * 2);
+  p.hpower = take(grad || dtype != ZS_F32 ? 0 : p.np * 4);
+  p.wpower = take(grad || dtype != ZS_F32 ? 0 : p.piece * 4);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
   p.dhidden = take(grad ? p.splits * p.np * p.dq * 4 : 0);
   p.bytes = at;
@@ -920,7 +990,15 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   const HeadPlan p = head_plan(n, vocab, dim, dtype, -1);
   char* ws = static_cast<char*>(workspace);
   const Tokens tok = tokens_at(p, workspace);
-  const Segments segs = p.planes == 3 ? kSix : kOne;
+  const bool half = dtype == ZS_F32;
+  const Segments segs = half ? kHalves : kOne;
+  int32_t *h_power = (int32_t*)(ws + p.hpower), *w_power = (int32_t*)(ws + p.wpower);
+  auto layout_half = [&](const void* src, int64_t ld, int64_t rows, uint16_t* to, int32_t* power, const int32_t* map,
+                         const int32_t* count) {
+    const unsigned grid = (unsigned)least((rows + 3) / 4, 4096);
+    hipLaunchKernelGGL(k_layout_half, dim3(grid), dim3(kThreads), 0, s, (const float*)src, ld, (uint32_t)dim, rows, to,
+                       p.dp, power, map, count);
+  };
   const bool h_lies = as_it_lies(hidden, hidden_ld, dim, dtype), w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   const Labels given{labels, index_type == ZS_I64, vocab};
   auto join = [&](auto tokens, auto placed, int64_t tiles) {
@@ -967,7 +1045,8 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   GemmSide h{(const uint16_t*)hidden, hidden_ld, 0, n, 0};
   if (gather || !h_lies) {
     uint16_t* to = (uint16_t*)(ws + p.hidden);
-    layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
+    if (half) layout_half(hidden, hidden_ld, n, to, h_power, tok.map, tok.count);
+    else layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
     h = GemmSide{to, p.dp * p.planes, p.dp, p.np, 0};
   }
   const Cut cut = cut_of(vocab, n).cut;
@@ -977,15 +1056,22 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, 0};
     if (!w_lies) {
       uint16_t* to = (uint16_t*)(ws + p.weight);
-      const int64_t size = dtype == ZS_F32 ? 4 : 2;
-      layout((const char*)weight + v0 * weight_ld * size, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
+      const char* from = (const char*)weight + v0 * weight_ld * (half ? 4 : 2);
+      if (half) layout_half(from, weight_ld, vc, to, w_power, nullptr, nullptr);
+      else layout(from, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
       w = GemmSide{to, p.dp * p.planes, p.dp, vc, 0};
     }
     with_cut(cut, [&](auto shape) {
       using S = decltype(shape);
-      hipLaunchKernelGGL((k_logits<S, 0>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs,
-                         (int)(p.dp / kBK), v0, tok, (float2*)(ws + p.parts) + v0 / S::BM * parts_of_tile<S>() * p.np, (float*)(ws + p.own),
-                         p.np, (uint16_t*)nullptr, (int64_t)0);
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), v0,
+                           tok, (float2*)(ws + p.parts) + v0 / S::BM * parts_of_tile<S>() * p.np, (float*)(ws + p.own),
+                           p.np, (uint16_t*)nullptr, (int64_t)0, w_power, h_power);
+      };
+      if constexpr (!std::is_same_v<S, Narrow>) {  // of fp32 few tokens took the head as it lies
+        if (half) return go(k_logits<S, 0, true>);
+      }
+      go(k_logits<S, 0>);
     });
   }
   int64_t tiles = 0;
@@ -1036,7 +1122,8 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
       using S = decltype(shape);
       auto go = [&](auto planes) {
         hipLaunchKernelGGL((k_logits<S, decltype(planes)::value>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w,
-                           h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp);
+                           h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, (const int32_t*)nullptr,
+                           (const int32_t*)nullptr);
       };
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
       else if (p.gplanes == 2) go(std::integral_constant<int, 2>{});

@@ -20,6 +20,7 @@ namespace zs {
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 enum GemmMode { K_IN_ROWS, K_IS_ROW };
 
@@ -196,7 +197,7 @@ __device__ __forceinline__ void barrier() {
 // turn), of the 1490 that the same loop reaches without loads. Stages of 32
 // values, four or five in LDS: 1130; loads sent off a few with each step: 1210 to
 // 1260; 32 x 32 x 16 products: 1190; of zeros, at the full clock: 1370.
-template <class S, GemmMode MA, GemmMode MB>
+template <class S, GemmMode MA, GemmMode MB, bool HALF = false>  // HALF: the operands are fp16
 struct TileLoop {
 #ifdef __HIP_DEVICE_COMPILE__
   static constexpr int A_BYTES = S::BM * kBK * 2;
@@ -261,8 +262,13 @@ struct TileLoop {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j)
-          acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u & 1][x], fb[kk][j], acc[i + x][j], 0, 0, 0);
+        for (int j = 0; j < S::TN; ++j) {
+          if constexpr (HALF)
+            acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, fa[u & 1][x]),
+                                                                   __builtin_bit_cast(f16x8, fb[kk][j]), acc[i + x][j], 0, 0, 0);
+          else
+            acc[i + x][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[u & 1][x], fb[kk][j], acc[i + x][j], 0, 0, 0);
+        }
     };
     if (n == 1) wait_reads_and_loads_but<0>();
     else if (stored) wait_reads_and_loads_but<NA + NB + kStored>();

@@ -727,9 +727,11 @@ size_t zs_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t
  *                      zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype, -1)
  *                      bytes on a 16-byte boundary; calls and graph replays that
  *                      may run at the same time need one each
- * Products of bf16 values are exact and added in fp32; fp32 values enter as sums
- * of three bf16, with an error of the size of fp32 products' roundings. Infinite
- * or NaN logits make their token's loss infinite or NaN, and no other's. dim at
+ * Products of bf16 values are exact and added in fp32. fp32 values enter as they
+ * are for up to 64 tokens, as sums of two fp16 scaled by a power of two of their row
+ * for more: a product h w is off by up to 2^-20 |h w|, or 2^-39 of one's magnitude by
+ * the largest of the other's row. Infinite or NaN logits make their token's loss
+ * infinite or NaN, and no other's; one of minus infinity counts as 0. dim at
  * most 2^20, and at most 2^31 - 1 tiles of 128 rows of the head by 128 tokens.
  * Weights that lie on 16-byte boundaries with a multiple of 64 columns are read
  * as they lie; others are laid out in the workspace first. No output or workspace
@@ -761,7 +763,9 @@ zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld,
  *                      zs_linear_cross_entropy_workspace_bytes(n, vocab, dim, dtype,
  *                      grad_dtype) bytes on a 16-byte boundary; calls and graph
  *                      replays that may run at the same time need one each
- * The logits are made again, a piece of the vocabulary at a time. g is rounded to
+ * The logits are made again, a piece of the vocabulary at a time, of fp32 values as
+ * sums of three bf16, with an error of the size of fp32 products' roundings. An
+ * infinite value makes the gradients that it reaches NaN. g is rounded to
  * bf16 for the gradients that are stored in bf16 from bf16 inputs; for the others
  * it has 24 bits, or 17 for an fp32 dweight of bf16 inputs and 4096 tokens or more,
  * whose sum is off by as much; sums are fp32, in an order that depends on the sizes and

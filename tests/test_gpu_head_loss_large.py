@@ -262,3 +262,46 @@ def test_graph_and_streams(n, vocab, dim, dtype):
         for a, b in zip(captured, eager):
             assert torch.equal(bits(a), bits(b))
     check_forward(h, w, t, captured[0], captured[1])
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(65, 301, 97), (300, 1000, 200)])
+def test_fp32_rows_of_any_magnitude(n, vocab, dim):
+    """Rows scaled from 2^-100 to 2^100, their columns over 12 decades, zero rows, an infinite one."""
+    rng = np.random.default_rng(n)
+    up = rng.integers(-100, 101, n)
+    h = rng.standard_normal((n, dim)) * 10.0 ** rng.uniform(-6, 6, dim)
+    h = np.ldexp(h / np.abs(h).max(1)[:, None], up[:, None])
+    w = rng.standard_normal((vocab, dim)) * 10.0 ** rng.uniform(-6, 6, dim)
+    w /= np.abs(w).max(1)[:, None]
+    h, w = h.astype(np.float32), w.astype(np.float32)
+    h[7], w[9] = 0.0, 0.0
+    h[8] = np.float32(2.0 ** -140)  # subnormal throughout
+    keep = up <= 3                  # of larger rows the logits' own size leaves no digits to compare
+    keep[[7, 8]] = True
+    t = rng.integers(0, vocab, n)
+    loss, lse = forward(torch.from_numpy(h).cuda(), torch.from_numpy(w).cuda(), torch.from_numpy(t).cuda(), "f32")
+    h, w = h.astype(np.float64), w.astype(np.float64)
+    want_loss, want_lse = oh.loss_forward(h, w, t)
+    a, b = np.abs(h), np.abs(w)
+    # each product within 3 2^-22 of itself and 2^-39 of |h| max|w| and |w| max|h|; sums of 32 products round twice a product at most
+    e = (3 * 2.0 ** -22 + 2 * (32 + 3 * dim / 32) * U) * (a @ b.T)
+    e += 2.0 ** -39 * (a.sum(1)[:, None] * b.max(1) + a.max(1)[:, None] * b.sum(1))
+    z = h @ w.T
+    top = z.max(1)
+    rest = 2 * ((top - z.min(1)) + 4) * 2.0 ** -23 + (128 + vocab / 1024) * U + 4 * U * (np.abs(top) + np.log(vocab))
+    assert np.isfinite(f64(loss)).all()
+    assert (np.abs(f64(lse) - want_lse) <= e.max(1) + rest)[keep].all()
+    assert (np.abs(f64(loss) - want_loss) <= 2 * e.max(1) + rest)[keep].all()
+
+
+def test_fp32_rows_of_minus_infinity():
+    g = gen(3)
+    w, h = matrix(g, 700, 100, "f32", 0, 0.3)[1], matrix(g, 300, 100, "f32")[1].abs()
+    t = labels_of(g, 300, 700, torch.int64, 0.0)
+    t[t == 3] = 4
+    w[3] = float("-inf")
+    w[3, 50:] = -1e38
+    loss, _ = forward(h, w, t, "f32")
+    w[3] = -1000.0
+    same, _ = forward(h, w, t, "f32")
+    assert torch.isfinite(loss).all() and torch.allclose(loss, same, rtol=1e-6, atol=1e-6)
