@@ -649,41 +649,137 @@ void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, co
   if (lse) lse[i] = counts ? top + log_sum : 0.0f;
 }
 
-// The hidden states' gradient over one piece: rows of the tile are columns of the
-// hidden states, columns tokens. Split i of the sum goes to fp32 rows of its own.
-template <class S>
+// A product whose sum is split, with fp32 rows of its own for each split: the hidden
+// states' gradient over one piece (rows of the tile are columns of the hidden states,
+// columns tokens), and logits of fewer tiles than CUs (rows of the head, tokens).
+template <class S, GemmMode MA, bool HALF>
 __global__ __launch_bounds__(S::THREADS, 2)
-void k_dhidden(GemmSide w, GemmSide g, Segments segs, int steps, int splits, int add, const int32_t* __restrict__ count_of,
-               float* __restrict__ out, int64_t dq, int64_t np) {
+void k_split(GemmSide a, GemmSide b, int64_t m, Segments segs, int steps, int splits, int add,
+             const int32_t* __restrict__ count_of, float* __restrict__ out, int64_t ld, int64_t np,
+             const int32_t* __restrict__ a_power, const int32_t* __restrict__ b_power) {
   __shared__ __align__(1024) char lds[S::LDS];
   const int64_t count = *count_of;
-  const uint32_t tm = (uint32_t)((w.cols + S::BM - 1) / S::BM), tn = (uint32_t)((count + S::BN - 1) / S::BN);
+  const uint32_t tm = (uint32_t)((m + S::BM - 1) / S::BM), tn = (uint32_t)((count + S::BN - 1) / S::BN);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int total = segs.count * steps;
   // the splits of a tile lie behind one another in the tiles' order: tile.n = split * tn + n
   auto make = [&](auto& loop, const Tile& at) {
     const int64_t split = at.n / tn;
-    loop.aim(w, g, at.m * S::BM, at.n % tn * S::BN, segs, steps, (int)(total * split / splits),
+    loop.aim(a, b, at.m * S::BM, at.n % tn * S::BN, segs, steps, (int)(total * split / splits),
              (int)(total * (split + 1) / splits));
   };
   auto finish = [&](const Tile& at, typename S::Acc& acc) {
-    float* mine = out + (int64_t)(at.n / tn) * np * dq;
+    float* mine = out + (int64_t)(at.n / tn) * np * ld;
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) {
       const int64_t token = at.n % tn * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
+      const int of_token = HALF && token < count ? b_power[token] : 0;
 #pragma unroll
       for (int i = 0; i < S::TM; ++i) {
         const int64_t c = at.m * S::BM + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
-        if (token < count && c < dq) {
-          f32x4* to = (f32x4*)(mine + token * dq + c);
+        if (token < count && c < ld) {
+          f32x4* to = (f32x4*)(mine + token * ld + c);
+          if constexpr (HALF) {
+            const int4 of_row = *(const int4*)(a_power + c);  // rows up to a multiple of 256 have a place
+            acc[i][j] = f32x4{ldexpf(acc[i][j].x, of_row.x + of_token), ldexpf(acc[i][j].y, of_row.y + of_token),
+                              ldexpf(acc[i][j].z, of_row.z + of_token), ldexpf(acc[i][j].w, of_row.w + of_token)};
+          }
           *to = add ? *to + acc[i][j] : acc[i][j];
         }
       }
     }
     return false;
   };
-  tiles_of<S, K_IS_ROW, K_IN_ROWS>(lds, tm * tn * splits, tm, tn * splits, make, finish);
+  tiles_of<S, MA, K_IN_ROWS, HALF>(lds, tm * tn * splits, tm, tn * splits, make, finish);
+}
+
+__device__ __forceinline__ f32x4 sum_of_splits(const float* p, int splits, int64_t apart) {
+  f32x4 z = *(const f32x4*)p;
+#pragma unroll 4
+  for (int k = 1; k < splits; ++k) z += *(const f32x4*)(p + k * apart);
+  return z;
+}
+
+// Split logits joined, 2048 of a token to a workgroup: their maximum and sum.
+constexpr int kJoinRows = 2048;
+__global__ __launch_bounds__(kThreads)
+void k_join_logits(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, int64_t vc, Tokens tok,
+                   float2* __restrict__ parts, float* __restrict__ own, int64_t np) {
+  constexpr int N = kJoinRows / (4 * kThreads);
+  __shared__ float2 joined[kThreads / 64];
+  const int64_t token = blockIdx.x;
+  if (token >= *tok.count) return;  // uniform
+  const int label = tok.label[token];
+  const int64_t mine = label >= 0 ? label - v0 : -1;
+  f32x4 x[N];
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t v = (int64_t)blockIdx.y * kJoinRows + (i * kThreads + threadIdx.x) * 4;
+    x[i] = f32x4{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (v >= vc) continue;
+    const f32x4 y = sum_of_splits(z + token * ld + v, splits, np * ld);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (v + r < vc) x[i][r] = y[r];
+      if (v + r == mine) own[token] = y[r];
+      top = fmaxf(top, x[i][r]);
+    }
+  }
+  auto of_wave = [&](float a, bool take_max) {
+    for (int d = 32; d > 0; d /= 2) {
+      const float b = __shfl_xor(a, d);
+      a = take_max ? fmaxf(a, b) : a + b;
+    }
+    return a;
+  };
+  top = of_wave(top, true);
+  const float from = top == -INFINITY ? 0.0f : top;  // exp(-inf) = 0 where all are that, not of -inf + inf
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum += exp_of(x[i][r] - from);
+  sum = of_wave(sum, false);
+  if ((threadIdx.x & 63) == 0) joined[threadIdx.x >> 6] = float2{top, sum};
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float m = joined[0].x, t = 0.0f;
+  for (int k = 1; k < kThreads / 64; ++k) m = fmaxf(m, joined[k].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  for (int k = 0; k < kThreads / 64; ++k) t += joined[k].y * exp_of(joined[k].x - base);
+  parts[(int64_t)blockIdx.y * np + token] = float2{m, t};
+}
+
+// Split logits joined to g, zeros behind the last token up to a multiple of 64 and behind the last row.
+template <int PLANES>
+__global__ __launch_bounds__(kThreads)
+void k_join_g(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, int64_t vc, Tokens tok, int64_t np,
+              uint16_t* __restrict__ g, int64_t gp) {
+  const int64_t count = *tok.count, written = (count + 63) / 64 * 64, per = gp / 4;
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < written * per; at += (int64_t)gridDim.x * kThreads) {
+    const int64_t token = at / per, v = at % per * 4;
+    f32x4 d = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (token < count && v < vc) {
+      const int64_t mine = (int64_t)tok.label[token] - v0;
+      const float lse = tok.lse[token], coef = tok.coef[token];
+      const f32x4 x = sum_of_splits(z + token * ld + v, splits, np * ld);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float p = exp_of(x[r] - lse);
+        d[r] = v + r < vc ? coef * (v + r == mine ? p - 1.0f : p) : 0.0f;
+        if (v + r == mine) tok.rest[token] = d[r] - bf16_lo(pack_bf16(d[r], d[r]));
+      }
+    }
+    uint16_t* row = g + token * gp * PLANES + v;
+#pragma unroll
+    for (int k = 0; k < PLANES; ++k) {
+      const uint2 y = uint2{pack_bf16(d.x, d.y), pack_bf16(d.z, d.w)};
+      *(uint2*)(row + k * gp) = y;
+      d = f32x4{d.x - bf16_lo(y.x), d.y - bf16_hi(y.x), d.z - bf16_lo(y.y), d.w - bf16_hi(y.y)};
+    }
+  }
 }
 
 // The head's gradient for one piece: rows of the tile are columns of the hidden
@@ -831,33 +927,37 @@ Tokens tokens_at(const HeadPlan& p, void* workspace) {
                 (float*)(w + p.coef), (float*)(w + p.lse), (float*)(w + p.rest)};
 }
 
-// The tiles of a product, and how long it takes: rounds of tiles on 256 CUs, in
-// the time of one round of the widest. Two of the others run on a CU at once and
-// reach 0.72 of its rate (128 x 128: 890 TFLOP/s against 1250), one alone takes
-// 0.6 of the time of two.
+// How a product is made: its tiles, in how many parts of the sum, and how long it
+// takes, in stages of the widest tile (1.7 us). 256 CUs take a round of these at once.
+// Two of the other tiles run on a CU at once and reach 0.72 of its rate (128 x 128:
+// 890 TFLOP/s against 1250), one alone takes 0.6 of the time of two. A round costs
+// some stages beside its own: first loads, what is done with the products. Parts are
+// of eight stages at least, and written and read once more.
 enum Cut { WIDE, SQUARE, NARROW };
-struct CutOf {
+struct Way {
   Cut cut;
-  double rounds;
+  int splits;
+  double cost;
 };
-CutOf cut_of(int64_t m, int64_t n) {
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  auto pairs = [&](int64_t t) { return (double)(t / 512) + (t % 512 == 0 ? 0.0 : t % 512 <= 256 ? 0.6 : 1.0); };
-  const double wide = (double)((tiles(256, 256) + 255) / 256), square = pairs(tiles(128, 128)) * 0.5 / 0.72,
-               narrow = pairs(tiles(256, 64)) * 0.5 / 0.72;
-  if (n <= 64 && narrow <= square && narrow <= wide) return {NARROW, narrow};
-  return square < wide ? CutOf{SQUARE, square} : CutOf{WIDE, wide};
-}
-// What a round costs beside its stages (first loads, what is done with the products), in stages.
 constexpr double kRoundStages = 10;
-
-// Parts of the sum for the hidden states' gradient, so that its tiles fill the CUs (two of the narrow ones on
-// each): eight stages at least to each.
-int splits_of(int64_t dim, int64_t n, int64_t stages) {
-  const int64_t tiles = ((dim + 255) / 256) * ((n + 255) / 256);
-  const int64_t splits = least(least(512 / tiles, n <= 64 ? 256 : 16), stages / 8);
-  return (int)(splits < 1 ? 1 : splits);
+Way way_of(int64_t m, int64_t n, int64_t stages, int most = 1, double join = 0.0) {
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+  const int64_t t[3] = {tiles(256, 256), tiles(128, 128), tiles(256, 64)};
+  auto pairs = [](int64_t t) { return ((double)(t / 512) + (t % 512 == 0 ? 0.0 : t % 512 <= 256 ? 0.6 : 1.0)) * 0.5 / 0.72; };
+  Way best{WIDE, 1, 1e300};
+  for (int splits = 1; splits <= most; splits += splits < 4 ? 1 : splits / 4 * 2) {  // 1 2 3 4 6 8 12 18 ...
+    if (splits > 1 && stages / splits < 8) break;
+    const double wide = (double)((t[0] * splits + 255) / 256), square = pairs(t[1] * splits), narrow = pairs(t[2] * splits);
+    const Cut cut = n <= 64 && narrow <= square && narrow <= wide ? NARROW : square < wide ? SQUARE : WIDE;
+    const double rounds = cut == NARROW ? narrow : cut == SQUARE ? square : wide;
+    const double cost = rounds * ((double)stages / splits + kRoundStages) +
+                        (splits > 1 ? join + (double)m * (double)n * splits * 1.2e-6 : 0.0);
+    if (cost < best.cost) best = Way{cut, splits, cost};
+  }
+  return best;
 }
+Way way_of_logits(int64_t vc, int64_t n, int64_t stages) { return way_of(vc, n, stages, 32, 4.0); }
+Way way_of_dhidden(int64_t dim, int64_t n, int64_t stages) { return way_of(dim, n, stages, n <= 64 ? 256 : 32); }
 
 // As many workgroups as 256 CUs hold at once, or tiles, which they then take in turn.
 template <class S>
@@ -935,11 +1035,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
     const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1,
                   wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;
     auto one = [&](int64_t vc) {
-      const int64_t stages = up(vc, kBK) / kBK * parts;
-      const int splits = splits_of(dim, n, stages);
-      return cut_of(vc, n).rounds * (double)(p.dp / kBK * parts + kRoundStages) +
-             cut_of(dim, n * splits).rounds * ((double)stages / splits + kRoundStages) +
-             cut_of(dim, vc).rounds * (double)(p.np / kBK * wparts + kRoundStages);
+      return way_of_logits(vc, n, p.dp / kBK * parts).cost + way_of_dhidden(dim, n, up(vc, kBK) / kBK * parts).cost +
+             way_of(dim, vc, p.np / kBK * wparts).cost;
     };
     auto all = [&](int64_t piece) {
       const int64_t rest = vocab % piece;
@@ -955,9 +1052,16 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
         p.piece = piece;
       }
     }
-    p.splits = splits_of(dim, n, p.piece / kBK * parts);
+    p.splits = way_of_dhidden(dim, n, up(least(p.piece, vocab), kBK) / kBK * parts).splits;
   }
   p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
+  // Room for logits in parts: of a piece and of the last one, or, in the forward pass, of the whole head where it lies.
+  const int64_t zstages = p.dp / kBK * (p.planes == 1 ? 1 : grad ? 6 : 3);
+  auto room = [&](int64_t rows) {
+    const int64_t splits = rows > 0 && n > 0 ? way_of_logits(rows, n, zstages).splits : 1;
+    return splits > 1 ? splits * p.np * up(rows, kBK) * 4 : 0;
+  };
+  const int64_t of_piece = room(least(p.piece, vocab)), of_other = room(grad && p.piece ? vocab % p.piece : vocab);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -978,6 +1082,7 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.weight = take(p.piece * p.dp * p.planes * 2);
   p.hpower = take(grad || dtype != ZS_F32 ? 0 : p.np * 4);
   p.wpower = take(grad || dtype != ZS_F32 ? 0 : p.piece * 4);
+  p.z = take(of_piece > of_other ? of_piece : of_other);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
   p.dhidden = take(grad ? p.splits * p.np * p.dq * 4 : 0);
   p.bytes = at;
@@ -1049,8 +1154,11 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     else layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
     h = GemmSide{to, p.dp * p.planes, p.dp, p.np, 0};
   }
-  const Cut cut = cut_of(vocab, n).cut;
-  const int64_t piece = w_lies ? vocab : p.piece;
+  const int64_t piece = w_lies ? vocab : least(p.piece, vocab), zq = up(piece, kBK), chunks = (piece + kJoinRows - 1) / kJoinRows;
+  const Way way = way_of_logits(piece, n, p.dp / kBK * segs.count);
+  const bool split = way.splits > 1;
+  float* z = (float*)(ws + p.z);
+  int64_t tiles = 0;
   for (int64_t v0 = 0; v0 < vocab; v0 += piece) {
     const int64_t vc = least(piece, vocab - v0);
     GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, 0};
@@ -1061,24 +1169,31 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
       else layout(from, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
       w = GemmSide{to, p.dp * p.planes, p.dp, vc, 0};
     }
-    with_cut(cut, [&](auto shape) {
+    float2* parts = (float2*)(ws + p.parts) + tiles * p.np;
+    with_cut(way.cut, [&](auto shape) {
       using S = decltype(shape);
-      auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs, (int)(p.dp / kBK), v0,
-                           tok, (float2*)(ws + p.parts) + v0 / S::BM * parts_of_tile<S>() * p.np, (float*)(ws + p.own),
-                           p.np, (uint16_t*)nullptr, (int64_t)0, w_power, h_power);
+      constexpr bool HALVES = !std::is_same_v<S, Narrow>;  // of fp32 few tokens took the head as it lies
+      auto go = [&](auto halves) {
+        constexpr bool H = HALVES && decltype(halves)::value;
+        if (split)
+          hipLaunchKernelGGL((k_split<S, K_IN_ROWS, H>), dim3(workgroups<S>(vc, n, way.splits)), dim3(S::THREADS), 0, s, w,
+                             h, vc, segs, (int)(p.dp / kBK), way.splits, 0, tok.count, z, zq, p.np, w_power, h_power);
+        else
+          hipLaunchKernelGGL((k_logits<S, 0, H>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w, h, segs,
+                             (int)(p.dp / kBK), v0, tok, parts, (float*)(ws + p.own), p.np, (uint16_t*)nullptr, (int64_t)0,
+                             w_power, h_power);
       };
-      if constexpr (!std::is_same_v<S, Narrow>) {  // of fp32 few tokens took the head as it lies
-        if (half) return go(k_logits<S, 0, true>);
-      }
-      go(k_logits<S, 0>);
+      if (half) go(std::true_type{});
+      else go(std::false_type{});
+      tiles += split ? chunks : (vc + S::BM - 1) / S::BM * parts_of_tile<S>();
     });
+    if (split) {
+      const int64_t of_vc = (vc + kJoinRows - 1) / kJoinRows;
+      hipLaunchKernelGGL(k_join_logits, dim3((unsigned)n, (unsigned)of_vc), dim3(kThreads), 0, s, z, way.splits, zq, v0,
+                         vc, tok, parts, (float*)(ws + p.own), p.np);
+      tiles += of_vc - chunks;
+    }
   }
-  int64_t tiles = 0;
-  with_cut(cut, [&](auto shape) {
-    using S = decltype(shape);
-    tiles = (vocab + S::BM - 1) / S::BM * parts_of_tile<S>();
-  });
   if (n <= 64) join(std::integral_constant<int, 1>{}, std::true_type{}, tiles);
   else join(std::integral_constant<int, 16>{}, std::true_type{}, tiles);
   return hipGetLastError();
@@ -1104,7 +1219,9 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
                                           : kOne;
   const bool w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   uint16_t *hp = (uint16_t*)(ws + p.hidden), *gp = (uint16_t*)(ws + p.g);
-  float* sums = (float*)(ws + p.dhidden);
+  float *sums = (float*)(ws + p.dhidden), *z = (float*)(ws + p.z);
+  const int32_t* no_power = nullptr;
+  const Way dway = way_of_dhidden(dim, n, up(p.piece < vocab ? p.piece : vocab, kBK) / kBK * segs.count);
   number_tokens(labels, index_type, n, vocab, true, lse, dloss, scale, tok, nullptr, nullptr, s);
   layout(hidden, hidden_ld, dtype, dim, n, hp, p.dp, tok.map, tok.count, s);
   for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
@@ -1118,29 +1235,44 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     }
     const GemmSide h{hp, p.dp * p.planes, p.dp, p.np, p.dp};
     const GemmSide g_rows{gp, ldg, vp, p.np, vp};
-    with_cut(cut_of(vc, n).cut, [&](auto shape) {
-      using S = decltype(shape);
-      auto go = [&](auto planes) {
-        hipLaunchKernelGGL((k_logits<S, decltype(planes)::value>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w,
-                           h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, (const int32_t*)nullptr,
-                           (const int32_t*)nullptr);
-      };
+    const Way zway = way_of_logits(vc, n, p.dp / kBK * segs.count);
+    auto by_planes = [&](auto go) {
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
       else if (p.gplanes == 2) go(std::integral_constant<int, 2>{});
       else go(std::integral_constant<int, 3>{});
-    });
-    with_cut(n <= 64 ? NARROW : cut_of(dim, n * p.splits).cut, [&](auto shape) {
+    };
+    with_cut(zway.cut, [&](auto shape) {
       using S = decltype(shape);
-      hipLaunchKernelGGL((k_dhidden<S>), dim3(workgroups<S>(dim, n, p.splits)), dim3(S::THREADS), 0, s, w, g_rows, segs,
-                         (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np);
-    });
-    with_cut(cut_of(dim, vc).cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {
-      using S = std::conditional_t<std::is_same_v<decltype(shape), Square>, Square, Wide>;
-      const unsigned grid = workgroups<S>(dim, vc);
-      if (grad_dtype == ZS_BF16)
-        hipLaunchKernelGGL((k_dweight<S, uint16_t>), dim3(grid), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tok.count, v0, vc, (uint32_t)dim, (uint16_t*)dweight, dweight_ld, (int)first);
+      if (zway.splits > 1)
+        hipLaunchKernelGGL((k_split<S, K_IN_ROWS, false>), dim3(workgroups<S>(vc, n, zway.splits)), dim3(S::THREADS), 0, s,
+                           w, h, vc, segs, (int)(p.dp / kBK), zway.splits, 0, tok.count, z, vp, p.np, no_power, no_power);
       else
-        hipLaunchKernelGGL((k_dweight<S, float>), dim3(grid), dim3(S::THREADS), 0, s, h, g_rows, wsegs, tok.count, v0, vc, (uint32_t)dim, (float*)dweight, dweight_ld, (int)first);
+        by_planes([&](auto planes) {
+          hipLaunchKernelGGL((k_logits<S, decltype(planes)::value>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w,
+                             h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, no_power,
+                             no_power);
+        });
+    });
+    if (zway.splits > 1)
+      by_planes([&](auto planes) {
+        hipLaunchKernelGGL((k_join_g<decltype(planes)::value>), dim3(grid_of(p.np * vp / 4)), dim3(kThreads), 0, s, z,
+                           zway.splits, vp, v0, vc, tok, p.np, gp, vp);
+      });
+    with_cut(dway.cut, [&](auto shape) {
+      using S = decltype(shape);
+      hipLaunchKernelGGL((k_split<S, K_IS_ROW, false>), dim3(workgroups<S>(dim, n, p.splits)), dim3(S::THREADS), 0, s, w,
+                         g_rows, dim, segs, (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np, no_power,
+                         no_power);
+    });
+    with_cut(way_of(dim, vc, p.np / kBK * wsegs.count).cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {
+      using S = std::conditional_t<std::is_same_v<decltype(shape), Square>, Square, Wide>;
+      auto go = [&](auto type) {
+        using Gt = decltype(type);
+        hipLaunchKernelGGL((k_dweight<S, Gt>), dim3(workgroups<S>(dim, vc)), dim3(S::THREADS), 0, s, h, g_rows, wsegs,
+                           tok.count, v0, vc, (uint32_t)dim, (Gt*)dweight, dweight_ld, (int)first);
+      };
+      if (grad_dtype == ZS_BF16) go(uint16_t{});
+      else go(float{});
     });
   }
   auto join = [&](auto type, auto groups) {

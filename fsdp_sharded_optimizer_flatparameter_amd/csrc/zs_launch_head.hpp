@@ -21,7 +21,7 @@ struct HeadPlan {
   int64_t piece;     // rows of the head at a time (a multiple of 256), where it is laid out anew or has a gradient
   int64_t pieces;
   int splits;        // parts of the sum over a piece for the hidden states' gradient
-  int64_t label, coef, lse, rest, map, inverse, count, own, parts, hidden, weight, hpower, wpower, g, dhidden, bytes;
+  int64_t label, coef, lse, rest, map, inverse, count, own, parts, hidden, weight, hpower, wpower, z, g, dhidden, bytes;
 };
 HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dtype);  // grad_dtype -1: the loss alone
 

@@ -305,3 +305,23 @@ def test_fp32_rows_of_minus_infinity():
     w[3] = -1000.0
     same, _ = forward(h, w, t, "f32")
     assert torch.isfinite(loss).all() and torch.allclose(loss, same, rtol=1e-6, atol=1e-6)
+
+
+@pytest.mark.parametrize("n,vocab,dim,dtype,grad", [
+    (40, 300, 4100, "bf16", "bf16"), (40, 5000, 4096, "bf16", "f32"), (9, 1, 8192, "bf16", "bf16"), (130, 2049, 3000, "bf16", "f32"),
+    (387, 260, 2050, "f32", "bf16"), (70, 4097, 1100, "f32", "f32"), (200, 129, 5000, "f32", "f32")])
+def test_few_tiles_of_long_rows(n, vocab, dim, dtype, grad):
+    """Fewer tiles than CUs: the logits' own sums are in parts."""
+    g = gen(dim)
+    w, h = matrix(g, vocab, dim, dtype, 0, dim ** -0.5)[1], matrix(g, n, dim, dtype)[1]
+    t = labels_of(g, n, vocab, torch.int32, 0.2)
+    t[: 3] = vocab - 1
+    loss, lse = forward(h, w, t, dtype)
+    check_forward(h, w, t, loss, lse)
+    c = torch.rand(n, generator=g, device="cuda") + 0.5
+    old = matrix(g, vocab, dim, grad)[1]
+    dh, dw = torch.full_like(h, float("nan")), old.clone()
+    big, ws = scratch(n, vocab, dim, dtype, grad)
+    zs.zs_linear_cross_entropy_backward(h, w, t, lse, dh, dw, dloss=c, scale=0.5, first=False, workspace=ws)
+    assert (big[ws.numel():] == 0xFF).all()
+    check_backward(h, w, t, lse, 0.5 * f64(c), dh, dw, old, False)
