@@ -789,6 +789,9 @@ __global__ __launch_bounds__(S::THREADS, 2)
 void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict__ count_of, int64_t v0, int64_t vc,
                uint32_t dim, Gt* __restrict__ dw, int64_t dw_ld, int first) {
   __shared__ __align__(1024) char lds[S::LDS];
+  // Whole tiles are stored by way of LDS, 64 columns of 16 rows at a time and wave: a lane holds 4 columns.
+  constexpr int IN = 4, EACH = 16 / sizeof(Gt), FLOATS = IN * 4, CHUNKS = IN * 16 / EACH;
+  __shared__ __align__(16) u32x4 lines[S::WM * S::WN][16 * FLOATS];
   const uint32_t tm = (dim + S::BM - 1) / S::BM, tn = (uint32_t)((vc + S::BN - 1) / S::BN);
   const int steps = (int)((*count_of + 63) / 64);  // none: the sums are zero
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -798,6 +801,60 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
   };
   auto finish = [&](const Tile& at, typename S::Acc& acc) {
     const bool whole = dim - at.m * S::BM >= S::BM && vc - at.n * S::BN >= S::BN;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+        for (int part = 0; part < S::TM / IN; ++part) {
+          const int t = lane & 15, c0 = wm * (S::BM / S::WM) + part * IN * 16;
+          Gt* to = dw + (v0 + at.n * S::BN + wn * (S::BN / S::WN) + j * 16) * dw_ld + at.m * S::BM + c0;
+          u32x4* mine = lines[wave];
+          u32x4 old[IN * 16 * 16 / EACH / 64];
+          if (!first)
+#pragma unroll
+            for (int x = 0; x < IN * 16 * 16 / EACH / 64; ++x) {
+              const int at16 = x * 64 + lane, row = at16 / CHUNKS, c = at16 % CHUNKS;
+              old[x] = ld16(to + row * dw_ld + c * EACH);
+            }
+#pragma unroll
+          for (int i = 0; i < IN; ++i) {
+            const f32x4 a = acc[part * IN + i][j];
+            // four columns lie in one chunk of fp32, or in half of one of two fp32 chunks
+            mine[t * FLOATS + ((4 * i + (lane >> 4)) ^ (t & (FLOATS - 1)))] =
+                u32x4{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w)};
+          }
+#pragma unroll
+          for (int x = 0; x < IN * 16 * 16 / EACH / 64; ++x) {
+            const int at16 = x * 64 + lane, row = at16 / CHUNKS, c = at16 % CHUNKS;
+            auto take = [&](int chunk) { return mine[row * FLOATS + (chunk ^ (row & (FLOATS - 1)))]; };
+            u32x4 y;
+            if constexpr (sizeof(Gt) == 4) {
+              y = take(c);
+              if (!first)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) + __uint_as_float(old[x][e]));
+            } else {
+              const u32x4 lo = take(2 * c), hi = take(2 * c + 1);
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[e] = __uint_as_float(lo[e]);
+                f[4 + e] = __uint_as_float(hi[e]);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (!first) {
+                  f[2 * e] += bf16_lo(old[x][e]);
+                  f[2 * e + 1] += bf16_hi(old[x][e]);
+                }
+                y[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+              }
+            }
+            st16(y, to + row * dw_ld + c * EACH);
+          }
+        }
+      return S::TN * (S::TM / IN) * (IN * 16 * 16 / EACH / 64) >= 16;
+    }
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) {
       const int64_t v = at.n * S::BN + wn * (S::BN / S::WN) + j * 16 + (lane & 15);
@@ -805,9 +862,9 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
 #pragma unroll
       for (int i = 0; i < S::TM; ++i) {
         const uint32_t c = (uint32_t)(at.m * S::BM) + wm * (S::BM / S::WM) + i * 16 + (lane >> 4) * 4;
-        if (!whole && (v >= vc || c >= dim)) continue;
+        if (v >= vc || c >= dim) continue;
         f32x4 x = acc[i][j];
-        if (whole || c + 4 <= dim) {
+        if (c + 4 <= dim) {
           if constexpr (sizeof(Gt) == 4) {
             if (!first) {
               const u32x4 old = ld16(row + c);
@@ -834,7 +891,7 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
         }
       }
     }
-    return whole && S::TM * S::TN >= 16;
+    return false;
   };
   tiles_of<S, K_IS_ROW, K_IS_ROW>(lds, tm * tn, tm, tn, make, finish);
 }
