@@ -783,23 +783,29 @@ void k_join_g(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, i
 }
 
 // The head's gradient for one piece: rows of the tile are columns of the hidden
-// states, columns rows of the head.
+// states, columns rows of the head. Splits of the sum over the tokens go to matrices
+// `apart` elements from each other.
 template <class S, typename Gt>
 __global__ __launch_bounds__(S::THREADS, 2)
 void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict__ count_of, int64_t v0, int64_t vc,
-               uint32_t dim, Gt* __restrict__ dw, int64_t dw_ld, int first) {
+               uint32_t dim, Gt* __restrict__ dw_of, int64_t dw_ld, int first, int splits, int64_t apart) {
   __shared__ __align__(1024) char lds[S::LDS];
   // Whole tiles are stored by way of LDS, 64 columns of 16 rows at a time and wave: a lane holds 4 columns.
   constexpr int IN = 4, EACH = 16 / sizeof(Gt), FLOATS = IN * 4, CHUNKS = IN * 16 / EACH;
   __shared__ __align__(16) u32x4 lines[S::WM * S::WN][16 * FLOATS];
   const uint32_t tm = (dim + S::BM - 1) / S::BM, tn = (uint32_t)((vc + S::BN - 1) / S::BN);
   const int steps = (int)((*count_of + 63) / 64);  // none: the sums are zero
+  const int total = segs.count * steps;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
   auto make = [&](auto& loop, const Tile& at) {
-    loop.aim(h, g, at.m * S::BM, at.n * S::BN, segs, steps, 0, segs.count * steps);
+    const int64_t split = at.n / tn;
+    loop.aim(h, g, at.m * S::BM, at.n % tn * S::BN, segs, steps, (int)(total * split / splits),
+             (int)(total * (split + 1) / splits));
   };
-  auto finish = [&](const Tile& at, typename S::Acc& acc) {
+  auto finish = [&](const Tile& part, typename S::Acc& acc) {
+    const Tile at{part.m, part.n % tn};
+    Gt* dw = dw_of + part.n / tn * apart;
     const bool whole = dim - at.m * S::BM >= S::BM && vc - at.n * S::BN >= S::BN;
     if (whole) {
 #pragma unroll
@@ -893,7 +899,31 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
     }
     return false;
   };
-  tiles_of<S, K_IS_ROW, K_IS_ROW>(lds, tm * tn, tm, tn, make, finish);
+  tiles_of<S, K_IS_ROW, K_IS_ROW>(lds, tm * tn * splits, tm, tn * splits, make, finish);
+}
+
+// The splits of the head's gradient, joined and rounded once.
+template <typename Gt>
+__global__ __launch_bounds__(kThreads)
+void k_join_dweight(const float* __restrict__ sums, int splits, int64_t apart, int64_t ld, int64_t vc, uint32_t dim,
+                    Gt* __restrict__ dw, int64_t dw_ld, int first) {
+  const int64_t per = (ld + 7) / 8;
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < vc * per; at += (int64_t)gridDim.x * kThreads) {
+    const int64_t v = at / per;
+    const uint32_t c = (uint32_t)(at % per) * 8;
+    const float* from = sums + v * ld + c;
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f}, a = sum_of_splits(from, splits, apart),
+                b = c + 4 < ld ? sum_of_splits(from + 4, splits, apart) : zero;
+    float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    Gt* to = dw + v * dw_ld;
+    if (!first) {
+      Piece<Gt, 8> p;
+      take_cols<Gt, 8>(p, to, c, dim);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += p.get(e);
+    }
+    store_cols<Gt, 8>(to, x, c, dim);
+  }
 }
 
 // The splits' sums, rounded once, back in the tokens' places; zeros where a token
@@ -1014,6 +1044,7 @@ Way way_of(int64_t m, int64_t n, int64_t stages, int most = 1, double join = 0.0
   return best;
 }
 Way way_of_logits(int64_t vc, int64_t n, int64_t stages) { return way_of(vc, n, stages, 32, 4.0); }
+Way way_of_dweight(int64_t dim, int64_t vc, int64_t stages) { return way_of(dim, vc, stages, 32, 4.0); }
 Way way_of_dhidden(int64_t dim, int64_t n, int64_t stages) { return way_of(dim, n, stages, n <= 64 ? 256 : 32); }
 
 // As many workgroups as 256 CUs hold at once, or tiles, which they then take in turn.
@@ -1087,13 +1118,13 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
   p.splits = 1;
+  const int64_t wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;  // products of planes for the head's gradient
   if (grad && p.pieces && n > 0 && dim > 0) {
     // Of pieces of equal size and those whose head's gradient fills rounds of the widest tiles, what takes least.
-    const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1,
-                  wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;
+    const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1;
     auto one = [&](int64_t vc) {
       return way_of_logits(vc, n, p.dp / kBK * parts).cost + way_of_dhidden(dim, n, up(vc, kBK) / kBK * parts).cost +
-             way_of(dim, vc, p.np / kBK * wparts).cost;
+             way_of_dweight(dim, vc, p.np / kBK * wparts).cost;
     };
     auto all = [&](int64_t piece) {
       const int64_t rest = vocab % piece;
@@ -1112,11 +1143,14 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
     p.splits = way_of_dhidden(dim, n, up(least(p.piece, vocab), kBK) / kBK * parts).splits;
   }
   p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
-  // Room for logits in parts: of a piece and of the last one, or, in the forward pass, of the whole head where it lies.
+  // Room for logits and the head's gradient in parts, one after the other: of a piece and of the last one, or, in the
+  // forward pass, of the whole head where it lies.
   const int64_t zstages = p.dp / kBK * (p.planes == 1 ? 1 : grad ? 6 : 3);
   auto room = [&](int64_t rows) {
-    const int64_t splits = rows > 0 && n > 0 ? way_of_logits(rows, n, zstages).splits : 1;
-    return splits > 1 ? splits * p.np * up(rows, kBK) * 4 : 0;
+    if (rows == 0 || n == 0 || dim == 0) return (int64_t)0;
+    const int64_t zs = way_of_logits(rows, n, zstages).splits, z = zs > 1 ? zs * p.np * up(rows, kBK) * 4 : 0;
+    const int64_t ws = grad ? way_of_dweight(dim, rows, p.np / kBK * wparts).splits : 1, w = ws > 1 ? ws * rows * p.dq * 4 : 0;
+    return z > w ? z : w;
   };
   const int64_t of_piece = room(least(p.piece, vocab)), of_other = room(grad && p.piece ? vocab % p.piece : vocab);
   int64_t at = 0;
@@ -1321,16 +1355,27 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
                          g_rows, dim, segs, (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np, no_power,
                          no_power);
     });
-    with_cut(way_of(dim, vc, p.np / kBK * wsegs.count).cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {
+    const Way wway = way_of_dweight(dim, vc, p.np / kBK * wsegs.count);
+    with_cut(wway.cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {
       using S = std::conditional_t<std::is_same_v<decltype(shape), Square>, Square, Wide>;
-      auto go = [&](auto type) {
-        using Gt = decltype(type);
-        hipLaunchKernelGGL((k_dweight<S, Gt>), dim3(workgroups<S>(dim, vc)), dim3(S::THREADS), 0, s, h, g_rows, wsegs,
-                           tok.count, v0, vc, (uint32_t)dim, (Gt*)dweight, dweight_ld, (int)first);
+      auto go = [&](auto* out, int64_t from, int64_t ld, int alone, int64_t apart) {
+        using Gt = std::remove_pointer_t<decltype(out)>;
+        hipLaunchKernelGGL((k_dweight<S, Gt>), dim3(workgroups<S>(dim, vc, wway.splits)), dim3(S::THREADS), 0, s, h, g_rows,
+                           wsegs, tok.count, from, vc, (uint32_t)dim, out, ld, alone, wway.splits, apart);
       };
-      if (grad_dtype == ZS_BF16) go(uint16_t{});
-      else go(float{});
+      if (wway.splits > 1) go(z, 0, p.dq, 1, vc * p.dq);
+      else if (grad_dtype == ZS_BF16) go((uint16_t*)dweight, v0, dweight_ld, (int)first, 0);
+      else go((float*)dweight, v0, dweight_ld, (int)first, 0);
     });
+    if (wway.splits > 1) {
+      auto go = [&](auto* out) {
+        using Gt = std::remove_pointer_t<decltype(out)>;
+        hipLaunchKernelGGL((k_join_dweight<Gt>), dim3(grid_of(vc * ((p.dq + 7) / 8))), dim3(kThreads), 0, s, z, wway.splits,
+                           vc * p.dq, p.dq, vc, (uint32_t)dim, out + v0 * dweight_ld, dweight_ld, (int)first);
+      };
+      if (grad_dtype == ZS_BF16) go((uint16_t*)dweight);
+      else go((float*)dweight);
+    }
   }
   auto join = [&](auto type, auto groups) {
     using T = decltype(type);

@@ -309,9 +309,10 @@ def test_fp32_rows_of_minus_infinity():
 
 @pytest.mark.parametrize("n,vocab,dim,dtype,grad", [
     (40, 300, 4100, "bf16", "bf16"), (40, 5000, 4096, "bf16", "f32"), (9, 1, 8192, "bf16", "bf16"), (130, 2049, 3000, "bf16", "f32"),
-    (387, 260, 2050, "f32", "bf16"), (70, 4097, 1100, "f32", "f32"), (200, 129, 5000, "f32", "f32")])
-def test_few_tiles_of_long_rows(n, vocab, dim, dtype, grad):
-    """Fewer tiles than CUs: the logits' own sums are in parts."""
+    (387, 260, 2050, "f32", "bf16"), (70, 4097, 1100, "f32", "f32"), (200, 129, 5000, "f32", "f32"),
+    (3000, 97, 130, "bf16", "bf16"), (5001, 65, 64, "bf16", "f32"), (1371, 450, 203, "f32", "f32"), (2000, 40, 301, "f32", "bf16")])
+def test_few_tiles_of_long_sums(n, vocab, dim, dtype, grad):
+    """Fewer tiles than CUs: the sums of the logits, or of the head's gradient, are in parts."""
     g = gen(dim)
     w, h = matrix(g, vocab, dim, dtype, 0, dim ** -0.5)[1], matrix(g, n, dim, dtype)[1]
     t = labels_of(g, n, vocab, torch.int32, 0.2)
