@@ -1015,11 +1015,13 @@ Tokens tokens_at(const HeadPlan& p, void* workspace) {
 }
 
 // How a product is made: its tiles, in how many parts of the sum, and how long it
-// takes, in stages of the widest tile (1.7 us). 256 CUs take a round of these at once.
-// Two of the other tiles run on a CU at once and reach 0.72 of its rate (128 x 128:
-// 890 TFLOP/s against 1250), one alone takes 0.6 of the time of two. A round costs
-// some stages beside its own: first loads, what is done with the products. Parts are
-// of eight stages at least, and written and read once more.
+// takes, in stages of the widest tile (1.7 us: 1250 TFLOP/s on 256 CUs), of which a
+// round costs some beside its own: first loads, what is done with the products
+// (256 x 256, 8 stages: 27 us). 128 x 128 tiles run on a CU at two at once (1.0 us a
+// stage, 1070 TFLOP/s) or alone (0.77 us). 256 x 64 ones wait for loads: 0.9 us a
+// stage for few, more for many, from HBM 1.6 us for 256 (5.3 TB/s), from the
+// memory-side cache about 1. Parts are of eight stages at least, and written and read
+// once more.
 enum Cut { WIDE, SQUARE, NARROW };
 struct Way {
   Cut cut;
@@ -1030,12 +1032,13 @@ constexpr double kRoundStages = 10;
 Way way_of(int64_t m, int64_t n, int64_t stages, int most = 1, double join = 0.0) {
   auto tiles = [&](int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
   const int64_t t[3] = {tiles(256, 256), tiles(128, 128), tiles(256, 64)};
-  auto pairs = [](int64_t t) { return ((double)(t / 512) + (t % 512 == 0 ? 0.0 : t % 512 <= 256 ? 0.6 : 1.0)) * 0.5 / 0.72; };
+  auto squares = [](int64_t t) { return (double)(t / 512) * 0.6 + (t % 512 == 0 ? 0.0 : t % 512 <= 256 ? 0.45 : 0.6); };
+  auto narrows = [](int64_t t) { return t < 220 ? 0.5 : (double)t * 0.0023; };
   Way best{WIDE, 1, 1e300};
   for (int splits = 1; splits <= most; splits += splits < 4 ? 1 : splits / 4 * 2) {  // 1 2 3 4 6 8 12 18 ...
     if (splits > 1 && stages / splits < 8) break;
-    const double wide = (double)((t[0] * splits + 255) / 256), square = pairs(t[1] * splits), narrow = pairs(t[2] * splits);
-    const Cut cut = n <= 64 && narrow <= square && narrow <= wide ? NARROW : square < wide ? SQUARE : WIDE;
+    const double wide = (double)((t[0] * splits + 255) / 256), square = squares(t[1] * splits), narrow = narrows(t[2] * splits);
+    const Cut cut = n <= 64 ? NARROW : square < wide ? SQUARE : WIDE;
     const double rounds = cut == NARROW ? narrow : cut == SQUARE ? square : wide;
     const double cost = rounds * ((double)stages / splits + kRoundStages) +
                         (splits > 1 ? join + (double)m * (double)n * splits * 1.2e-6 : 0.0);
@@ -1097,7 +1100,7 @@ constexpr int64_t kGradBytes = 1 << 30;
 constexpr int64_t kMostPiece = 1 << 20;
 // For an fp32 gradient of a bf16 head g has 24 bits, or 17 where this many tokens are added: rounding g to 17 bits is
 // off by 2^-19 of it on average, about what the fp32 sum of 4096 products is by itself, and a third of the products
-// for dw and of g's bytes are saved (8192 tokens, 50257 x 768: 2.9 ms, 3.6 with 24 bits).
+// for dw and of g's bytes are saved (8192 tokens, 50257 x 768: 2.75 ms, 3.40 with 24 bits).
 constexpr int64_t kLongSum = 4096;
 // Calls of fewer tokens keep every row where it is in the forward pass.
 constexpr int64_t kGatherTokens = 256;
