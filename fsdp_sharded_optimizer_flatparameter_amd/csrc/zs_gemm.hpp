@@ -1,4 +1,4 @@
-// bf16 matrix products D[m, n] = sum_k A[m, k] B[n, k] on the matrix units,
+// bf16 (or fp16) matrix products D[m, n] = sum_k A[m, k] B[n, k] on the matrix units,
 // accumulated in fp32; the epilogue that uses D is the caller's.
 //
 // Either operand lies in memory as rows of consecutive k (K_IN_ROWS: the logits
@@ -11,7 +11,7 @@
 // An fp32 operand is a sum of up to three bf16 planes that lie side by side in
 // each row, and a product of two such operands the sum of the products of their
 // planes that matter: Segments lists them, and the loop over k runs through one
-// after another into the same accumulators.
+// after another into the same accumulators. Scaled by rows, two fp16 planes do too.
 #pragma once
 
 #include "zs_device.hpp"
@@ -58,7 +58,7 @@ struct GemmShape {
 // 16 bytes from byte `off` of each lane behind the buffer's start to LDS, lane l's
 // to 16 l behind `lds`. Written out, as behind the builtin the compiler waits for
 // all loads before the next transposing read (ds_read_b64_tr_b16), which it
-// takes to read what they write; the waits are gemm_tile's own. M0 holds the LDS
+// takes to read what they write; the waits are TileLoop's own. M0 holds the LDS
 // address, and needs a wait state before it is used.
 __device__ __forceinline__ void load_to_lds(u32x4 buffer, uint32_t lds, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"

@@ -221,7 +221,8 @@ def test_against_differences():
             assert abs((up - down) / (2 * e) - d[at]) < 1e-8 + 1000 * U
 
 
-@pytest.mark.parametrize("n,vocab,dim,dtype", [(600, 3000, 192, "bf16"), (7, 3000, 100, "bf16"), (300, 1000, 100, "f32")])
+@pytest.mark.parametrize("n,vocab,dim,dtype", [
+    (600, 3000, 192, "bf16"), (7, 3000, 100, "bf16"), (300, 1000, 100, "f32"), (100, 700, 2048, "bf16"), (2000, 90, 130, "f32")])
 def test_graph_and_streams(n, vocab, dim, dtype):
     """Captured forward and backward passes on a stream of their own, replayed with new inputs, with other calls on
     another stream and workspace at the same time."""
@@ -320,9 +321,13 @@ def test_few_tiles_of_long_sums(n, vocab, dim, dtype, grad):
     loss, lse = forward(h, w, t, dtype)
     check_forward(h, w, t, loss, lse)
     c = torch.rand(n, generator=g, device="cuda") + 0.5
-    old = matrix(g, vocab, dim, grad)[1]
-    dh, dw = torch.full_like(h, float("nan")), old.clone()
-    big, ws = scratch(n, vocab, dim, dtype, grad)
-    zs.zs_linear_cross_entropy_backward(h, w, t, lse, dh, dw, dloss=c, scale=0.5, first=False, workspace=ws)
-    assert (big[ws.numel():] == 0xFF).all()
-    check_backward(h, w, t, lse, 0.5 * f64(c), dh, dw, old, False)
+    for first in (False, True):
+        flat, old = matrix(g, vocab, dim, grad, 3)
+        if first:
+            old[:] = float("nan")
+        dh, dw, kept = torch.full_like(h, float("nan")), old, old.clone()
+        big, ws = scratch(n, vocab, dim, dtype, grad)
+        zs.zs_linear_cross_entropy_backward(h, w, t, lse, dh, dw, dloss=c, scale=0.5, first=first, workspace=ws)
+        assert (big[ws.numel():] == 0xFF).all()
+        assert torch.isnan(flat[:vocab * (dim + 3)].view(vocab, dim + 3)[:, dim:]).all()
+        check_backward(h, w, t, lse, 0.5 * f64(c), dh, dw, kept, first)
