@@ -22,8 +22,8 @@
 // gradients in bf16, which are rounded as much themselves; for an fp32
 // gradient of a bf16 head it is a sum of three bf16 (24 bits) or, for many
 // tokens, of two (17 bits), and the three operands of an fp32 head's gradients are
-// sums of three, whose products below 2^-21 of the largest are left out. The loss
-// alone takes fp32 rows as sums of two fp16.
+// sums of three, whose products below 2^-21 of the largest are left out. The loss, and
+// the logits of many tokens for the gradients, take fp32 rows as sums of two fp16.
 //
 // Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.6 ms (its logits 6.5, 1330
 // TFLOP/s), the gradients 21 ms (1230 TFLOP/s); 8192 tokens, 50257 x 768 into an fp32
@@ -192,7 +192,7 @@ void k_layout(const T* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows,
   }
 }
 
-// fp32 rows for the loss alone, as fp16: with 2^k the power of two that brings the
+// fp32 rows for the logits, as fp16: with 2^k the power of two that brings the
 // row's largest finite magnitude to [2^14, 2^15), x 2^k = hi + lo, of 11 bits each, lie
 // as planes hi, hi 2^-11 and lo 2^11 (so that lo is rarely subnormal), of `dp` elements.
 // hi hi' + (hi 2^-11)(lo' 2^11) + (lo 2^11)(hi' 2^-11) is the product of two rows
@@ -200,12 +200,21 @@ void k_layout(const T* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows,
 // the other's largest, in three products instead of bf16's six. power takes -k.
 // Infinities lie in hi alone, so that they meet each value once. A wave takes a row,
 // and reads it twice.
+//
+// BOTH: the three bf16 planes of the gradients' products beside them, with zeros for the
+// rows behind the last up to a multiple of 64.
+template <bool BOTH>
 __global__ __launch_bounds__(kThreads)
 void k_layout_half(const float* __restrict__ src, int64_t ld, uint32_t dim, int64_t rows, uint16_t* __restrict__ dst,
-                   int64_t dp, int32_t* __restrict__ power, const int32_t* __restrict__ map, const int32_t* __restrict__ count) {
+                   int64_t dp, int32_t* __restrict__ power, const int32_t* __restrict__ map, const int32_t* __restrict__ count,
+                   uint16_t* __restrict__ planes) {
   const int lane = threadIdx.x & 63;
-  const int64_t live = count ? *count : rows;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < live; r += (int64_t)gridDim.x * 4) {
+  const int64_t live = count ? *count : rows, all = BOTH && count ? (live + 63) / 64 * 64 : live;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < all; r += (int64_t)gridDim.x * 4) {
+    if (BOTH && r >= live) {
+      for (int64_t c = lane * 8; c < 3 * dp; c += 64 * 8) *(u32x4*)(planes + r * dp * 3 + c) = u32x4{0u, 0u, 0u, 0u};
+      continue;
+    }
     const float* from = src + (map ? (int64_t)map[r] : r) * ld;
     float top = 0.0f;
     for (uint32_t c = lane * 8; c < dim; c += 64 * 8) {
@@ -241,6 +250,15 @@ void k_layout_half(const float* __restrict__ src, int64_t ld, uint32_t dim, int6
       *(f16x8*)to = hi;
       *(f16x8*)(to + dp) = low;
       *(f16x8*)(to + 2 * dp) = lo;
+      if constexpr (BOTH) {
+        uint32_t t[8][3];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) three_planes(p.get(i), t[i]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *(u32x4*)(planes + r * dp * 3 + k * dp + c) =
+              u32x4{bits_hi(t[0][k], t[1][k]), bits_hi(t[2][k], t[3][k]), bits_hi(t[4][k], t[5][k]), bits_hi(t[6][k], t[7][k])};
+      }
     }
   }
 }
@@ -1084,6 +1102,17 @@ void layout(const void* src, int64_t ld, int dtype, int64_t dim, int64_t rows, u
                        dst, dp, map, count);
 }
 
+void layout_half(const void* src, int64_t ld, int64_t dim, int64_t rows, uint16_t* dst, int64_t dp, int32_t* power,
+                 const int32_t* map, const int32_t* count, uint16_t* planes, hipStream_t s) {
+  const dim3 grid((unsigned)least((up(rows, 64) + 3) / 4, 4096)), block(kThreads);
+  if (planes)
+    hipLaunchKernelGGL((k_layout_half<true>), grid, block, 0, s, (const float*)src, ld, (uint32_t)dim, rows, dst, dp, power,
+                       map, count, planes);
+  else
+    hipLaunchKernelGGL((k_layout_half<false>), grid, block, 0, s, (const float*)src, ld, (uint32_t)dim, rows, dst, dp, power,
+                       map, count, planes);
+}
+
 void number_tokens(const void* labels, int index_type, int64_t n, int64_t vocab, bool gather, const float* lse,
                    const float* dloss, float scale, const Tokens& t, float* loss, float* lse_out, hipStream_t s) {
   if (index_type == ZS_I64)
@@ -1106,11 +1135,16 @@ void zero_rows(void* p, int dtype, int64_t ld, int64_t rows, int64_t dim, hipStr
 // piece (at least 4096 rows of the head, so that their product stays long).
 constexpr int64_t kLayoutBytes = 1 << 28;
 constexpr int64_t kGradBytes = 1 << 30;
+constexpr int64_t kWeightBytes = 1ll << 31;  // of the head's rows of such a piece, where they are laid out
 constexpr int64_t kMostPiece = 1 << 20;
 // For an fp32 gradient of a bf16 head g has 24 bits, or 17 where this many tokens are added: rounding g to 17 bits is
 // off by 2^-19 of it on average, about what the fp32 sum of 4096 products is by itself, and a third of the products
 // for dw and of g's bytes are saved (8192 tokens, 50257 x 768: 2.75 ms, 3.40 with 24 bits).
 constexpr int64_t kLongSum = 4096;
+// The gradients' logits of fp32 take three products of fp16 pairs instead of six of bf16 planes from this many tokens
+// on. For fewer, laying out both costs more than that saves (70 tokens, 18898 x 5170: 361 + 177 us, 161 + 254 with the
+// six; 3364 of 4805 tokens, 17606 x 1216: 85 + 514, 46 + 811).
+constexpr int64_t kHalfTokens = 512;
 // Calls of fewer tokens keep every row where it is in the forward pass.
 constexpr int64_t kGatherTokens = 256;
 
@@ -1120,22 +1154,25 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   HeadPlan p{};
   const bool grad = grad_dtype >= 0;
   p.planes = dtype == ZS_F32 ? 3 : 1;
+  p.half = dtype == ZS_F32 && (!grad || n >= kHalfTokens);
   p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? (n < kLongSum ? 3 : 2) : 1;
   p.np = up(n, 64);
   p.dp = up(dim, 64);
   p.dq = up(dim, 4);
   const int64_t row = grad ? p.np * p.gplanes * 2 : p.dp * p.planes * 2;
   int64_t most = (grad ? kGradBytes : kLayoutBytes) / (row > 0 ? row : 1);
+  if (grad) most = least(most, kWeightBytes / (p.dp > 0 ? p.dp * p.planes * (p.half ? 4 : 2) : 1));
   most = most < 4096 ? 4096 : most > kMostPiece ? kMostPiece : most / 256 * 256;
   p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
   p.splits = 1;
+  const int64_t zstages = p.dp / kBK * (p.half ? 3 : p.planes == 3 ? 6 : 1);
   const int64_t wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;  // products of planes for the head's gradient
   if (grad && p.pieces && n > 0 && dim > 0) {
     // Of pieces of equal size and those whose head's gradient fills rounds of the widest tiles, what takes least.
     const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1;
     auto one = [&](int64_t vc) {
-      return way_of_logits(vc, n, p.dp / kBK * parts).cost + way_of_dhidden(dim, n, up(vc, kBK) / kBK * parts).cost +
+      return way_of_logits(vc, n, zstages).cost + way_of_dhidden(dim, n, up(vc, kBK) / kBK * parts).cost +
              way_of_dweight(dim, vc, p.np / kBK * wparts).cost;
     };
     auto all = [&](int64_t piece) {
@@ -1157,7 +1194,6 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
   // Room for logits and the head's gradient in parts, one after the other: of a piece and of the last one, or, in the
   // forward pass, of the whole head where it lies.
-  const int64_t zstages = p.dp / kBK * (p.planes == 1 ? 1 : grad ? 6 : 3);
   auto room = [&](int64_t rows) {
     if (rows == 0 || n == 0 || dim == 0) return (int64_t)0;
     const int64_t zs = way_of_logits(rows, n, zstages).splits, z = zs > 1 ? zs * p.np * up(rows, kBK) * 4 : 0;
@@ -1183,8 +1219,10 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.parts = take(grad ? 0 : parts * p.np * (int64_t)sizeof(float2));
   p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
   p.weight = take(p.piece * p.dp * p.planes * 2);
-  p.hpower = take(grad || dtype != ZS_F32 ? 0 : p.np * 4);
-  p.wpower = take(grad || dtype != ZS_F32 ? 0 : p.piece * 4);
+  p.hpower = take(p.half ? p.np * 4 : 0);
+  p.wpower = take(p.half ? p.piece * 4 : 0);
+  p.hhalf = take(grad && p.half ? p.np * p.dp * 6 : 0);
+  p.whalf = take(grad && p.half ? p.piece * p.dp * 6 : 0);
   p.z = take(of_piece > of_other ? of_piece : of_other);
   p.g = take(grad ? p.np * p.piece * p.gplanes * 2 : 0);
   p.dhidden = take(grad ? p.splits * p.np * p.dq * 4 : 0);
@@ -1198,15 +1236,9 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   const HeadPlan p = head_plan(n, vocab, dim, dtype, -1);
   char* ws = static_cast<char*>(workspace);
   const Tokens tok = tokens_at(p, workspace);
-  const bool half = dtype == ZS_F32;
+  const bool half = p.half;
   const Segments segs = half ? kHalves : kOne;
   int32_t *h_power = (int32_t*)(ws + p.hpower), *w_power = (int32_t*)(ws + p.wpower);
-  auto layout_half = [&](const void* src, int64_t ld, int64_t rows, uint16_t* to, int32_t* power, const int32_t* map,
-                         const int32_t* count) {
-    const unsigned grid = (unsigned)least((rows + 3) / 4, 4096);
-    hipLaunchKernelGGL(k_layout_half, dim3(grid), dim3(kThreads), 0, s, (const float*)src, ld, (uint32_t)dim, rows, to,
-                       p.dp, power, map, count);
-  };
   const bool h_lies = as_it_lies(hidden, hidden_ld, dim, dtype), w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   const Labels given{labels, index_type == ZS_I64, vocab};
   auto join = [&](auto tokens, auto placed, int64_t tiles) {
@@ -1253,7 +1285,7 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
   GemmSide h{(const uint16_t*)hidden, hidden_ld, 0, n, 0};
   if (gather || !h_lies) {
     uint16_t* to = (uint16_t*)(ws + p.hidden);
-    if (half) layout_half(hidden, hidden_ld, n, to, h_power, tok.map, tok.count);
+    if (half) layout_half(hidden, hidden_ld, dim, n, to, p.dp, h_power, tok.map, tok.count, nullptr, s);
     else layout(hidden, hidden_ld, dtype, dim, n, to, p.dp, tok.map, tok.count, s);
     h = GemmSide{to, p.dp * p.planes, p.dp, p.np, 0};
   }
@@ -1268,7 +1300,7 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
     if (!w_lies) {
       uint16_t* to = (uint16_t*)(ws + p.weight);
       const char* from = (const char*)weight + v0 * weight_ld * (half ? 4 : 2);
-      if (half) layout_half(from, weight_ld, vc, to, w_power, nullptr, nullptr);
+      if (half) layout_half(from, weight_ld, dim, vc, to, p.dp, w_power, nullptr, nullptr, nullptr, s);
       else layout(from, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
       w = GemmSide{to, p.dp * p.planes, p.dp, vc, 0};
     }
@@ -1323,22 +1355,28 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
   const bool w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   uint16_t *hp = (uint16_t*)(ws + p.hidden), *gp = (uint16_t*)(ws + p.g);
   float *sums = (float*)(ws + p.dhidden), *z = (float*)(ws + p.z);
-  const int32_t* no_power = nullptr;
   const Way dway = way_of_dhidden(dim, n, up(p.piece < vocab ? p.piece : vocab, kBK) / kBK * segs.count);
   number_tokens(labels, index_type, n, vocab, true, lse, dloss, scale, tok, nullptr, nullptr, s);
-  layout(hidden, hidden_ld, dtype, dim, n, hp, p.dp, tok.map, tok.count, s);
+  const bool half = p.half;  // the logits' operands are fp16
+  const Segments zsegs = half ? kHalves : segs;
+  uint16_t *h_half = (uint16_t*)(ws + p.hhalf), *w_half = (uint16_t*)(ws + p.whalf);
+  int32_t *h_power = (int32_t*)(ws + p.hpower), *w_power = (int32_t*)(ws + p.wpower);
+  if (half) layout_half(hidden, hidden_ld, dim, n, h_half, p.dp, h_power, tok.map, tok.count, hp, s);
+  else layout(hidden, hidden_ld, dtype, dim, n, hp, p.dp, tok.map, tok.count, s);
   for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
     const int64_t vc = least(p.piece, vocab - v0), vp = up(vc, kBK), ldg = vp * p.gplanes;
     GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, dim};
     if (!w_lies) {
       uint16_t* to = (uint16_t*)(ws + p.weight);
-      const int64_t size = dtype == ZS_F32 ? 4 : 2;
-      layout((const char*)weight + v0 * weight_ld * size, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
+      const char* from = (const char*)weight + v0 * weight_ld * (dtype == ZS_F32 ? 4 : 2);
+      if (half) layout_half(from, weight_ld, dim, vc, w_half, p.dp, w_power, nullptr, nullptr, to, s);
+      else layout(from, weight_ld, dtype, dim, vc, to, p.dp, nullptr, nullptr, s);
       w = GemmSide{to, p.dp * p.planes, p.dp, vc, p.dp};
     }
     const GemmSide h{hp, p.dp * p.planes, p.dp, p.np, p.dp};
     const GemmSide g_rows{gp, ldg, vp, p.np, vp};
-    const Way zway = way_of_logits(vc, n, p.dp / kBK * segs.count);
+    const GemmSide zw = half ? GemmSide{w_half, p.dp * 3, p.dp, vc, 0} : w, zh = half ? GemmSide{h_half, p.dp * 3, p.dp, p.np, 0} : h;
+    const Way zway = way_of_logits(vc, n, p.dp / kBK * zsegs.count);
     auto by_planes = [&](auto go) {
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
       else if (p.gplanes == 2) go(std::integral_constant<int, 2>{});
@@ -1346,15 +1384,18 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     };
     with_cut(zway.cut, [&](auto shape) {
       using S = decltype(shape);
-      if (zway.splits > 1)
-        hipLaunchKernelGGL((k_split<S, K_IN_ROWS, false>), dim3(workgroups<S>(vc, n, zway.splits)), dim3(S::THREADS), 0, s,
-                           w, h, vc, segs, (int)(p.dp / kBK), zway.splits, 0, tok.count, z, vp, p.np, no_power, no_power);
-      else
-        by_planes([&](auto planes) {
-          hipLaunchKernelGGL((k_logits<S, decltype(planes)::value>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0, s, w,
-                             h, segs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp, no_power,
-                             no_power);
-        });
+      auto go = [&](auto planes, auto halves) {
+        constexpr bool HALF = decltype(halves)::value && !std::is_same_v<S, Narrow>;  // not for few tokens
+        if (zway.splits > 1)
+          hipLaunchKernelGGL((k_split<S, K_IN_ROWS, HALF>), dim3(workgroups<S>(vc, n, zway.splits)), dim3(S::THREADS), 0, s,
+                             zw, zh, vc, zsegs, (int)(p.dp / kBK), zway.splits, 0, tok.count, z, vp, p.np, w_power, h_power);
+        else
+          hipLaunchKernelGGL((k_logits<S, decltype(planes)::value, HALF>), dim3(workgroups<S>(vc, n)), dim3(S::THREADS), 0,
+                             s, zw, zh, zsegs, (int)(p.dp / kBK), v0, tok, (float2*)nullptr, (float*)nullptr, p.np, gp, vp,
+                             w_power, h_power);
+      };
+      if (half) go(std::integral_constant<int, 3>{}, std::true_type{});
+      else by_planes([&](auto planes) { go(planes, std::false_type{}); });
     });
     if (zway.splits > 1)
       by_planes([&](auto planes) {
@@ -1364,8 +1405,8 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     with_cut(dway.cut, [&](auto shape) {
       using S = decltype(shape);
       hipLaunchKernelGGL((k_split<S, K_IS_ROW, false>), dim3(workgroups<S>(dim, n, p.splits)), dim3(S::THREADS), 0, s, w,
-                         g_rows, dim, segs, (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np, no_power,
-                         no_power);
+                         g_rows, dim, segs, (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np, w_power,
+                         h_power);
     });
     const Way wway = way_of_dweight(dim, vc, p.np / kBK * wsegs.count);
     with_cut(wway.cut == SQUARE ? SQUARE : WIDE, [&](auto shape) {

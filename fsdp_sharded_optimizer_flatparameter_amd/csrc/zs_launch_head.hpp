@@ -15,13 +15,15 @@ namespace zs {
 struct HeadPlan {
   int planes;        // bf16 planes of the hidden states and of the head's weight
   int gplanes;       // of the logits' gradient
+  bool half;         // fp32 logits from pairs of fp16
   int64_t np;        // tokens rounded up to 64
   int64_t dp;        // dim rounded up to 64
   int64_t dq;        // dim rounded up to 4: a row of the hidden states' gradient in fp32
   int64_t piece;     // rows of the head at a time (a multiple of 256), where it is laid out anew or has a gradient
   int64_t pieces;
   int splits;        // parts of the sum over a piece for the hidden states' gradient
-  int64_t label, coef, lse, rest, map, inverse, count, own, parts, hidden, weight, hpower, wpower, z, g, dhidden, bytes;
+  int64_t label, coef, lse, rest, map, inverse, count, own, parts, hidden, weight, hpower, wpower, hhalf, whalf, z,
+      g, dhidden, bytes;
 };
 HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dtype);  // grad_dtype -1: the loss alone
 

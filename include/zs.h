@@ -764,7 +764,8 @@ zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld,
  *                      grad_dtype) bytes on a 16-byte boundary; calls and graph
  *                      replays that may run at the same time need one each
  * The logits are made again, a piece of the vocabulary at a time, of fp32 values as
- * sums of three bf16, with an error of the size of fp32 products' roundings. An
+ * sums of three bf16, with an error of the size of fp32 products' roundings, or, for
+ * 512 tokens and more, of two fp16 as in the forward pass. An
  * infinite value makes the gradients that it reaches NaN. g is rounded to
  * bf16 for the gradients that are stored in bf16 from bf16 inputs; for the others
  * it has 24 bits, or 17 for an fp32 dweight of bf16 inputs and 4096 tokens or more,
