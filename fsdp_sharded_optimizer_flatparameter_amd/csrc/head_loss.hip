@@ -20,16 +20,15 @@
 //
 // Rounding: bf16 products are exact and added in fp32. g is rounded to bf16 for
 // gradients in bf16, which are rounded as much themselves; for an fp32
-// gradient of a bf16 head it is a sum of three bf16 (24 bits) or, for many
-// tokens, of two (17 bits), and the three operands of an fp32 head's gradients are
-// sums of three, whose products below 2^-21 of the largest are left out. The loss, and
-// the logits of many tokens for the gradients, take fp32 rows as sums of two fp16.
+// gradient it is a sum of three bf16 (24 bits; two of them take 2.75 instead of 3.4 ms
+// for 8192 tokens, 50257 x 768, but leave dw up to 2.4e-6 off, where fp32 products
+// leave 1.6e-6), and the three operands of an fp32 head's gradients are sums of three,
+// whose products below 2^-21 of the largest are left out. The loss, and the logits of
+// many tokens for the gradients, take fp32 rows as sums of two fp16.
 //
 // Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.6 ms (its logits 6.5, 1330
-// TFLOP/s), the gradients 21 ms (1230 TFLOP/s); 8192 tokens, 50257 x 768 into an fp32
-// accumulator: 2.75 ms, of which the logits 0.88 (720 TFLOP/s: g is 1.6 GB, and a
-// tile has 12 stages), dh 0.80, dw 1.1 (of two planes: 1130 TFLOP/s); one token,
-// 128256 x 4096: 181 us, 5.8 TB/s.
+// TFLOP/s), the gradients 21 ms (1230 TFLOP/s); one token: 181 us, 5.8 TB/s; 8192
+// tokens, 50257 x 768 into an fp32 accumulator: 3.4 ms.
 #include <type_traits>
 
 #include "zs_e4m3.hpp"
@@ -47,7 +46,6 @@ using Narrow = GemmShape<256, 64, 4, 1>;  // at most 64 tokens: the head's rows 
 
 // The smallest products come first: a sum rounds by its size so far.
 constexpr Segments kOne{1, 0, 0};
-constexpr Segments kTwo{2, 0x00, 0x01};           // one plane times two
 constexpr Segments kOneThree{3, 0x000, 0x012};    // one plane times three
 constexpr Segments kThree{3, 0x010, 0x001};       // 2 x 2 planes without the last
 constexpr Segments kSix{6, 0x010120, 0x001102};   // 3 x 3 planes, those above 2^-21
@@ -349,7 +347,7 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
   __shared__ float2 joined[PLANES == 0 && APART == 1 ? S::WM * S::BN : 1];
   // The lanes of a store hold 32 bytes each of 16 tokens' rows of g. By way of LDS, where
   // there is room, they are whole lines: 335 instead of 439 us for 8192 tokens, 21760
-  // rows of 768, two planes (287 without stores). The chunk of 16 bytes c of token t lies at
+  // rows of 768 in two planes (287 without stores). The chunk of 16 bytes c of token t lies at
   // place c ^ t.
   constexpr bool LINES = PLANES > 0 && APART == 1;
   constexpr int CHUNKS = ROWS / 8;
@@ -1137,10 +1135,6 @@ constexpr int64_t kLayoutBytes = 1 << 28;
 constexpr int64_t kGradBytes = 1 << 30;
 constexpr int64_t kWeightBytes = 1ll << 31;  // of the head's rows of such a piece, where they are laid out
 constexpr int64_t kMostPiece = 1 << 20;
-// For an fp32 gradient of a bf16 head g has 24 bits, or 17 where this many tokens are added: rounding g to 17 bits is
-// off by 2^-19 of it on average, about what the fp32 sum of 4096 products is by itself, and a third of the products
-// for dw and of g's bytes are saved (8192 tokens, 50257 x 768: 2.75 ms, 3.40 with 24 bits).
-constexpr int64_t kLongSum = 4096;
 // The gradients' logits of fp32 take three products of fp16 pairs instead of six of bf16 planes from this many tokens
 // on. For fewer, laying out both costs more than that saves (70 tokens, 18898 x 5170: 361 + 177 us, 161 + 254 with the
 // six; 3364 of 4805 tokens, 17606 x 1216: 85 + 514, 46 + 811).
@@ -1155,7 +1149,7 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   const bool grad = grad_dtype >= 0;
   p.planes = dtype == ZS_F32 ? 3 : 1;
   p.half = dtype == ZS_F32 && (!grad || n >= kHalfTokens);
-  p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? (n < kLongSum ? 3 : 2) : 1;
+  p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? 3 : 1;
   p.np = up(n, 64);
   p.dp = up(dim, 64);
   p.dq = up(dim, 4);
@@ -1348,10 +1342,7 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
   char* ws = static_cast<char*>(workspace);
   const Tokens tok = tokens_at(p, workspace);
   const Segments segs = p.planes == 3 ? kSix : kOne;
-  const Segments wsegs = p.planes == 3      ? (grad_dtype == ZS_F32 ? kSix : kThree)
-                         : p.gplanes == 3 ? kOneThree
-                         : p.gplanes == 2 ? kTwo
-                                          : kOne;
+  const Segments wsegs = p.planes == 3 ? (grad_dtype == ZS_F32 ? kSix : kThree) : p.gplanes == 3 ? kOneThree : kOne;
   const bool w_lies = as_it_lies(weight, weight_ld, dim, dtype);
   uint16_t *hp = (uint16_t*)(ws + p.hidden), *gp = (uint16_t*)(ws + p.g);
   float *sums = (float*)(ws + p.dhidden), *z = (float*)(ws + p.z);
@@ -1379,7 +1370,6 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     const Way zway = way_of_logits(vc, n, p.dp / kBK * zsegs.count);
     auto by_planes = [&](auto go) {
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
-      else if (p.gplanes == 2) go(std::integral_constant<int, 2>{});
       else go(std::integral_constant<int, 3>{});
     };
     with_cut(zway.cut, [&](auto shape) {

@@ -766,11 +766,10 @@ zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld,
  * The logits are made again, a piece of the vocabulary at a time, of fp32 values as
  * sums of three bf16, with an error of the size of fp32 products' roundings, or, for
  * 512 tokens and more, of two fp16 as in the forward pass. An
- * infinite value makes the gradients that it reaches NaN. g is rounded to
- * bf16 for the gradients that are stored in bf16 from bf16 inputs; for the others
- * it has 24 bits, or 17 for an fp32 dweight of bf16 inputs and 4096 tokens or more,
- * whose sum is off by as much; sums are fp32, in an order that depends on the sizes and
- * on how many tokens count alone. n == 0 with first != 0 sets dweight to zero.
+ * infinite value makes the gradients that it reaches NaN. g is rounded to bf16 for
+ * the gradients that are stored in bf16 from bf16 inputs, and has 24 bits for the
+ * others; sums are fp32, in an order that depends on the sizes and on how many tokens
+ * count alone. n == 0 with first != 0 sets dweight to zero.
  * Limits, overlaps and errors as above, and ZS_ERR_HPARAM.
  */
 zs_status zs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_ld, int32_t dtype,

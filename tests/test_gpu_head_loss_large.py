@@ -72,6 +72,8 @@ def check_sampled(h, w, t, lse, scale, dh, dw, old, first, tokens, rows):
     (17, 30011, 512, "f32", "bf16", True, 0.0),
     (5, 128256, 1024, "bf16", "bf16", True, 0.0),
     (3, 40009, 777, "f32", "f32", False, 0.0),
+    (20000, 9001, 96, "f32", "f32", False, 0.2),
+    (100, 50021, 1000, "f32", "bf16", True, 0.0),
 ])
 def test_large(n, vocab, dim, dtype, grad, first, ignored):
     g = gen(n + vocab)
