@@ -28,7 +28,8 @@
 //
 // Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.6 ms (its logits 6.5, 1330
 // TFLOP/s), the gradients 21 ms (1230 TFLOP/s); one token: 181 us, 5.8 TB/s; 8192
-// tokens, 50257 x 768 into an fp32 accumulator: 3.4 ms.
+// tokens, 50257 x 768 into an fp32 accumulator: 3.4 ms, of which the logits 1.06 (600
+// TFLOP/s: a tile has 12 stages, then 2.5 GB of g), dh 0.81, dw 1.6 (1210 TFLOP/s).
 #include <type_traits>
 
 #include "zs_e4m3.hpp"
