@@ -508,10 +508,12 @@ constexpr int kFewWaves = 4096;    // 4 workgroups of 4 waves on each CU
 // 1855: 100 in all, 35 here; 64: 92, 101 here; fp32, 20 tokens of 1856: over 260, 104 here).
 constexpr int kFewAligned = 8;
 
-template <typename T, int NT>
+// KEPT: for fp32 gradients, with the logits of token i and row v in own[i np + v], of `each`
+// columns to a part (blockIdx.y), which lie `apart` elements from each other.
+template <typename T, int NT, bool KEPT = false>
 __global__ __launch_bounds__(kThreads, 3)
 void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h0, const T* __restrict__ h1, int64_t h_ld,
-                  int n, int64_t vocab, uint32_t dim, int64_t groups, Labels labels, float2* __restrict__ parts, float* __restrict__ own, int64_t np) {
+                  int n, int64_t vocab, uint32_t dim, int64_t groups, Labels labels, float2* __restrict__ parts, float* __restrict__ own, int64_t np, uint32_t each, int64_t apart) {
   constexpr int VEC = 16 / (int)sizeof(T), U = NT == 1 ? 8 : 4;  // values of a piece, pieces of the head on their way
   constexpr uint32_t STEP = 4 * VEC;                             // values of k that a wave's instruction takes of a row
   __shared__ float2 joined[4][16 * NT];
@@ -523,6 +525,14 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
     const int i = t * 16 + col;
     label[t] = i < n ? labels.at(i) : -1;
     token_at[t] = (int64_t)(i < n ? i : n - 1) * h_ld;
+  }
+  if constexpr (KEPT) {
+    const uint32_t from = blockIdx.y * each;  // below dim
+    w += from;
+    h0 += from;
+    h1 += from;
+    own += blockIdx.y * apart;
+    dim = dim - from < each ? dim - from : each;
   }
   const bool paired = sizeof(T) == 2 && (w_ld & 1);
   const int64_t g0 = ((int64_t)blockIdx.x * 4 + wave) * groups;
@@ -592,6 +602,12 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
       }
     }
     // lane l has the wave's rows 4 (l / 16) to 4 (l / 16) + 3 for token l % 16 of each tile
+    if constexpr (KEPT) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t * 16 + col < n) *(f32x4*)(own + (t * 16 + col) * np + first + 4 * q) = acc[t];
+      continue;
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float m = top[t];
@@ -609,6 +625,7 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
       top[t] = m;
     }
   }
+  if constexpr (KEPT) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const float all = join4(top[t], true), from = all == -INFINITY ? 0.0f : all;
@@ -719,6 +736,71 @@ void k_split(GemmSide a, GemmSide b, int64_t m, Segments segs, int steps, int sp
   tiles_of<S, MA, K_IN_ROWS, HALF>(lds, tm * tn * splits, tm, tn * splits, make, finish);
 }
 
+// The fp32 hidden states' gradient of few tokens: the head's rows stream through
+// registers as they lie. A wave takes 64 columns of one part of the rows, 32 rows at
+// a time: lane l loads 16 bytes of rows 8 (l / 16) to 8 (l / 16) + 7, and with them g of
+// token l % 16 of each tile. 5203 x 7616 and 3, 20 and 64 tokens: 37, 60 and 105 us,
+// and the logits in place 33, 54 and 112; the planes of this head and the products with
+// them take 61, 107 and 77, whatever the number of tokens.
+template <int NT>
+__global__ __launch_bounds__(kThreads)
+void k_dhidden_few(const float* __restrict__ w, int64_t w_ld, const float* __restrict__ g, int64_t g_ld, Tokens tok,
+                   int64_t vc, uint32_t dim, int splits, int add, float* __restrict__ out, int64_t dq, int64_t np) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 63, col = lane & 15, q = lane >> 4, count = *tok.count;
+  const int64_t blocks = (dim + 63) / 64, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (count == 0 || id >= blocks * splits) return;  // uniform in a wave, and no barriers
+  const int64_t split = id / blocks, turns = (vc + 31) / 32;
+  const uint32_t c = (uint32_t)(id % blocks) * 64 + col * 4;
+  const float* row_of[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) row_of[t] = g + (int64_t)tok.map[t * 16 + col < count ? t * 16 + col : 0] * g_ld + q * U;
+  f32x4 acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int64_t turn = turns * split / splits; turn < turns * (split + 1) / splits; ++turn) {
+    const int64_t v0 = turn * 32;
+    Piece<float, 4> a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t v = v0 + q * U + u;  // g is zero for rows behind the last
+      load_cols<float, 4>(a[u], w + (v < vc ? v : vc - 1) * w_ld, c, dim);
+    }
+    f32x4 gv[NT][U / 4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int x = 0; x < U / 4; ++x) gv[t][x] = *(const f32x4*)(row_of[t] + v0 + 4 * x);
+    if (ragged(dim, 4))
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t v = v0 + q * U + u;
+        settle_cols<float, 4>(a[u], w + (v < vc ? v : vc - 1) * w_ld, c, dim);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[t][e] = __builtin_amdgcn_mfma_f32_16x16x4f32(gv[t][u / 4][u % 4], a[u].get(e), acc[t][e], 0, 0, 0);
+  }
+  // lane l has tokens 4 (l / 16) to 4 (l / 16) + 3 of each tile
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int token = t * 16 + 4 * q + r;
+      if (token < count && c < dq) {
+        f32x4* to = (f32x4*)(out + (split * np + token) * dq + c);
+        const f32x4 x = {acc[t][0][r], acc[t][1][r], acc[t][2][r], acc[t][3][r]};
+        *to = add ? *to + x : x;
+      }
+    }
+}
+
 __device__ __forceinline__ f32x4 sum_of_splits(const float* p, int splits, int64_t apart) {
   f32x4 z = *(const f32x4*)p;
 #pragma unroll 4
@@ -778,9 +860,10 @@ void k_join_logits(const float* __restrict__ z, int splits, int64_t ld, int64_t 
 }
 
 // Split logits joined to g, zeros behind the last token up to a multiple of 64 and behind the last row.
-template <int PLANES>
+// KEPT: the logits are k_logits_few's, in the tokens' rows, and g takes their place in fp32 too.
+template <int PLANES, bool KEPT = false>
 __global__ __launch_bounds__(kThreads)
-void k_join_g(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, int64_t vc, Tokens tok, int64_t np,
+void k_join_g(float* __restrict__ z, int splits, int64_t ld, int64_t v0, int64_t vc, Tokens tok, int64_t np,
               uint16_t* __restrict__ g, int64_t gp) {
   const int64_t count = *tok.count, written = (count + 63) / 64 * 64, per = gp / 4;
   for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < written * per; at += (int64_t)gridDim.x * kThreads) {
@@ -789,7 +872,7 @@ void k_join_g(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, i
     if (token < count && v < vc) {
       const int64_t mine = (int64_t)tok.label[token] - v0;
       const float lse = tok.lse[token], coef = tok.coef[token];
-      const f32x4 x = sum_of_splits(z + token * ld + v, splits, np * ld);
+      const f32x4 x = sum_of_splits(z + (KEPT ? tok.map[token] : token) * ld + v, splits, np * ld);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float p = exp_of(x[r] - lse);
@@ -797,6 +880,7 @@ void k_join_g(const float* __restrict__ z, int splits, int64_t ld, int64_t v0, i
         if (v + r == mine) tok.rest[token] = d[r] - bf16_lo(pack_bf16(d[r], d[r]));
       }
     }
+    if (KEPT && token < count) *(f32x4*)(z + tok.map[token] * ld + v) = d;
     uint16_t* row = g + token * gp * PLANES + v;
 #pragma unroll
     for (int k = 0; k < PLANES; ++k) {
@@ -1076,6 +1160,35 @@ Way way_of_logits(int64_t vc, int64_t n, int64_t stages) { return way_of(vc, n, 
 Way way_of_dweight(int64_t dim, int64_t vc, int64_t stages) { return way_of(dim, vc, stages, 32, 4.0); }
 Way way_of_dhidden(int64_t dim, int64_t n, int64_t stages) { return way_of(dim, n, stages, n <= 64 ? 256 : 32); }
 
+// Parts of the sum for few tokens' hidden states' gradient: 2048 waves, 8 a CU, with 32 rows of the head each at least.
+int few_splits(int64_t dim, int64_t rows) {
+  const int64_t blocks = (dim + 63) / 64, splits = least(least((2048 + blocks - 1) / blocks, 256), (rows + 31) / 32);
+  return (int)(splits < 1 ? 1 : splits);
+}
+// Workgroups that stream a head of few tokens, and 16-row groups of a wave.
+struct FewGrid {
+  int64_t groups, grid;
+};
+FewGrid few_grid(int64_t vocab) {
+  const int64_t all = (vocab + 31) / 32 * 2, groups = (all + kFewWaves - 1) / kFewWaves;
+  return {groups, groups ? (all + 4 * groups - 1) / (4 * groups) : 0};
+}
+// Columns of a part of few tokens' fp32 logits, so that there are 2048 waves, with 512 columns each at least.
+int64_t few_columns(int64_t rows, int64_t dim) {
+  const int64_t most = least(2048 / ((rows + 15) / 16), dim / 512), parts = most < 1 ? 1 : most;
+  return up((dim + parts - 1) / parts, 128);
+}
+int64_t few_parts(int64_t rows, int64_t dim) {
+  const int64_t each = few_columns(rows, dim);
+  return (dim + each - 1) / each;
+}
+template <typename F>
+void by_tokens(int64_t n, F&& f) {
+  if (n <= 16) f(std::integral_constant<int, 1>{});
+  else if (n <= 32) f(std::integral_constant<int, 2>{});
+  else f(std::integral_constant<int, 4>{});
+}
+
 // As many workgroups as 256 CUs hold at once, or tiles, which they then take in turn.
 template <class S>
 unsigned workgroups(int64_t m, int64_t n, int64_t splits = 1) {
@@ -1150,13 +1263,14 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   const bool grad = grad_dtype >= 0;
   p.planes = dtype == ZS_F32 ? 3 : 1;
   p.half = dtype == ZS_F32 && (!grad || n >= kHalfTokens);
+  p.few = grad && dtype == ZS_F32 && n <= kFewTokens;
   p.gplanes = dtype == ZS_F32 ? 3 : grad_dtype == ZS_F32 ? 3 : 1;
   p.np = up(n, 64);
   p.dp = up(dim, 64);
   p.dq = up(dim, 4);
   const int64_t row = grad ? p.np * p.gplanes * 2 : p.dp * p.planes * 2;
   int64_t most = (grad ? kGradBytes : kLayoutBytes) / (row > 0 ? row : 1);
-  if (grad) most = least(most, kWeightBytes / (p.dp > 0 ? p.dp * p.planes * (p.half ? 4 : 2) : 1));
+  if (grad && !p.few) most = least(most, kWeightBytes / (p.dp > 0 ? p.dp * p.planes * (p.half ? 4 : 2) : 1));
   most = most < 4096 ? 4096 : most > kMostPiece ? kMostPiece : most / 256 * 256;
   p.pieces = vocab > 0 ? (vocab + most - 1) / most : 0;
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
@@ -1184,14 +1298,15 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
         p.piece = piece;
       }
     }
-    p.splits = way_of_dhidden(dim, n, up(least(p.piece, vocab), kBK) / kBK * parts).splits;
+    p.splits = p.few ? few_splits(dim, least(p.piece, vocab))
+                     : way_of_dhidden(dim, n, up(least(p.piece, vocab), kBK) / kBK * parts).splits;
   }
   p.pieces = p.piece ? (vocab + p.piece - 1) / p.piece : 0;
   // Room for logits and the head's gradient in parts, one after the other: of a piece and of the last one, or, in the
   // forward pass, of the whole head where it lies.
   auto room = [&](int64_t rows) {
     if (rows == 0 || n == 0 || dim == 0) return (int64_t)0;
-    const int64_t zs = way_of_logits(rows, n, zstages).splits, z = zs > 1 ? zs * p.np * up(rows, kBK) * 4 : 0;
+    const int64_t zs = p.few ? few_parts(rows, dim) : way_of_logits(rows, n, zstages).splits, z = zs > 1 || p.few ? zs * p.np * up(rows, kBK) * 4 : 0;
     const int64_t ws = grad ? way_of_dweight(dim, rows, p.np / kBK * wparts).splits : 1, w = ws > 1 ? ws * rows * p.dq * 4 : 0;
     return z > w ? z : w;
   };
@@ -1213,7 +1328,7 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   const int64_t parts = n <= kFewTokens ? vocab / 64 + 4 : (vocab + 127) / 128;  // 64 or 128 rows of the head each
   p.parts = take(grad ? 0 : parts * p.np * (int64_t)sizeof(float2));
   p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
-  p.weight = take(p.piece * p.dp * p.planes * 2);
+  p.weight = take(p.few ? 0 : p.piece * p.dp * p.planes * 2);
   p.hpower = take(p.half ? p.np * 4 : 0);
   p.wpower = take(p.half ? p.piece * 4 : 0);
   p.hhalf = take(grad && p.half ? p.np * p.dp * 6 : 0);
@@ -1255,23 +1370,18 @@ hipError_t launch_head_forward(const void* hidden, int64_t hidden_ld, int dtype,
       if (dim > 1)
         layout((const uint16_t*)hidden + 1, hidden_ld, dtype, dim - 1, n, to + p.np * p.dp, p.dp, nullptr, nullptr, s);
     }
-    const int64_t all = (vocab + 31) / 32 * 2, groups = (all + kFewWaves - 1) / kFewWaves;
-    const int64_t grid = groups ? (all + 4 * groups - 1) / (4 * groups) : 0;
-    auto go = [&](auto type, auto tiles) {
+    const auto [groups, grid] = few_grid(vocab);
+    auto go = [&, groups = groups, grid = grid](auto type, auto tiles) {
       using T = decltype(type);
       hipLaunchKernelGGL((k_logits_few<T, decltype(tiles)::value>), dim3((unsigned)grid), dim3(kThreads), 0, s,
                          (const T*)weight, weight_ld, (const T*)h0, (const T*)h1, h_ld, (int)n, vocab, (uint32_t)dim,
-                         groups, given, (float2*)(ws + p.parts), (float*)(ws + p.own), p.np);
+                         groups, given, (float2*)(ws + p.parts), (float*)(ws + p.own), p.np, 0u, (int64_t)0);
     };
-    auto by_tokens = [&](auto type) {
-      if (n <= 16) go(type, std::integral_constant<int, 1>{});
-      else if (n <= 32) go(type, std::integral_constant<int, 2>{});
-      else go(type, std::integral_constant<int, 4>{});
-    };
-    if (grid > 0) {
-      if (bf16) by_tokens(uint16_t{});
-      else by_tokens(float{});
-    }
+    if (grid > 0)
+      by_tokens(n, [&](auto tiles) {
+        if (bf16) go(uint16_t{}, tiles);
+        else go(float{}, tiles);
+      });
     join(std::integral_constant<int, 1>{}, std::false_type{}, grid);
     return hipGetLastError();
   }
@@ -1358,7 +1468,8 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
   for (int64_t v0 = 0; v0 < vocab; v0 += p.piece) {
     const int64_t vc = least(p.piece, vocab - v0), vp = up(vc, kBK), ldg = vp * p.gplanes;
     GemmSide w{(const uint16_t*)weight + v0 * weight_ld, weight_ld, 0, vc, dim};
-    if (!w_lies) {
+    const float* in_place = (const float*)weight + v0 * weight_ld;  // few tokens' fp32
+    if (!w_lies && !p.few) {
       uint16_t* to = (uint16_t*)(ws + p.weight);
       const char* from = (const char*)weight + v0 * weight_ld * (dtype == ZS_F32 ? 4 : 2);
       if (half) layout_half(from, weight_ld, dim, vc, w_half, p.dp, w_power, nullptr, nullptr, to, s);
@@ -1373,7 +1484,22 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
       else go(std::integral_constant<int, 3>{});
     };
-    with_cut(zway.cut, [&](auto shape) {
+    if (p.few)
+      by_tokens(n, [&, v0 = v0](auto tiles) {
+        const FewGrid f = few_grid(vc);
+        const int zparts = (int)few_parts(vc, dim);
+        hipLaunchKernelGGL((k_logits_few<float, decltype(tiles)::value, true>), dim3((unsigned)f.grid, (unsigned)zparts), dim3(kThreads), 0, s,
+                           in_place, weight_ld, (const float*)hidden, (const float*)hidden, hidden_ld, (int)n, vc,
+                           (uint32_t)dim, f.groups, Labels{labels, index_type == ZS_I64, vocab}, (float2*)nullptr, z, vp,
+                           (uint32_t)few_columns(vc, dim), p.np * vp);
+        hipLaunchKernelGGL((k_join_g<3, true>), dim3(grid_of(p.np * vp / 4)), dim3(kThreads), 0, s, z, zparts, vp, v0, vc, tok,
+                           p.np, gp, vp);
+        const int64_t waves = (dim + 63) / 64 * p.splits;
+        hipLaunchKernelGGL((k_dhidden_few<decltype(tiles)::value>), dim3((unsigned)((waves + 3) / 4)), dim3(kThreads), 0, s,
+                           in_place, weight_ld, (const float*)z, vp, tok, vc, (uint32_t)dim, p.splits, (int)(v0 > 0), sums,
+                           p.dq, p.np);
+      });
+    else with_cut(zway.cut, [&](auto shape) {
       using S = decltype(shape);
       auto go = [&](auto planes, auto halves) {
         constexpr bool HALF = decltype(halves)::value && !std::is_same_v<S, Narrow>;  // not for few tokens
@@ -1388,12 +1514,12 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
       if (half) go(std::integral_constant<int, 3>{}, std::true_type{});
       else by_planes([&](auto planes) { go(planes, std::false_type{}); });
     });
-    if (zway.splits > 1)
+    if (zway.splits > 1 && !p.few)
       by_planes([&](auto planes) {
         hipLaunchKernelGGL((k_join_g<decltype(planes)::value>), dim3(grid_of(p.np * vp / 4)), dim3(kThreads), 0, s, z,
                            zway.splits, vp, v0, vc, tok, p.np, gp, vp);
       });
-    with_cut(dway.cut, [&](auto shape) {
+    if (!p.few) with_cut(dway.cut, [&](auto shape) {
       using S = decltype(shape);
       hipLaunchKernelGGL((k_split<S, K_IS_ROW, false>), dim3(workgroups<S>(dim, n, p.splits)), dim3(S::THREADS), 0, s, w,
                          g_rows, dim, segs, (int)(vp / kBK), p.splits, (int)(v0 > 0), tok.count, sums, p.dq, p.np, w_power,

@@ -16,6 +16,7 @@ struct HeadPlan {
   int planes;        // bf16 planes of the hidden states and of the head's weight
   int gplanes;       // of the logits' gradient
   bool half;         // fp32 logits from pairs of fp16
+  bool few;          // few tokens' fp32 gradients take the head as it lies
   int64_t np;        // tokens rounded up to 64
   int64_t dp;        // dim rounded up to 64
   int64_t dq;        // dim rounded up to 4: a row of the hidden states' gradient in fp32

@@ -74,6 +74,7 @@ def check_sampled(h, w, t, lse, scale, dh, dw, old, first, tokens, rows):
     (3, 40009, 777, "f32", "f32", False, 0.0),
     (20000, 9001, 96, "f32", "f32", False, 0.2),
     (100, 50021, 1000, "f32", "bf16", True, 0.0),
+    (64, 30001, 1027, "f32", "f32", False, 0.4),
 ])
 def test_large(n, vocab, dim, dtype, grad, first, ignored):
     g = gen(n + vocab)
@@ -224,7 +225,8 @@ def test_against_differences():
 
 
 @pytest.mark.parametrize("n,vocab,dim,dtype", [
-    (600, 3000, 192, "bf16"), (7, 3000, 100, "bf16"), (300, 1000, 100, "f32"), (100, 700, 2048, "bf16"), (2000, 90, 130, "f32")])
+    (600, 3000, 192, "bf16"), (7, 3000, 100, "bf16"), (300, 1000, 100, "f32"), (100, 700, 2048, "bf16"), (2000, 90, 130, "f32"),
+    (50, 3000, 100, "f32")])
 def test_graph_and_streams(n, vocab, dim, dtype):
     """Captured forward and backward passes on a stream of their own, replayed with new inputs, with other calls on
     another stream and workspace at the same time."""
@@ -313,6 +315,7 @@ def test_fp32_rows_of_minus_infinity():
 @pytest.mark.parametrize("n,vocab,dim,dtype,grad", [
     (40, 300, 4100, "bf16", "bf16"), (40, 5000, 4096, "bf16", "f32"), (9, 1, 8192, "bf16", "bf16"), (130, 2049, 3000, "bf16", "f32"),
     (387, 260, 2050, "f32", "bf16"), (70, 4097, 1100, "f32", "f32"), (200, 129, 5000, "f32", "f32"),
+    (5, 300, 4100, "f32", "f32"), (40, 700, 2050, "f32", "bf16"), (64, 129, 1537, "f32", "f32"), (23, 33, 8191, "f32", "bf16"),
     (3000, 97, 130, "bf16", "bf16"), (5001, 65, 64, "bf16", "f32"), (1371, 450, 203, "f32", "f32"), (2000, 40, 301, "f32", "bf16")])
 def test_few_tiles_of_long_sums(n, vocab, dim, dtype, grad):
     """Fewer tiles than CUs: the sums of the logits, or of the head's gradient, are in parts."""
