@@ -509,7 +509,11 @@ constexpr int kFewWaves = 4096;    // 4 workgroups of 4 waves on each CU
 constexpr int kFewAligned = 8;
 
 // KEPT: for fp32 gradients, with the logits of token i and row v in own[i np + v], of `each`
-// columns to a part (blockIdx.y), which lie `apart` elements from each other.
+// columns to a part (blockIdx.y), which lie `apart` elements from each other. An error of
+// a logit is one of its g relative to it, and the fp32 products round 512 times in a sum of
+// 512; so two pieces at a time are taken apart to three bf16 each, whose products round once
+// for 32, the small ones into a sum of their own (64 tokens, 5000 x 1027: the gradients
+// are 0.3e-6 off, those of the plain fp32 form 1.2e-6; 3 tokens, 5203 x 7616: 47 us, 33 with fp32 products).
 template <typename T, int NT, bool KEPT = false>
 __global__ __launch_bounds__(kThreads, 3)
 void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h0, const T* __restrict__ h1, int64_t h_ld,
@@ -545,9 +549,35 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
     const int64_t mine = first + col * step, row = mine < vocab ? mine : first;  // rows behind the last: the first's copies
     const bool shift = sizeof(T) == 2 && (((uint32_t)(uintptr_t)w >> 1) + (uint32_t)(first * w_ld)) & 1;  // uniform
     const T *wr = w + row * w_ld, *h = shift ? h1 : h0;
-    f32x4 acc[NT];
+    f32x4 acc[NT], small[KEPT ? NT : 1];
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int t = 0; t < (KEPT ? NT : 1); ++t) small[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto apart3 = [&](bf16x8 (&to)[3], const Piece<T, VEC>& a, const Piece<T, VEC>& b) {
+      if constexpr (KEPT) {
+        uint32_t p[8][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          three_planes(a.get(e), p[e]);
+          three_planes(b.get(e), p[4 + e]);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          to[k] = __builtin_bit_cast(bf16x8, u32x4{bits_hi(p[0][k], p[1][k]), bits_hi(p[2][k], p[3][k]),
+                                                   bits_hi(p[4][k], p[5][k]), bits_hi(p[6][k], p[7][k])});
+      }
+    };
+    auto multiply3 = [&](int t, const bf16x8 (&a)[3], const bf16x8 (&b)[3]) {
+      if constexpr (KEPT) {
+        small[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[2], b[0], small[t], 0, 0, 0);
+        small[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0], b[2], small[t], 0, 0, 0);
+        small[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1], b[1], small[t], 0, 0, 0);
+        small[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1], b[0], small[t], 0, 0, 0);
+        small[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0], b[1], small[t], 0, 0, 0);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0], b[0], acc[t], 0, 0, 0);
+      }
+    };
     auto multiply = [&](int t, const Piece<T, VEC>& a, const Piece<T, VEC>& b) {
       if constexpr (sizeof(T) == 2) {
         acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b),
@@ -581,10 +611,23 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
 #pragma unroll
       for (int t = 0; t < NT; ++t) fetch(ph[t], h + token_at[t] + q * VEC + k);
       if (k + U * STEP < whole) fetch(pw[which ^ 1], wk + k + U * STEP);
+      if constexpr (KEPT) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int u = 0; u < U; u += 2) {
+          bf16x8 a[3], b[3];
+          apart3(a, pw[which][u], pw[which][u + 1]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) multiply(t, pw[which][u], ph[t][u]);
+          for (int t = 0; t < NT; ++t) {
+            apart3(b, ph[t][u], ph[t][u + 1]);
+            multiply3(t, a, b);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < U; ++u) multiply(t, pw[which][u], ph[t][u]);
+      }
       k += U * STEP;
     };
     if (whole) fetch(pw[0], wk);
@@ -598,14 +641,23 @@ void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         take_cols<T, VEC>(b, h + token_at[t], k + q * VEC, left);
-        multiply(t, a, b);
+        if constexpr (KEPT) {
+          Piece<T, VEC> zero;
+          zero.clear();
+          bf16x8 a3[3], b3[3];
+          apart3(a3, a, zero);
+          apart3(b3, b, zero);
+          multiply3(t, a3, b3);
+        } else {
+          multiply(t, a, b);
+        }
       }
     }
     // lane l has the wave's rows 4 (l / 16) to 4 (l / 16) + 3 for token l % 16 of each tile
     if constexpr (KEPT) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        if (t * 16 + col < n) *(f32x4*)(own + (t * 16 + col) * np + first + 4 * q) = acc[t];
+        if (t * 16 + col < n) *(f32x4*)(own + (t * 16 + col) * np + first + 4 * q) = acc[t] + small[t];
       continue;
     }
 #pragma unroll
@@ -740,7 +792,7 @@ void k_split(GemmSide a, GemmSide b, int64_t m, Segments segs, int steps, int sp
 // registers as they lie. A wave takes 64 columns of one part of the rows, 32 rows at
 // a time: lane l loads 16 bytes of rows 8 (l / 16) to 8 (l / 16) + 7, and with them g of
 // token l % 16 of each tile. 5203 x 7616 and 3, 20 and 64 tokens: 37, 60 and 105 us,
-// and the logits in place 33, 54 and 112; the planes of this head and the products with
+// and the logits in place 47, 66 and 124; the planes of this head and the products with
 // them take 61, 107 and 77, whatever the number of tokens.
 template <int NT>
 __global__ __launch_bounds__(kThreads)

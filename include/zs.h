@@ -764,8 +764,8 @@ zs_status zs_linear_cross_entropy_forward(const void* hidden, int64_t hidden_ld,
  *                      grad_dtype) bytes on a 16-byte boundary; calls and graph
  *                      replays that may run at the same time need one each
  * The logits are made again, a piece of the vocabulary at a time, of fp32 values as
- * they are for up to 64 tokens, as sums of three bf16 for up to 511, with an error of
- * the size of fp32 products' roundings, and of two fp16 as above for more. An
+ * sums of three bf16 for up to 511 tokens, with an error of the size of fp32 products'
+ * roundings, and of two fp16 as above for more. An
  * infinite value makes the gradients that it reaches NaN. g is rounded to bf16 for
  * the gradients that are stored in bf16 from bf16 inputs, and has 24 bits for the
  * others; sums are fp32, in an order that depends on the sizes and on how many tokens
