@@ -517,7 +517,8 @@ constexpr int kFewAligned = 8;
 template <typename T, int NT, bool KEPT = false>
 __global__ __launch_bounds__(kThreads, 3)
 void k_logits_few(const T* __restrict__ w, int64_t w_ld, const T* __restrict__ h0, const T* __restrict__ h1, int64_t h_ld,
-                  int n, int64_t vocab, uint32_t dim, int64_t groups, Labels labels, float2* __restrict__ parts, float* __restrict__ own, int64_t np, uint32_t each, int64_t apart) {
+                  int n, int64_t vocab, uint32_t dim, int64_t groups, Labels labels, float2* __restrict__ parts,
+                  float* __restrict__ own, int64_t np, uint32_t each, int64_t apart) {
   constexpr int VEC = 16 / (int)sizeof(T), U = NT == 1 ? 8 : 4;  // values of a piece, pieces of the head on their way
   constexpr uint32_t STEP = 4 * VEC;                             // values of k that a wave's instruction takes of a row
   __shared__ float2 joined[4][16 * NT];
@@ -1328,7 +1329,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.piece = p.pieces ? up((vocab + p.pieces - 1) / p.pieces, 256) : 0;
   p.splits = 1;
   const int64_t zstages = p.dp / kBK * (p.half ? 3 : p.planes == 3 ? 6 : 1);
-  const int64_t wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;  // products of planes for the head's gradient
+  // products of planes for the head's gradient
+  const int64_t wparts = p.planes == 3 ? (grad_dtype == ZS_F32 ? 6 : 3) : p.gplanes;
   if (grad && p.pieces && n > 0 && dim > 0) {
     // Of pieces of equal size and those whose head's gradient fills rounds of the widest tiles, what takes least.
     const int64_t tm = (dim + 255) / 256, parts = p.planes == 3 ? 6 : 1;
@@ -1358,7 +1360,8 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   // forward pass, of the whole head where it lies.
   auto room = [&](int64_t rows) {
     if (rows == 0 || n == 0 || dim == 0) return (int64_t)0;
-    const int64_t zs = p.few ? few_parts(rows, dim) : way_of_logits(rows, n, zstages).splits, z = zs > 1 || p.few ? zs * p.np * up(rows, kBK) * 4 : 0;
+    const int64_t zs = p.few ? few_parts(rows, dim) : way_of_logits(rows, n, zstages).splits,
+                  z = zs > 1 || p.few ? zs * p.np * up(rows, kBK) * 4 : 0;
     const int64_t ws = grad ? way_of_dweight(dim, rows, p.np / kBK * wparts).splits : 1, w = ws > 1 ? ws * rows * p.dq * 4 : 0;
     return z > w ? z : w;
   };
@@ -1530,7 +1533,8 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
     }
     const GemmSide h{hp, p.dp * p.planes, p.dp, p.np, p.dp};
     const GemmSide g_rows{gp, ldg, vp, p.np, vp};
-    const GemmSide zw = half ? GemmSide{w_half, p.dp * 3, p.dp, vc, 0} : w, zh = half ? GemmSide{h_half, p.dp * 3, p.dp, p.np, 0} : h;
+    const GemmSide zw = half ? GemmSide{w_half, p.dp * 3, p.dp, vc, 0} : w,
+                   zh = half ? GemmSide{h_half, p.dp * 3, p.dp, p.np, 0} : h;
     const Way zway = way_of_logits(vc, n, p.dp / kBK * zsegs.count);
     auto by_planes = [&](auto go) {
       if (p.gplanes == 1) go(std::integral_constant<int, 1>{});
@@ -1540,7 +1544,8 @@ hipError_t launch_head_backward(const void* hidden, int64_t hidden_ld, int dtype
       by_tokens(n, [&, v0 = v0](auto tiles) {
         const FewGrid f = few_grid(vc);
         const int zparts = (int)few_parts(vc, dim);
-        hipLaunchKernelGGL((k_logits_few<float, decltype(tiles)::value, true>), dim3((unsigned)f.grid, (unsigned)zparts), dim3(kThreads), 0, s,
+        hipLaunchKernelGGL((k_logits_few<float, decltype(tiles)::value, true>), dim3((unsigned)f.grid, (unsigned)zparts),
+                           dim3(kThreads), 0, s,
                            in_place, weight_ld, (const float*)hidden, (const float*)hidden, hidden_ld, (int)n, vc,
                            (uint32_t)dim, f.groups, Labels{labels, index_type == ZS_I64, vocab}, (float2*)nullptr, z, vp,
                            (uint32_t)few_columns(vc, dim), p.np * vp);
