@@ -8,7 +8,8 @@
 // or several waves of a workgroup), the weights in registers over all rows of a
 // workgroup. Everything is fp32 and rounded once when it is stored: the norm is of
 // the sum before its rounding. The squares' sum has no cancellation, so unlike a
-// variance it needs no second reading. 16384 rows of 4096 bf16 with a residual, to the
+// variance it needs no second reading; where fp32 cannot hold it, it is made again
+// of the values times a power of two. 16384 rows of 4096 bf16 with a residual, to the
 // sum and 8 bits: 84 us, 473 MB at 5.6 TB/s. One row of 8192: 3.4 us, one round trip and
 // a barrier behind the launch.
 #include "zs_e4m3.hpp"
@@ -50,6 +51,20 @@ __device__ __forceinline__ void load_weights(float (&to)[VEC], const void* w, in
   }
 }
 
+// Whether a row's sum of squares left fp32's range: magnitudes of about 2^64 / sqrt(dim) and
+// above make it infinite; below 2^-78 squares may have vanished, and what they add up to matters
+// beside an eps below 2^-54. Such a row is summed again times a power of two: 2^-80 leaves
+// the largest sum of 2^24 squares below 2^120 and the smallest above 2^-33, 2^90 those
+// below 2^-78 below 2^103, and the square of the smallest subnormal 2^-118.
+__device__ __forceinline__ bool out_of_range(float s, float eps) {
+  return !(s < INFINITY) || (s < 0x1p-78f && eps < 0x1p-54f);
+}
+__device__ __forceinline__ float factor_of(float s) { return s < 1.0f ? 0x1p90f : 0x1p-80f; }
+// 1 / sqrt(mean + eps) for the sum s of the squares of the values times `factor`
+__device__ __forceinline__ float rstd_of(float s, float inv_dim, float eps, float factor) {
+  return factor / sqrtf(s * inv_dim + eps * factor * factor);
+}
+
 struct RmsForward {
   const void *x, *residual, *weight;
   void *sum, *y;
@@ -81,7 +96,7 @@ void k_rms_fwd(RmsForward a) {
   constexpr int NW = LPR / 64;   // waves per row (0 below a wave)
   constexpr int G = LPR < 64 ? LPR : 64;
   constexpr int BLOCK = kScaleBlock / VEC < LPR ? kScaleBlock / VEC : LPR;  // lanes of a block of one scale
-  __shared__ float parts[2][BS / 64];
+  __shared__ float parts[2][BS / 64], again[BS / 64];
   const int l = threadIdx.x % LPR;
   const uint32_t dim = a.dim;
   const int64_t step = (int64_t)gridDim.x * RPB;
@@ -126,16 +141,44 @@ void k_rms_fwd(RmsForward a) {
         s = fmaf(h[j][e], h[j][e], s);
       }
     s = lane_sum<G>(s);
+    bool far = false;  // the same in all waves that meet at a barrier
     if constexpr (NW > 1) {
-      const int w0 = threadIdx.x / LPR * NW;  // the row's first wave
       if ((threadIdx.x & 63) == 0) parts[turn][threadIdx.x / 64] = s;
       __syncthreads();  // the other turn's entries are read by nobody any more
+#pragma unroll
+      for (int k = 0; k < RPB; ++k) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) t += parts[turn][k * NW + i];
+        far = far || out_of_range(t, a.eps);
+        if (RPB == 1 || k == (int)threadIdx.x / LPR) s = t;
+      }
+    } else {
+      far = out_of_range(s, a.eps);
+    }
+    float factor = 1.0f;
+    if (__any(far)) {  // rows of the workgroup that are in range get the same sum again
+      if (out_of_range(s, a.eps)) factor = factor_of(s);
       s = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) s += parts[turn][w0 + i];
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float x = h[j][e] * factor;
+          s = fmaf(x, x, s);
+        }
+      s = lane_sum<G>(s);
+      if constexpr (NW > 1) {
+        const int w0 = threadIdx.x / LPR * NW;  // the row's first wave
+        if ((threadIdx.x & 63) == 0) again[threadIdx.x / 64] = s;
+        __syncthreads();  // the last such turn's entries were read before this turn's first barrier
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) s += again[w0 + i];
+      }
     }
     if (!live) continue;
-    const float rstd = 1.0f / sqrtf(s * inv_dim + a.eps);
+    const float rstd = rstd_of(s, inv_dim, a.eps, factor);
     if (l == 0 && a.rstd) a.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j) store_row<T, R, VEC, BLOCK, NT>(a, row, h[j], w[j], rstd, col_of<LPR, VEC>(j, l));
@@ -145,7 +188,7 @@ void k_rms_fwd(RmsForward a) {
 constexpr int kLongBS = 1024;
 
 // Rows longer than the registers of 1024 lanes hold: one workgroup reads the row
-// twice (squares, outputs). A sum in place is written by the lanes that read
+// twice (squares, outputs; squares out of range once more). A sum in place is written by the lanes that read
 // these elements, in the second reading.
 template <typename T, typename R, int VEC>
 __global__ __launch_bounds__(kLongBS)
@@ -169,22 +212,33 @@ void k_rms_fwd_long(RmsForward a) {
         for (int e = 0; e < VEC; ++e) h[e] += pr.get(e);
       }
     };
-    float s = 0.0f;
-    for (uint32_t t = 0; t < turns; ++t) {
-      float h[VEC], p = 0.0f;
-      take((t * kLongBS + threadIdx.x) * VEC, h);
+    auto squares = [&](float factor) {  // of the row, in all lanes
+      float s = 0.0f;
+      for (uint32_t t = 0; t < turns; ++t) {
+        float h[VEC], p = 0.0f;
+        take((t * kLongBS + threadIdx.x) * VEC, h);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) p = fmaf(h[e], h[e], p);
-      s += p;
+        for (int e = 0; e < VEC; ++e) {
+          const float x = h[e] * factor;
+          p = fmaf(x, x, p);
+        }
+        s += p;
+      }
+      s = lane_sum<64>(s);
+      if ((threadIdx.x & 63) == 0) lds[threadIdx.x / 64] = s;
+      __syncthreads();
+      s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kLongBS / 64; ++i) s += lds[i];
+      __syncthreads();
+      return s;
+    };
+    float s = squares(1.0f), factor = 1.0f;
+    if (out_of_range(s, a.eps)) {  // the same in all lanes
+      factor = factor_of(s);
+      s = squares(factor);
     }
-    s = lane_sum<64>(s);
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x / 64] = s;
-    __syncthreads();
-    s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kLongBS / 64; ++i) s += lds[i];
-    __syncthreads();
-    const float rstd = 1.0f / sqrtf(s * inv_dim + a.eps);
+    const float rstd = rstd_of(s, inv_dim, a.eps, factor);
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     for (uint32_t t = 0; t < turns; ++t) {
       const uint32_t c = (t * kLongBS + threadIdx.x) * VEC;

@@ -655,8 +655,10 @@ zs_status zs_activation_unpack(const uint8_t* codes, int64_t codes_ld, const flo
  *                      zs_activation_pack gives it for y before its rounding
  *   rstd[rows]         optional DEVICE fp32 (the backward pass needs it)
  * Apart from sum in place no output may share bytes with another argument.
- * Squares are added in fp32: magnitudes above 2^63 overflow to rstd = 0. Errors:
- * ZS_ERR_NULL (sum without residual, neither y nor codes, codes or scales alone
+ * Any finite h of any size gives the norm of that formula: where the sum of squares
+ * leaves fp32's range, it is made again of h times a power of two (rstd is subnormal for
+ * root mean squares above 2^126, and infinite for those below 2^-128 with eps 0, or of
+ * zeros). Errors: ZS_ERR_NULL (sum without residual, neither y nor codes, codes or scales alone
  * among them), ZS_ERR_SIZE (dim < 1 with rows > 0 among them), ZS_ERR_DTYPE,
  * ZS_ERR_HPARAM, ZS_ERR_ALIGN, ZS_ERR_OVERLAP, ZS_ERR_HIP.
  */
