@@ -1365,7 +1365,10 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
     const int64_t ws = grad ? way_of_dweight(dim, rows, p.np / kBK * wparts).splits : 1, w = ws > 1 ? ws * rows * p.dq * 4 : 0;
     return z > w ? z : w;
   };
-  const int64_t of_piece = room(least(p.piece, vocab)), of_other = room(grad && p.piece ? vocab % p.piece : vocab);
+  // The loss of few tokens reads the head as it lies: bf16 on 16-byte boundaries by tiles, others by k_logits_few.
+  const bool streams = !grad && n <= kFewTokens, lies = streams && dtype == ZS_BF16;
+  const int64_t of_piece = streams ? 0 : room(least(p.piece, vocab)),
+                of_other = streams && !lies ? 0 : room(grad && p.piece ? vocab % p.piece : vocab);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t from = at;
@@ -1382,10 +1385,10 @@ HeadPlan head_plan(int64_t n, int64_t vocab, int64_t dim, int dtype, int grad_dt
   p.own = take(grad ? 0 : p.np * 4);
   const int64_t parts = n <= kFewTokens ? vocab / 64 + 4 : (vocab + 127) / 128;  // 64 or 128 rows of the head each
   p.parts = take(grad ? 0 : parts * p.np * (int64_t)sizeof(float2));
-  p.hidden = take(p.np * p.dp * p.planes * 2 * (!grad && n <= kFewTokens ? 2 : 1));
-  p.weight = take(p.few ? 0 : p.piece * p.dp * p.planes * 2);
-  p.hpower = take(p.half ? p.np * 4 : 0);
-  p.wpower = take(p.half ? p.piece * 4 : 0);
+  p.hidden = take(streams && !lies ? 0 : p.np * p.dp * p.planes * 2 * (streams ? 2 : 1));
+  p.weight = take(p.few || streams || n == 0 ? 0 : p.piece * p.dp * p.planes * 2);
+  p.hpower = take(p.half && !streams ? p.np * 4 : 0);
+  p.wpower = take(p.half && !streams ? p.piece * 4 : 0);
   p.hhalf = take(grad && p.half ? p.np * p.dp * 6 : 0);
   p.whalf = take(grad && p.half ? p.piece * p.dp * 6 : 0);
   p.z = take(of_piece > of_other ? of_piece : of_other);
