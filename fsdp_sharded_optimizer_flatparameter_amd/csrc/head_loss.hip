@@ -299,6 +299,14 @@ __device__ __forceinline__ float join4(float x, bool take_max) {  // over the la
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// Between a wave's accesses to LDS that other lanes of it have written or still read: LDS
+// keeps a wave's order, so this tells the compiler alone and costs no instruction.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The tiles of one workgroup, one after another: make(at) aims the loop at a tile,
 // finish(at) uses its products and says whether all lanes have sent off at least
 // kStored stores.
@@ -442,12 +450,14 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
               const int place = (2 * i + (lane >> 5)) ^ (t & (CHUNKS - 1));
               reinterpret_cast<uint2*>(mine_of + t * CHUNKS + place)[lane >> 4 & 1] = v;
             }
+            wave_lds();
 #pragma unroll
             for (int x = 0; x < 16 * CHUNKS / 64; ++x) {
               const int at16 = x * 64 + lane, t2 = at16 / CHUNKS, c = at16 % CHUNKS;
               const u32x4 v = mine_of[t2 * CHUNKS + (c ^ (t2 & (CHUNKS - 1)))];
               *(u32x4*)(g + (token - t + t2) * gp * PLANES + k * gp + first + c * 8) = v;
             }
+            wave_lds();
           }
           continue;
         }
@@ -992,6 +1002,7 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
             mine[t * FLOATS + ((4 * i + (lane >> 4)) ^ (t & (FLOATS - 1)))] =
                 u32x4{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w)};
           }
+          wave_lds();
 #pragma unroll
           for (int x = 0; x < IN * 16 * 16 / EACH / 64; ++x) {
             const int at16 = x * 64 + lane, row = at16 / CHUNKS, c = at16 % CHUNKS;
@@ -1021,6 +1032,7 @@ void k_dweight(GemmSide h, GemmSide g, Segments segs, const int32_t* __restrict_
             }
             st16(y, to + row * dw_ld + c * EACH);
           }
+          wave_lds();
         }
       return S::TN * (S::TM / IN) * (IN * 16 * 16 / EACH / 64) >= 16;
     }
