@@ -59,10 +59,12 @@ struct GemmShape {
 // to 16 l behind `lds`. Written out, as behind the builtin the compiler waits for
 // all loads before the next transposing read (ds_read_b64_tr_b16), which it
 // takes to read what they write; the waits are TileLoop's own. M0 holds the LDS
-// address, and needs a wait state before it is used.
+// address, and needs a wait state before it is used; it is the compiler's, which does
+// not take it as clobbered, so it gets its value back.
 __device__ __forceinline__ void load_to_lds(u32x4 buffer, uint32_t lds, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
+  uint32_t kept;
+  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+               : "=&s"(kept)
                : "s"(lds), "v"(off), "s"(buffer)
                : "memory");
 }
