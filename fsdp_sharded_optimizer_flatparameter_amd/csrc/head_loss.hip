@@ -335,10 +335,16 @@ __device__ __forceinline__ void tiles_of(char* lds, uint32_t total, uint32_t tm,
   }
 }
 
+// Partial maxima and sums that a tile leaves for each token: one, joined in LDS, where the
+// workgroups that share a CU's 160 KB have room for that beside their stages (8 bytes for each wave
+// and token of a tile), else one for each row of waves.
 template <class S>
-constexpr int parts_of_tile() {  // partial maxima and sums that a tile leaves for each token
-  return S::LDS % (80 * 1024) == 0 ? S::WM : 1;
+constexpr int parts_of_tile() {
+  constexpr int sharing = 2 * S::LDS <= 160 * 1024 ? 2 : 1, joined = S::WM * S::BN * 8;
+  return sharing * (S::LDS + joined) <= 160 * 1024 ? 1 : S::WM;
 }
+static_assert(parts_of_tile<Wide>() == 1 && parts_of_tile<Square>() == 1 && parts_of_tile<Narrow>() == 4,
+              "the room for the tiles' maxima in head_plan is for 128 rows of the head, or 64 of a narrow tile's");
 
 // Rows of the tile are rows of the head, columns tokens: a lane holds 4 TM
 // logits of each of its TN tokens. PLANES: 0 for the loss, else those of g. HALF:
