@@ -26,7 +26,7 @@
 // whose products below 2^-21 of the largest are left out. The loss, and the logits of
 // many tokens for the gradients, take fp32 rows as sums of two fp16.
 //
-// Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.6 ms (its logits 6.5, 1330
+// Measured: 8192 tokens, 128256 x 4096 bf16: the loss 6.7 ms (its logits 6.5, 1330
 // TFLOP/s), the gradients 21 ms (1230 TFLOP/s); one token: 181 us, 5.8 TB/s; 8192
 // tokens, 50257 x 768 into an fp32 accumulator: 3.4 ms, of which the logits 1.06 (600
 // TFLOP/s: a tile has 12 stages, then 2.5 GB of g), dh 0.81, dw 1.6 (1210 TFLOP/s).
@@ -265,7 +265,7 @@ void k_layout_half(const float* __restrict__ src, int64_t ld, uint32_t dim, int6
 // ---------------------------------------------------------------- products
 
 // Which tile a workgroup takes. Workgroups go round robin over the 8 XCDs, each
-// with an L2 of its own: an XCD takes tiles that lie together, four rows of
+// with an L2 of its own: an XCD takes tiles that lie together, eight rows of
 // tiles deep, so that its workgroups share both operands' panels.
 struct Tile {
   int64_t m, n;
@@ -361,9 +361,8 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
   constexpr int APART = parts_of_tile<S>();
   __shared__ float2 joined[PLANES == 0 && APART == 1 ? S::WM * S::BN : 1];
   // The lanes of a store hold 32 bytes each of 16 tokens' rows of g. By way of LDS, where
-  // there is room, they are whole lines: 335 instead of 439 us for 8192 tokens, 21760
-  // rows of 768 in two planes (287 without stores). The chunk of 16 bytes c of token t lies at
-  // place c ^ t.
+  // there is room, they are whole lines: 453 instead of 581 us for 8192 tokens, 21760
+  // rows of 768 in three planes. The chunk of 16 bytes c of token t lies at place c ^ t.
   constexpr bool LINES = PLANES > 0 && APART == 1;
   constexpr int CHUNKS = ROWS / 8;
   __shared__ __align__(16) u32x4 lines[LINES ? S::WM * S::WN : 1][LINES ? 16 * CHUNKS : 1];
@@ -519,9 +518,10 @@ void k_logits(GemmSide w, GemmSide h, Segments segs, int steps, int64_t v0, Toke
 // its own, and takes the tokens from a copy that starts one element later.
 constexpr int kFewTokens = 64;
 constexpr int kFewWaves = 4096;    // 4 workgroups of 4 waves on each CU
-// Rows that the narrow tiles take as they lie are read as fast by them (1 token, 128256 rows of 4096 bf16: 181 us,
-// 179 here; 16 tokens of 1856: 111, 125 here); what they would have to lay out first is not (4 tokens, 41246 rows of
-// 1855: 100 in all, 35 here; 64: 92, 101 here; fp32, 20 tokens of 1856: over 260, 104 here).
+// Rows that the narrow tiles take as they lie are read as fast by them, or faster from some tokens on (16 tokens of
+// bf16, 128256 rows of 4096: 181 us, 242 here; 41246 rows of 1856: 44, 45 here; 64 tokens: 46, 104 here); what they would
+// have to lay out first is not (41246 rows of 1855, 4 tokens: 100 in all, 41 here; 64: 92, 111 here; fp32, 20 tokens,
+// 41246 rows of 1856: over 260, 105 here).
 constexpr int kFewAligned = 8;
 
 // KEPT: for fp32 gradients, with the logits of token i and row v in own[i np + v], of `each`

@@ -733,7 +733,8 @@ size_t zs_linear_cross_entropy_workspace_bytes(int64_t n, int64_t vocab, int64_t
  * are for up to 64 tokens, as sums of two fp16 scaled by a power of two of their row
  * for more: a product h w is off by up to 2^-20 |h w|, or 2^-39 of one's magnitude by
  * the largest of the other's row. Infinite or NaN logits make their token's loss
- * infinite or NaN, and no other's; one of minus infinity counts as 0. n and vocab are
+ * infinite or NaN, and no other's; one of minus infinity counts as 0 (in fp32 over more than 64
+ * tokens an infinite value times one below 2^-39 of its row's largest is NaN, as times 0). n and vocab are
  * below 2^31, dim at most 2^20, with at most 2^31 - 1 tiles of 128 rows of the head
  * by 128 tokens. Weights that lie on 16-byte boundaries with a multiple of 64 columns
  * are read as they lie; others are laid out in the workspace first. No output or

@@ -4,8 +4,12 @@ Tolerances, u = 2^-24, half = half a step of a type (fp32 2^-24, bf16 2^-8). The
 matrix units add 32 exact products at a time to an fp32 sum, not necessarily
 rounded to nearest, so a sum of K products in S segments is off by at most
   sum(K) = 2 (32 + S K / 32) u of the sum of their magnitudes.
-fp32 operands are sums of three bf16 (S = 6); the products left out are below
-2^-21 of the whole. With A_iv = sum_k |h_ik w_vk| and R_i = max_v |z_iv - top_i|:
+fp32 operands are sums of three bf16 (S = 6), whose products left out are below
+2^-21 of the whole. The loss of more than 64 tokens, and the gradients' logits from 512
+tokens on, take sums of two fp16 (S = 3, products off by 3 2^-22 = 12 u), which the same
+bound holds: 12 u + 6 dim / 32 u is below 8 u + 12 dim / 32 u for widths from 22 on, and
+narrower sums do not make the 32 additions that it counts.
+With A_iv = sum_k |h_ik w_vk| and R_i = max_v |z_iv - top_i|:
   z:    E_iv = (sum(dim) + 2^-21 where fp32) A_iv
   exp:  x log2(e) is rounded (|x| 2^-23 with the constant's error) and the
         function good to 2^-22: relative e(x) = (|x| + 4) 2^-23
@@ -13,7 +17,8 @@ fp32 operands are sums of three bf16 (S = 6); the products left out are below
         lane adds up to 32 terms and tiles are joined in 16 groups; loss twice the
         first term, for the label's own logit
   g:    with p = exp(z - lse): |c| (p (1.01 E + e(z - lse)) + 3 u (p + 1)) + r |g|, r the rounding
-        to one, two or three bf16: 2^-8, 2^-16, 2^-23
+        allowed: 2^-8 where g is one bf16, 2^-16 for dw in fp32 of bf16 inputs and 2^-23 for
+        fp32 inputs, where it is three (test_gpu_head_loss_precision holds both to 2^-23)
   dh:   sum_v dg |w| + (sum(vocab) + 64 u + 2^-21 where fp32) sum_v |g w| + half |dh|
   dw:   sum_i dg |h| + (sum(n) + 64 u + 2^-21 where fp32, 2^-13 where of fp32 inputs for bf16)
         sum_i |g h| + 2 u |old| + half |dw|
